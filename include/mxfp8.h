@@ -307,6 +307,131 @@ mx_status mx_grouped_gemm_wgrad_elem(mx_elem_type a_elem, mx_elem_type b_elem, i
                                      const void* a, const void* sa, const void* b, const void* sb,
                                      void* c, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Around the MoE experts' products: routing, token movement, gradient norm.
+ * ------------------------------------------------------------------------- */
+
+/* Element type of router logits and of gradients. */
+typedef enum mx_dtype {
+    MX_DTYPE_BF16 = 0,
+    MX_DTYPE_F32 = 1
+} mx_dtype;
+
+/* Router scores of a token's logits x[E]. */
+typedef enum mx_score {
+    MX_SCORE_SOFTMAX = 0, /* s = exp(x) / sum over all experts */
+    MX_SCORE_SIGMOID = 1  /* s = 1 / (1 + exp(-x)) */
+} mx_score;
+
+/* Value of a group of experts when groups are chosen first. */
+typedef enum mx_group_value {
+    MX_GROUP_TOP2 = 0, /* sum of its best two choice values (its best one, if only one is unmasked) */
+    MX_GROUP_MAX = 1   /* its best choice value */
+} mx_group_value;
+
+/* Routing of T tokens to top_k of E experts, and the expert order that
+ * mx_grouped_gemm's rows are laid out by.
+ *   logits: [T, E] of dtype; bias: FP32 [E] or NULL.
+ * Choice values are v = s + bias (the bias balances the choice and enters
+ * nothing else); an expert whose logit (or bias) is -inf is masked.  With
+ * n_groups > 1 the experts form n_groups groups of E / n_groups consecutive
+ * ones, and only those of the top_groups best groups stay.  The top_k
+ * unmasked experts with the largest v are chosen, in descending order, equal
+ * values by the lowest index (groups alike).  The choice follows the scores,
+ * not their 32-bit roundings: logits are compared as they are where that is
+ * the same order, otherwise v in 64 bits, where values that agree in their
+ * first 43 bits count as equal.  A NaN value ranks below every number.
+ *   weights [T, top_k] FP32: w_j = scale * s[e_j], or with renormalize
+ *            scale * s[e_j] / sum_i s[e_i]; 0 where no expert is left.  Under
+ *            softmax a NaN logit makes its token's weights NaN; a +inf logit
+ *            takes the whole score, several share it.
+ *   experts [T, top_k] INT32: e_j, -1 where fewer than top_k are unmasked.
+ *   offsets [E + 1] INT64: rows offsets[e] .. offsets[e + 1] - 1 of the
+ *            expert order belong to expert e; offsets[E] = the choices made.
+ *   slots [T, top_k] INT32: the row of each choice, tokens in order within
+ *            an expert; -1 where experts is -1.
+ * Requires 1 <= E <= 512, 1 <= top_k <= min(E, 16), 1 <= top_groups <=
+ * n_groups <= 32, E % n_groups == 0, T * top_k < 2^31.  T == 0 writes
+ * offsets only.  workspace: DEVICE scratch of mx_route_workspace_size bytes. */
+mx_status mx_route(mx_score score, mx_dtype dtype, const void* logits, const float* bias,
+                   int64_t T, int64_t E, int64_t top_k, int64_t n_groups, int64_t top_groups,
+                   mx_group_value group_value, int renormalize, float scale, float* weights,
+                   int32_t* experts, int64_t* offsets, int32_t* slots, void* workspace,
+                   size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of device workspace mx_route needs for T tokens and E experts.  Pure
+ * host function, no HIP call; 0 for a size mx_route rejects. */
+size_t mx_route_workspace_size(int64_t T, int64_t E);
+
+/* Gradient of mx_route's weights with respect to the logits, for the choice
+ * that was made (experts [T, top_k], -1 skipped): dlogits [T, E] of dtype
+ * from dweights [T, top_k] FP32.  The bias has no gradient.  An experts entry
+ * outside [0, E) is skipped.  Requires T * 16 < 2^32 besides mx_route's
+ * limits.  T == 0 is a no-op. */
+mx_status mx_route_backward(mx_score score, mx_dtype dtype, const float* dweights,
+                            const void* logits, const int32_t* experts, int64_t T, int64_t E,
+                            int64_t top_k, int renormalize, float scale, void* dlogits,
+                            hipStream_t stream);
+
+/* Token rows into the expert order: y[slots[t][j]] = x[t] for every choice,
+ * rows offsets[E] .. T * top_k - 1 zero.  x: BF16 [T, H], y: BF16
+ * [T * top_k, H]; offsets, slots as mx_route writes them.  They are read on
+ * the device and trusted: a slot outside [0, T * top_k) is skipped and
+ * offsets[E] is clamped, so bad ones give wrong rows but never a bad access.
+ * Its gradient is mx_combine of dy with weights = NULL.  Requires 1 <= E <=
+ * 512, 1 <= top_k <= 16, T * top_k < 2^31, T * ceil(H / 512) < 2^26.
+ * T == 0 or H == 0 is a no-op. */
+mx_status mx_dispatch(const void* x, int64_t T, int64_t H, int64_t top_k, int64_t E,
+                      const int64_t* offsets, const int32_t* slots, void* y, hipStream_t stream);
+
+/* mx_dispatch with the rows quantised in 1x32 blocks on the way: q [T *
+ * top_k, H] payload of elem, s [T * top_k, H / 32], the bytes of
+ * mx_quant_elem(MX_QUANT_ROW_1x32, elem) of the dispatched rows (0x00 in
+ * rows past offsets[E]), i.e. mx_grouped_gemm's a and sa.  Each token is
+ * quantised once and no BF16 copy is made.  Requires H % 32 == 0 too. */
+mx_status mx_dispatch_quant(mx_elem_type elem, const void* x, int64_t T, int64_t H, int64_t top_k,
+                            int64_t E, const int64_t* offsets, const int32_t* slots, void* q,
+                            void* s, hipStream_t stream);
+
+/* Expert rows back to the tokens: out[t] = residual[t] + sum_j w[t][j]
+ * y[slots[t][j]], added in FP32 in the order of the choices and rounded once.
+ * y: BF16 [T * top_k, H]; weights: FP32 [T, top_k] or NULL for ones;
+ * residual: BF16 [T, H] or NULL; out: BF16 [T, H], may be residual itself.
+ * A slot outside [0, T * top_k) adds nothing.  Limits as mx_dispatch. */
+mx_status mx_combine(const void* y, int64_t T, int64_t H, int64_t top_k, const int32_t* slots,
+                     const float* weights, const void* residual, void* out, hipStream_t stream);
+
+/* Gradient of mx_combine: dy[slots[t][j]] = w[t][j] dout[t] (BF16 [T * top_k,
+ * H], rows offsets[E] .. zero) and dweights[t][j] = <dout[t], y[slots[t][j]]>
+ * (FP32 [T, top_k], 0 where there is no slot; summed in FP32 in a fixed
+ * order).  The residual's gradient is dout.  Limits as mx_dispatch, and
+ * T < 2^24.  T == 0 is a no-op; H == 0 writes dweights only. */
+mx_status mx_combine_backward(const void* dout, const void* y, int64_t T, int64_t H, int64_t top_k,
+                              int64_t E, const int64_t* offsets, const int32_t* slots,
+                              const float* weights, void* dy, float* dweights, hipStream_t stream);
+
+/* Global norm of n tensors: *norm (DEVICE, FP32) = sqrt(sum of all squares),
+ * added in 64 bits in a fixed order and rounded once.  tensors, numels and
+ * dtypes are HOST arrays of n device pointers, element counts and element
+ * types; they are read during the call only.  workspace: DEVICE scratch of
+ * mx_grad_norm_workspace_size(n) bytes.  Requires fewer than 2^45 bytes in
+ * all.  n == 0 gives norm 0. */
+mx_status mx_grad_norm(int64_t n, const void* const* tensors, const int64_t* numels,
+                       const mx_dtype* dtypes, float* norm, void* workspace,
+                       size_t workspace_bytes, hipStream_t stream);
+
+/* mx_grad_norm, then every tensor scaled in place by min(1, max_norm / (norm
+ * + 1e-6)), formed in 64 bits and rounded to its type.  *norm is the norm
+ * before (+inf past FP32's range; the scaling uses the 64-bit one).  Infinite
+ * elements scale the rest by 0 and become NaN; a NaN makes all NaN.  Tensors must not overlap (MX_ERR_INVALID_ARG). */
+mx_status mx_grad_clip(int64_t n, void* const* tensors, const int64_t* numels,
+                       const mx_dtype* dtypes, float max_norm, float* norm, void* workspace,
+                       size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of device workspace mx_grad_norm and mx_grad_clip need for n
+ * tensors.  Pure host function, no HIP call; 0 for n <= 0. */
+size_t mx_grad_norm_workspace_size(int64_t n);
+
 #ifdef __cplusplus
 }
 #endif

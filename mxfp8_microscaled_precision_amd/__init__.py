@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import Any, NamedTuple
 
 __all__ = [
     "MXError", "lib", "mx_device_check", "mx_arch_supported", "mx_status_string",
@@ -26,6 +27,11 @@ __all__ = [
     "grouped_gemm", "quant_batched", "quant_grouped_col", "grouped_gemm_wgrad",
     "grouped_col_capacity", "process_quant_result", "QUANT_MODES", "GEMM_LAYOUTS",
     "BSCALE_KINDS", "ELEM_TYPES",
+    "mx_route", "mx_route_workspace_size", "mx_route_backward", "mx_dispatch", "mx_dispatch_quant",
+    "mx_combine", "mx_combine_backward", "mx_grad_norm", "mx_grad_clip",
+    "mx_grad_norm_workspace_size", "Routing", "route", "route_backward", "dispatch",
+    "dispatch_quant", "combine", "combine_backward", "grad_norm", "grad_clip", "SCORES",
+    "GROUP_VALUES",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmxfp8.so")
@@ -35,6 +41,8 @@ QUANT_MODES = {"row": 0, "col": 1, "dual": 2, "32x32": 3}
 GEMM_LAYOUTS = {"fprop": 0, "dgrad": 1, "wgrad": 2}
 BSCALE_KINDS = {"1x32": 0, "32x32": 1}
 ELEM_TYPES = {"e4m3": 0, "e5m2": 1}
+SCORES = {"softmax": 0, "sigmoid": 1}
+GROUP_VALUES = {"top2": 0, "max": 1}
 
 
 class MXError(RuntimeError):
@@ -96,6 +104,28 @@ def lib() -> ctypes.CDLL:
         L.mx_grouped_gemm_wgrad_elem.restype = c_int
         L.mx_grouped_gemm_wgrad_elem.argtypes = [c_int, c_int, i64, vp, i64, i64, i64, vp, vp, vp, vp,
                                                  vp, vp]
+        f32 = ctypes.c_float
+        L.mx_route.restype = c_int
+        L.mx_route.argtypes = [c_int, c_int, vp, vp, i64, i64, i64, i64, i64, c_int, c_int, f32, vp,
+                               vp, vp, vp, vp, sz, vp]
+        L.mx_route_workspace_size.restype = sz
+        L.mx_route_workspace_size.argtypes = [i64, i64]
+        L.mx_route_backward.restype = c_int
+        L.mx_route_backward.argtypes = [c_int, c_int, vp, vp, vp, i64, i64, i64, c_int, f32, vp, vp]
+        L.mx_dispatch.restype = c_int
+        L.mx_dispatch.argtypes = [vp, i64, i64, i64, i64, vp, vp, vp, vp]
+        L.mx_dispatch_quant.restype = c_int
+        L.mx_dispatch_quant.argtypes = [c_int, vp, i64, i64, i64, i64, vp, vp, vp, vp, vp]
+        L.mx_combine.restype = c_int
+        L.mx_combine.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp, vp]
+        L.mx_combine_backward.restype = c_int
+        L.mx_combine_backward.argtypes = [vp, vp, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp]
+        L.mx_grad_norm.restype = c_int
+        L.mx_grad_norm.argtypes = [i64, vp, vp, vp, vp, vp, sz, vp]
+        L.mx_grad_clip.restype = c_int
+        L.mx_grad_clip.argtypes = [i64, vp, vp, vp, f32, vp, vp, sz, vp]
+        L.mx_grad_norm_workspace_size.restype = sz
+        L.mx_grad_norm_workspace_size.argtypes = [i64]
         _lib = L
     return _lib
 
@@ -182,6 +212,55 @@ def mx_quant_grouped_col_elem(elem, x, T, C, G, offsets, q_t, s_t, stream) -> in
 def mx_grouped_gemm_wgrad_elem(a_elem, b_elem, G, offsets, T, M, N, a, sa, b, sb, c, stream) -> int:
     return lib().mx_grouped_gemm_wgrad_elem(a_elem, b_elem, G, offsets, T, M, N, a, sa, b, sb, c,
                                             stream)
+
+
+def mx_route(score, dtype, logits, bias, T, E, top_k, n_groups, top_groups, group_value, renormalize,
+             scale, weights, experts, offsets, slots, workspace, workspace_bytes, stream) -> int:
+    return lib().mx_route(score, dtype, logits, bias, T, E, top_k, n_groups, top_groups, group_value,
+                          renormalize, scale, weights, experts, offsets, slots, workspace,
+                          workspace_bytes, stream)
+
+
+def mx_route_workspace_size(T, E) -> int:
+    return lib().mx_route_workspace_size(T, E)
+
+
+def mx_route_backward(score, dtype, dweights, logits, experts, T, E, top_k, renormalize, scale,
+                      dlogits, stream) -> int:
+    return lib().mx_route_backward(score, dtype, dweights, logits, experts, T, E, top_k, renormalize,
+                                   scale, dlogits, stream)
+
+
+def mx_dispatch(x, T, H, top_k, E, offsets, slots, y, stream) -> int:
+    return lib().mx_dispatch(x, T, H, top_k, E, offsets, slots, y, stream)
+
+
+def mx_dispatch_quant(elem, x, T, H, top_k, E, offsets, slots, q, s, stream) -> int:
+    return lib().mx_dispatch_quant(elem, x, T, H, top_k, E, offsets, slots, q, s, stream)
+
+
+def mx_combine(y, T, H, top_k, slots, weights, residual, out, stream) -> int:
+    return lib().mx_combine(y, T, H, top_k, slots, weights, residual, out, stream)
+
+
+def mx_combine_backward(dout, y, T, H, top_k, E, offsets, slots, weights, dy, dweights,
+                        stream) -> int:
+    return lib().mx_combine_backward(dout, y, T, H, top_k, E, offsets, slots, weights, dy, dweights,
+                                     stream)
+
+
+def mx_grad_norm(n, tensors, numels, dtypes, norm, workspace, workspace_bytes, stream) -> int:
+    return lib().mx_grad_norm(n, tensors, numels, dtypes, norm, workspace, workspace_bytes, stream)
+
+
+def mx_grad_clip(n, tensors, numels, dtypes, max_norm, norm, workspace, workspace_bytes,
+                 stream) -> int:
+    return lib().mx_grad_clip(n, tensors, numels, dtypes, max_norm, norm, workspace, workspace_bytes,
+                              stream)
+
+
+def mx_grad_norm_workspace_size(n) -> int:
+    return lib().mx_grad_norm_workspace_size(n)
 
 
 def _check(status: int):
@@ -491,3 +570,235 @@ def process_quant_result(weight, recipe: str = "mxfp8", dst_type="e4m3"):
         return q, s, qt, st
     q, s = quant(weight, "32x32", elem)
     return q, s, q, s
+
+
+# ---------------------------------------------------------------------------
+# Around the experts' products: routing, token movement, gradient norm
+# ---------------------------------------------------------------------------
+
+class Routing(NamedTuple):
+    """Which experts T tokens go to, and the expert order of their rows.
+
+    weights [T, k] FP32, experts [T, k] INT32 (-1: no expert left), offsets
+    [E + 1] INT64 (``grouped_gemm``'s), slots [T, k] INT32: the row of each
+    choice in the expert order, -1 where there is none.
+    """
+    weights: Any
+    experts: Any
+    offsets: Any
+    slots: Any
+
+
+def _dtype_code(t, name):
+    torch = _torch()
+    if t.dtype == torch.float32:
+        return 1
+    if t.dtype == torch.bfloat16:
+        return 0
+    raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+
+
+def _logits(logits):
+    torch = _torch()
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a CUDA (HIP) tensor")
+    code = _dtype_code(logits, "logits")
+    _need(logits, logits.dtype, "logits", 2)
+    return code
+
+
+def route(logits, top_k: int, score: str = "softmax", bias=None, n_groups: int = 1,
+          top_groups: int = 1, group_value: str = "top2", renormalize: bool = True,
+          scale: float = 1.0) -> Routing:
+    """Route T tokens to top_k of E experts (logits [T, E] BF16 or FP32).
+
+    score       "softmax" over all experts or "sigmoid" of each.
+    bias        FP32 [E], added to the scores for the choice only (balance).
+    n_groups, top_groups, group_value
+                with n_groups > 1 only the experts of the top_groups best
+                groups of consecutive experts can be chosen; a group's value
+                is the sum of its best two ("top2") or its best ("max").
+    renormalize weights are divided by their sum; scale multiplies them.
+
+    Experts with a logit of -inf are masked; a token with fewer than top_k
+    unmasked experts has -1 and weight 0 in the places left over.  Equal
+    values go to the lowest index.
+    """
+    torch = _torch()
+    if score not in SCORES:
+        raise ValueError(f"unknown score {score!r}; expected one of {list(SCORES)}")
+    if group_value not in GROUP_VALUES:
+        raise ValueError(f"unknown group value {group_value!r}; expected one of {list(GROUP_VALUES)}")
+    code = _logits(logits)
+    T, E = logits.shape
+    if bias is not None:
+        _need(bias, torch.float32, "bias", 1)
+        _shape(bias, (E,), "bias")
+    top_k = int(top_k)
+    if not 1 <= top_k <= E:
+        raise ValueError(f"top_k {top_k} not in [1, {E}]")
+    dev, i32 = logits.device, torch.int32
+    weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    experts = torch.empty((T, top_k), dtype=i32, device=dev)
+    offsets = torch.empty(E + 1, dtype=torch.int64, device=dev)
+    slots = torch.empty((T, top_k), dtype=i32, device=dev)
+    nws = mx_route_workspace_size(T, E)
+    ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
+    _check(mx_route(SCORES[score], code, _ptr(logits), _ptr(bias), T, E, top_k, n_groups, top_groups,
+                    GROUP_VALUES[group_value], int(bool(renormalize)), scale, _ptr(weights),
+                    _ptr(experts), _ptr(offsets), _ptr(slots), _ptr(ws), nws, _stream(dev)))
+    return Routing(weights, experts, offsets, slots)
+
+
+def route_backward(dweights, logits, experts, score: str = "softmax", renormalize: bool = True,
+                   scale: float = 1.0):
+    """Gradient of ``route``'s weights with respect to the logits, for the
+    choice it made: dweights FP32 [T, k], experts INT32 [T, k] -> dlogits
+    [T, E] in the logits' type."""
+    torch = _torch()
+    if score not in SCORES:
+        raise ValueError(f"unknown score {score!r}; expected one of {list(SCORES)}")
+    code = _logits(logits)
+    _need(dweights, torch.float32, "dweights", 2)
+    _need(experts, torch.int32, "experts", 2)
+    T, E = logits.shape
+    k = experts.shape[1]
+    _shape(experts, (T, k), "experts")
+    _shape(dweights, (T, k), "dweights")
+    out = torch.empty_like(logits)
+    _check(mx_route_backward(SCORES[score], code, _ptr(dweights), _ptr(logits), _ptr(experts), T, E, k,
+                             int(bool(renormalize)), scale, _ptr(out), _stream(logits.device)))
+    return out
+
+
+def _routed(routing, weights: bool = False):
+    """(T, k, E) of a routing, after checking the tensors a call reads."""
+    torch = _torch()
+    offsets, slots = routing.offsets, routing.slots
+    _need(slots, torch.int32, "routing.slots", 2)
+    _need(offsets, torch.int64, "routing.offsets", 1)
+    T, k = slots.shape
+    if weights:
+        _need(routing.weights, torch.float32, "routing.weights", 2)
+        _shape(routing.weights, (T, k), "routing.weights")
+    if offsets.numel() < 2:
+        raise ValueError("routing.offsets must hold at least two entries (one expert)")
+    return T, k, offsets.numel() - 1
+
+
+def dispatch(x, routing):
+    """Token rows in the expert order: x BF16 [T, H] -> BF16 [T k, H] with
+    row slots[t, j] = x[t]; rows that no choice takes are zero.  Its gradient
+    is ``combine(dy, routing, weighted=False)``."""
+    torch = _torch()
+    T, k, E = _routed(routing)
+    _need(x, torch.bfloat16, "x", 2)
+    H = x.shape[1]
+    _shape(x, (T, H), "x")
+    y = torch.empty((T * k, H), dtype=torch.bfloat16, device=x.device)
+    _check(mx_dispatch(_ptr(x), T, H, k, E, _ptr(routing.offsets), _ptr(routing.slots), _ptr(y),
+                       _stream(x.device)))
+    return y
+
+
+def dispatch_quant(x, routing, elem: str = "e4m3"):
+    """``quant(dispatch(x, routing), "row", elem)`` in one pass: (q [T k, H]
+    u8, s [T k, H/32] u8), ``grouped_gemm``'s a and sa."""
+    torch = _torch()
+    if elem not in ELEM_TYPES:
+        raise ValueError(f"unknown element type {elem!r}; expected one of {list(ELEM_TYPES)}")
+    T, k, E = _routed(routing)
+    _need(x, torch.bfloat16, "x", 2)
+    H = x.shape[1]
+    _shape(x, (T, H), "x")
+    q = torch.empty((T * k, H), dtype=torch.uint8, device=x.device)
+    s = torch.empty((T * k, H // 32), dtype=torch.uint8, device=x.device)
+    _check(mx_dispatch_quant(ELEM_TYPES[elem], _ptr(x), T, H, k, E, _ptr(routing.offsets),
+                             _ptr(routing.slots), _ptr(q), _ptr(s), _stream(x.device)))
+    return q, s
+
+
+def combine(y, routing, residual=None, weighted: bool = True, out=None):
+    """Expert rows back to the tokens: y BF16 [T k, H] -> BF16 [T, H],
+    out[t] = residual[t] + sum_j weights[t, j] y[slots[t, j]] (weights of one
+    with weighted=False).  out may be residual."""
+    torch = _torch()
+    T, k, _ = _routed(routing, weighted)
+    _need(y, torch.bfloat16, "y", 2)
+    H = y.shape[1]
+    _shape(y, (T * k, H), "y")
+    if residual is not None:
+        _need(residual, torch.bfloat16, "residual", 2)
+        _shape(residual, (T, H), "residual")
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=y.device)
+    else:
+        _need(out, torch.bfloat16, "out", 2)
+        _shape(out, (T, H), "out")
+    _check(mx_combine(_ptr(y), T, H, k, _ptr(routing.slots),
+                      _ptr(routing.weights) if weighted else None, _ptr(residual), _ptr(out),
+                      _stream(y.device)))
+    return out
+
+
+def combine_backward(dout, y, routing):
+    """Gradient of ``combine``: (dy BF16 [T k, H], dweights FP32 [T, k]) from
+    dout BF16 [T, H] and the y that was combined.  The residual's gradient is
+    dout."""
+    torch = _torch()
+    T, k, E = _routed(routing, True)
+    _need(dout, torch.bfloat16, "dout", 2)
+    _need(y, torch.bfloat16, "y", 2)
+    H = dout.shape[1]
+    _shape(dout, (T, H), "dout")
+    _shape(y, (T * k, H), "y")
+    dy = torch.empty((T * k, H), dtype=torch.bfloat16, device=y.device)
+    dw = torch.empty((T, k), dtype=torch.float32, device=y.device)
+    _check(mx_combine_backward(_ptr(dout), _ptr(y), T, H, k, E, _ptr(routing.offsets),
+                               _ptr(routing.slots), _ptr(routing.weights), _ptr(dy), _ptr(dw),
+                               _stream(y.device)))
+    return dy, dw
+
+
+def _tensor_list(tensors):
+    """(count, pointers, element counts, element types) of gradients."""
+    tensors = list(tensors)
+    n = len(tensors)
+    codes = []
+    for i, t in enumerate(tensors):
+        code = _dtype_code(t, f"tensors[{i}]")
+        _need(t, t.dtype, f"tensors[{i}]")
+        codes.append(code)
+    return (n, (ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]),
+            (ctypes.c_int64 * n)(*[t.numel() for t in tensors]), (ctypes.c_int * n)(*codes))
+
+
+def _norm_buffers(n, device):
+    torch = _torch()
+    nws = mx_grad_norm_workspace_size(n)
+    norm = torch.empty((), dtype=torch.float32, device=device)
+    ws = torch.empty(nws, dtype=torch.uint8, device=device) if nws else None
+    return norm, ws, nws
+
+
+def grad_norm(tensors):
+    """L2 norm of all elements of a list of BF16 and FP32 tensors, as a 0-d
+    FP32 tensor on the device."""
+    tensors = list(tensors)
+    n, ptrs, sizes, codes = _tensor_list(tensors)
+    device = tensors[0].device if tensors else "cuda"
+    norm, ws, nws = _norm_buffers(n, device)
+    _check(mx_grad_norm(n, ptrs, sizes, codes, _ptr(norm), _ptr(ws), nws, _stream(device)))
+    return norm
+
+
+def grad_clip(tensors, max_norm: float):
+    """Scale a list of BF16 and FP32 tensors in place by min(1, max_norm /
+    (norm + 1e-6)), norm their global L2 norm; returns the norm before, as a
+    0-d FP32 tensor on the device.  Tensors of the list must not overlap."""
+    tensors = list(tensors)
+    n, ptrs, sizes, codes = _tensor_list(tensors)
+    device = tensors[0].device if tensors else "cuda"
+    norm, ws, nws = _norm_buffers(n, device)
+    _check(mx_grad_clip(n, ptrs, sizes, codes, max_norm, _ptr(norm), _ptr(ws), nws, _stream(device)))
+    return norm

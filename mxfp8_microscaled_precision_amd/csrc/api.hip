@@ -2,10 +2,13 @@
 // (before any HIP call), the gfx950 gate, and dispatch to the kernels.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <memory>
 #include <mutex>
+#include <new>
 
 #include "../../include/mxfp8.h"
 #include "mx_kernels.h"
@@ -74,6 +77,78 @@ bool row_tiles_too_large(int64_t R) { return ((R + 127) / 128) * 512 >= (int64_t
 // The GEMM kernels address a 256-row tile with 32-bit offsets (rows * K or
 // rows * cap bytes, out-of-range loads flagged by bit 31).
 constexpr int64_t K_LIMIT = (int64_t(1) << 31) / 256;
+
+constexpr int64_t MAX_EXPERTS = 512, MAX_TOP_K = 16, MAX_EXPERT_GROUPS = 32;
+
+// Sizes that routing, dispatch and combine share.
+mx_status check_routing(int64_t T, int64_t E, int64_t top_k) {
+  if (T < 0) return fail(MX_ERR_INVALID_ARG, "negative token count %lld", (long long)T);
+  if (E < 1 || E > MAX_EXPERTS)
+    return fail(MX_ERR_INVALID_ARG, "expert count %lld not in [1, 512]", (long long)E);
+  if (top_k < 1 || top_k > MAX_TOP_K || top_k > E)
+    return fail(MX_ERR_INVALID_ARG, "top_k %lld not in [1, min(16, experts)]", (long long)top_k);
+  if (T >= (int64_t(1) << 31) / top_k)
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%lld tokens x %lld choices reach 2^31 rows", (long long)T,
+                (long long)top_k);
+  return MX_OK;
+}
+
+mx_status check_move(int64_t T, int64_t H, int64_t E, int64_t top_k) {
+  const mx_status st = check_routing(T, E, top_k);
+  if (st != MX_OK) return st;
+  if (H < 0) return fail(MX_ERR_INVALID_ARG, "negative row length %lld", (long long)H);
+  // one wave per token and 512 elements, fewer than 2^32 work-items
+  if (H > (int64_t(1) << 40) || mul_overflows(T, H / 512 + 1) ||
+      T * ((H + 511) / 512) >= (int64_t(1) << 26))
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%lld tokens of %lld elements exceed one launch grid",
+                (long long)T, (long long)H);
+  return MX_OK;
+}
+
+// The tensors of a gradient list; with `apart`, that no two share memory.
+mx_status check_tensors(int64_t n, const void* const* tensors, const int64_t* numels,
+                        const mx_dtype* dtypes, bool apart) {
+  if (n < 0 || n > (1 << 24)) return fail(MX_ERR_INVALID_ARG, "tensor count %lld", (long long)n);
+  if (n > 0 && (!tensors || !numels || !dtypes))
+    return fail(MX_ERR_INVALID_ARG, "tensors, numels or dtypes is NULL");
+  int64_t bytes = 0;
+  for (int64_t i = 0; i < n; i++) {
+    if (dtypes[i] != MX_DTYPE_BF16 && dtypes[i] != MX_DTYPE_F32)
+      return fail(MX_ERR_INVALID_ARG, "tensor %lld: unknown element type %d", (long long)i, (int)dtypes[i]);
+    if (numels[i] < 0) return fail(MX_ERR_INVALID_ARG, "tensor %lld: negative size", (long long)i);
+    if (numels[i] > 0 && !tensors[i]) return fail(MX_ERR_INVALID_ARG, "tensor %lld is NULL", (long long)i);
+    const uintptr_t size = dtypes[i] == MX_DTYPE_F32 ? 4 : 2;
+    if (numels[i] > 0 && (uintptr_t)tensors[i] % size != 0)
+      return fail(MX_ERR_INVALID_ARG, "tensor %lld is not aligned to its elements", (long long)i);
+    if (numels[i] >= (int64_t(1) << 45) || (bytes += numels[i] * (int64_t)size) >= (int64_t(1) << 45))
+      return fail(MX_ERR_UNSUPPORTED_SHAPE, "the tensors hold 2^45 bytes or more");
+  }
+  if (!apart || n < 2) return MX_OK;
+  struct Span {
+    uintptr_t lo, hi;
+  };
+  std::unique_ptr<Span[]> v(new (std::nothrow) Span[(size_t)n]);
+  if (!v) return fail(MX_ERR_INVALID_ARG, "no host memory for %lld tensors", (long long)n);
+  int64_t m = 0;
+  for (int64_t i = 0; i < n; i++)
+    if (numels[i] > 0) {
+      const uintptr_t lo = (uintptr_t)tensors[i];
+      v[(size_t)m++] = {lo, lo + (uintptr_t)numels[i] * (dtypes[i] == MX_DTYPE_F32 ? 4 : 2)};
+    }
+  std::sort(v.get(), v.get() + m, [](const Span& a, const Span& b) { return a.lo < b.lo; });
+  for (int64_t i = 1; i < m; i++)
+    if (v[(size_t)i].lo < v[(size_t)i - 1].hi)
+      return fail(MX_ERR_INVALID_ARG, "two tensors of the list share memory");
+  return MX_OK;
+}
+
+mx_status check_score(mx_score score, mx_dtype dtype) {
+  if (score != MX_SCORE_SOFTMAX && score != MX_SCORE_SIGMOID)
+    return fail(MX_ERR_INVALID_ARG, "unknown score %d", (int)score);
+  if (dtype != MX_DTYPE_BF16 && dtype != MX_DTYPE_F32)
+    return fail(MX_ERR_INVALID_ARG, "unknown element type %d", (int)dtype);
+  return MX_OK;
+}
 
 }  // namespace
 
@@ -458,6 +533,184 @@ mx_status mx_grouped_gemm_wgrad(int64_t G, const int64_t* offsets, int64_t T, in
                                 void* c, hipStream_t stream) {
   return mx_grouped_gemm_wgrad_elem(MX_ELEM_E4M3, MX_ELEM_E4M3, G, offsets, T, M, N, a, sa, b, sb,
                                     c, stream);
+}
+
+size_t mx_route_workspace_size(int64_t T, int64_t E) {
+  if (T < 1 || T >= (int64_t(1) << 31) || E < 1 || E > MAX_EXPERTS) return 0;
+  return mx::route_workspace(T, E);
+}
+
+mx_status mx_route(mx_score score, mx_dtype dtype, const void* logits, const float* bias,
+                   int64_t T, int64_t E, int64_t top_k, int64_t n_groups, int64_t top_groups,
+                   mx_group_value group_value, int renormalize, float scale, float* weights,
+                   int32_t* experts, int64_t* offsets, int32_t* slots, void* workspace,
+                   size_t workspace_bytes, hipStream_t stream) {
+  g_err[0] = '\0';
+  mx_status st = check_score(score, dtype);
+  if (st == MX_OK) st = check_routing(T, E, top_k);
+  if (st != MX_OK) return st;
+  if (group_value != MX_GROUP_TOP2 && group_value != MX_GROUP_MAX)
+    return fail(MX_ERR_INVALID_ARG, "unknown group value %d", (int)group_value);
+  if (n_groups < 1 || n_groups > MAX_EXPERT_GROUPS || E % n_groups != 0)
+    return fail(MX_ERR_INVALID_ARG, "%lld groups: a divisor of the %lld experts in [1, 32] is needed",
+                (long long)n_groups, (long long)E);
+  if (top_groups < 1 || top_groups > n_groups)
+    return fail(MX_ERR_INVALID_ARG, "top_groups %lld not in [1, %lld]", (long long)top_groups,
+                (long long)n_groups);
+  if (top_k > top_groups * (E / n_groups))
+    return fail(MX_ERR_INVALID_ARG, "top_k %lld exceeds the %lld experts of %lld groups",
+                (long long)top_k, (long long)(top_groups * (E / n_groups)), (long long)top_groups);
+  if (!offsets) return fail(MX_ERR_INVALID_ARG, "offsets is NULL");
+  if (T > 0 && (!logits || !weights || !experts || !slots))
+    return fail(MX_ERR_INVALID_ARG, "logits, weights, experts or slots is NULL");
+  const size_t need = mx_route_workspace_size(T, E);
+  if (workspace_bytes < need || (need > 0 && !workspace))
+    return fail(MX_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  int dev;
+  st = current_device(&dev);
+  if (st != MX_OK) return st;
+  hipError_t e;
+  if (T == 0)
+    e = mx::launch_fill_zero(offsets, 8 * (E + 1), stream);
+  else
+    e = mx::launch_route(score == MX_SCORE_SOFTMAX, dtype == MX_DTYPE_F32, logits, bias, T, E, top_k,
+                         n_groups, top_groups, group_value == MX_GROUP_MAX, renormalize != 0, scale,
+                         weights, experts, offsets, slots, workspace, stream);
+  if (e != hipSuccess) return hip_fail(e, "routing kernel launch");
+  return MX_OK;
+}
+
+mx_status mx_route_backward(mx_score score, mx_dtype dtype, const float* dweights,
+                            const void* logits, const int32_t* experts, int64_t T, int64_t E,
+                            int64_t top_k, int renormalize, float scale, void* dlogits,
+                            hipStream_t stream) {
+  g_err[0] = '\0';
+  mx_status st = check_score(score, dtype);
+  if (st == MX_OK) st = check_routing(T, E, top_k);
+  if (st != MX_OK) return st;
+  if (T >= (int64_t(1) << 28))
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%lld tokens exceed one launch grid", (long long)T);
+  if (T == 0) return MX_OK;
+  if (!dweights || !logits || !experts || !dlogits)
+    return fail(MX_ERR_INVALID_ARG, "dweights, logits, experts or dlogits is NULL");
+  int dev;
+  st = current_device(&dev);
+  if (st != MX_OK) return st;
+  const hipError_t e = mx::launch_route_backward(score == MX_SCORE_SOFTMAX, dtype == MX_DTYPE_F32, T, E,
+                                                 top_k, renormalize != 0, scale, dweights, logits,
+                                                 experts, dlogits, stream);
+  if (e != hipSuccess) return hip_fail(e, "routing gradient kernel launch");
+  return MX_OK;
+}
+
+mx_status mx_dispatch(const void* x, int64_t T, int64_t H, int64_t top_k, int64_t E,
+                      const int64_t* offsets, const int32_t* slots, void* y, hipStream_t stream) {
+  g_err[0] = '\0';
+  mx_status st = check_move(T, H, E, top_k);
+  if (st != MX_OK) return st;
+  if (T == 0 || H == 0) return MX_OK;
+  if (!x || !offsets || !slots || !y)
+    return fail(MX_ERR_INVALID_ARG, "x, offsets, slots or y is NULL");
+  int dev;
+  st = current_device(&dev);
+  if (st != MX_OK) return st;
+  const hipError_t e = mx::launch_dispatch(x, T, H, top_k, E, offsets, slots, y, stream);
+  if (e != hipSuccess) return hip_fail(e, "dispatch kernel launch");
+  return MX_OK;
+}
+
+mx_status mx_dispatch_quant(mx_elem_type elem, const void* x, int64_t T, int64_t H, int64_t top_k,
+                            int64_t E, const int64_t* offsets, const int32_t* slots, void* q,
+                            void* s, hipStream_t stream) {
+  g_err[0] = '\0';
+  if (elem != MX_ELEM_E4M3 && elem != MX_ELEM_E5M2)
+    return fail(MX_ERR_INVALID_ARG, "unknown element type %d", (int)elem);
+  mx_status st = check_move(T, H, E, top_k);
+  if (st != MX_OK) return st;
+  if (H % 32 != 0)
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "row length %lld is not a multiple of 32", (long long)H);
+  if (T == 0 || H == 0) return MX_OK;
+  if (!x || !offsets || !slots || !q || !s)
+    return fail(MX_ERR_INVALID_ARG, "x, offsets, slots, q or s is NULL");
+  int dev;
+  st = current_device(&dev);
+  if (st != MX_OK) return st;
+  const hipError_t e =
+      mx::launch_dispatch_quant((int)elem, x, T, H, top_k, E, offsets, slots, q, s, stream);
+  if (e != hipSuccess) return hip_fail(e, "quantising dispatch kernel launch");
+  return MX_OK;
+}
+
+mx_status mx_combine(const void* y, int64_t T, int64_t H, int64_t top_k, const int32_t* slots,
+                     const float* weights, const void* residual, void* out, hipStream_t stream) {
+  g_err[0] = '\0';
+  mx_status st = check_move(T, H, MAX_EXPERTS, top_k);
+  if (st != MX_OK) return st;
+  if (T == 0 || H == 0) return MX_OK;
+  if (!y || !slots || !out) return fail(MX_ERR_INVALID_ARG, "y, slots or out is NULL");
+  int dev;
+  st = current_device(&dev);
+  if (st != MX_OK) return st;
+  const hipError_t e = mx::launch_combine(y, T, H, top_k, slots, weights, residual, out, stream);
+  if (e != hipSuccess) return hip_fail(e, "combine kernel launch");
+  return MX_OK;
+}
+
+mx_status mx_combine_backward(const void* dout, const void* y, int64_t T, int64_t H, int64_t top_k,
+                              int64_t E, const int64_t* offsets, const int32_t* slots,
+                              const float* weights, void* dy, float* dweights, hipStream_t stream) {
+  g_err[0] = '\0';
+  mx_status st = check_move(T, H, E, top_k);
+  if (st != MX_OK) return st;
+  if (T >= (int64_t(1) << 24))
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%lld tokens exceed one launch grid", (long long)T);
+  if (T == 0) return MX_OK;
+  if (!offsets || !slots || !weights || !dweights || (H > 0 && (!dout || !y || !dy)))
+    return fail(MX_ERR_INVALID_ARG, "a pointer is NULL");
+  int dev;
+  st = current_device(&dev);
+  if (st != MX_OK) return st;
+  const hipError_t e = mx::launch_combine_backward(dout, y, T, H, top_k, E, offsets, slots, weights,
+                                                   dy, dweights, stream);
+  if (e != hipSuccess) return hip_fail(e, "combine gradient kernel launch");
+  return MX_OK;
+}
+
+size_t mx_grad_norm_workspace_size(int64_t n) { return n <= 0 ? 0 : mx::grad_workspace(n); }
+
+static mx_status grad_call(int64_t n, void* const* tensors, const int64_t* numels,
+                           const mx_dtype* dtypes, bool clip, float max_norm, float* norm,
+                           void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  mx_status st = check_tensors(n, tensors, numels, dtypes, clip);
+  if (st != MX_OK) return st;
+  if (!norm) return fail(MX_ERR_INVALID_ARG, "norm is NULL");
+  const size_t need = mx_grad_norm_workspace_size(n);
+  if (workspace_bytes < need || (need > 0 && !workspace))
+    return fail(MX_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  int dev;
+  st = current_device(&dev);
+  if (st != MX_OK) return st;
+  static_assert(sizeof(mx_dtype) == sizeof(int) && MX_DTYPE_F32 == 1, "element types are passed as int");
+  const hipError_t e = mx::launch_grad(n, tensors, numels, (const int*)dtypes, clip, max_norm, norm,
+                                       workspace, stream);
+  if (e != hipSuccess) return hip_fail(e, "gradient norm kernel launch");
+  return MX_OK;
+}
+
+mx_status mx_grad_norm(int64_t n, const void* const* tensors, const int64_t* numels,
+                       const mx_dtype* dtypes, float* norm, void* workspace,
+                       size_t workspace_bytes, hipStream_t stream) {
+  g_err[0] = '\0';
+  return grad_call(n, const_cast<void* const*>(tensors), numels, dtypes, false, 0.0f, norm, workspace,
+                   workspace_bytes, stream);
+}
+
+mx_status mx_grad_clip(int64_t n, void* const* tensors, const int64_t* numels,
+                       const mx_dtype* dtypes, float max_norm, float* norm, void* workspace,
+                       size_t workspace_bytes, hipStream_t stream) {
+  g_err[0] = '\0';
+  if (!(max_norm >= 0.0f)) return fail(MX_ERR_INVALID_ARG, "max_norm %g is not a norm", (double)max_norm);
+  return grad_call(n, tensors, numels, dtypes, true, max_norm, norm, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -61,4 +61,37 @@ hipError_t launch_grouped_wgrad(int a_elem, int b_elem, int64_t G, const int64_t
 // so the call can sit in a captured graph).
 hipError_t launch_fill_zero(void* p, int64_t nbytes, hipStream_t stream);
 
+// Routing [T, E] logits (f32 0 = BF16, 1 = FP32) to k experts a token; bias
+// may be null.  workspace: route_workspace(T, E) bytes.
+size_t route_workspace(int64_t T, int64_t E);
+hipError_t launch_route(int softmax, int f32, const void* logits, const float* bias, int64_t T,
+                        int64_t E, int64_t k, int64_t n_groups, int64_t top_groups, int group_max,
+                        int renorm, float scale, float* weights, int32_t* experts,
+                        int64_t* offsets, int32_t* slots, void* workspace, hipStream_t stream);
+hipError_t launch_route_backward(int softmax, int f32, int64_t T, int64_t E, int64_t k, int renorm,
+                                 float scale, const float* dweights, const void* logits,
+                                 const int32_t* experts, void* dlogits, hipStream_t stream);
+
+// Token rows into the expert order and back (slots [T, k], -1 for none).
+hipError_t launch_dispatch(const void* x, int64_t T, int64_t H, int64_t k, int64_t E,
+                           const int64_t* offsets, const int32_t* slots, void* y,
+                           hipStream_t stream);
+hipError_t launch_dispatch_quant(int elem, const void* x, int64_t T, int64_t H, int64_t k, int64_t E,
+                                 const int64_t* offsets, const int32_t* slots, void* q, void* s,
+                                 hipStream_t stream);
+hipError_t launch_combine(const void* y, int64_t T, int64_t H, int64_t k, const int32_t* slots,
+                          const float* weights, const void* residual, void* out,
+                          hipStream_t stream);
+hipError_t launch_combine_backward(const void* dout, const void* y, int64_t T, int64_t H, int64_t k,
+                                   int64_t E, const int64_t* offsets, const int32_t* slots,
+                                   const float* weights, void* dy, float* dweights,
+                                   hipStream_t stream);
+
+// Norm of n tensors (f32[i] 0 = BF16, 1 = FP32), and, with clip, their
+// scaling in place.  workspace: grad_workspace(n) bytes.
+constexpr int GRAD_TENSORS = 160;  // tensors of one launch: their table fills a kernel's 4 KiB of arguments
+size_t grad_workspace(int64_t n);
+hipError_t launch_grad(int64_t n, void* const* tensors, const int64_t* numels, const int* f32,
+                       int clip, float max_norm, float* norm, void* workspace, hipStream_t stream);
+
 }  // namespace mx
