@@ -338,9 +338,10 @@ typedef enum mx_group_value {
  * ones, and only those of the top_groups best groups stay.  The top_k
  * unmasked experts with the largest v are chosen, in descending order, equal
  * values by the lowest index (groups alike).  The choice follows the scores,
- * not their 32-bit roundings: logits are compared as they are where that is
- * the same order, otherwise v in 64 bits, where values that agree in their
- * first 43 bits count as equal.  A NaN value ranks below every number.
+ * not their 32-bit roundings: without a bias experts are compared by their
+ * logits, whose order the scores keep; with one by v, and groups by their
+ * sums, in 64 bits, where values that agree in their first 43 bits count as
+ * equal.  A NaN value ranks below every number.
  *   weights [T, top_k] FP32: w_j = scale * s[e_j], or with renormalize
  *            scale * s[e_j] / sum_i s[e_i]; 0 where no expert is left.  Under
  *            softmax a NaN logit makes its token's weights NaN; a +inf logit

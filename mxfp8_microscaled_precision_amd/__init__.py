@@ -282,8 +282,11 @@ def _ptr(t):
 
 
 def _stream(device):
+    # the raw handle alone: building a torch.cuda.Stream object takes 2 us of
+    # host time, as long as a launch
     torch = _torch()
-    return torch.cuda.current_stream(device).cuda_stream
+    index = torch.cuda.current_device() if device.index is None else device.index
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _need(t, dtype, name, ndim=None):
@@ -761,14 +764,23 @@ def combine_backward(dout, y, routing):
 
 
 def _tensor_list(tensors):
-    """(count, pointers, element counts, element types) of gradients."""
-    tensors = list(tensors)
+    """(count, pointers, element counts, element types) of gradients.  A list
+    holds hundreds of tensors, so each property is checked in one sweep and
+    the tensor at fault is looked for only once there is one."""
+    torch = _torch()
     n = len(tensors)
-    codes = []
-    for i, t in enumerate(tensors):
-        code = _dtype_code(t, f"tensors[{i}]")
-        _need(t, t.dtype, f"tensors[{i}]")
-        codes.append(code)
+    known = {torch.bfloat16: 0, torch.float32: 1}
+    try:
+        codes = [known[t.dtype] for t in tensors]
+        good = ({t.get_device() for t in tensors} <= {torch.cuda.current_device()}
+                and False not in {t.is_contiguous() for t in tensors})
+    except (AttributeError, KeyError, RuntimeError, AssertionError):
+        good = False
+    if not good:
+        for i, t in enumerate(tensors):
+            _need(t, getattr(t, "dtype", None), f"tensors[{i}]")
+            _dtype_code(t, f"tensors[{i}]")
+        codes = [known[t.dtype] for t in tensors]
     return (n, (ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]),
             (ctypes.c_int64 * n)(*[t.numel() for t in tensors]), (ctypes.c_int * n)(*codes))
 

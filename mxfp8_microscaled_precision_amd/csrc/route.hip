@@ -9,9 +9,10 @@
 //   their sum.  Then a stable counting sort of the choices by expert.
 //
 // The choice follows the scores and not their 32-bit roundings.  Without a
-// bias (and with groups valued by their best) both score functions keep the
-// logits' order, so the logits themselves are compared; otherwise v is
-// computed in 64 bits.
+// bias both score functions keep the logits' order, so the logits themselves
+// are compared (and only a group's best two are scored, in 64 bits).  With a
+// bias v is first taken from 32-bit scores; where two values that the choice
+// turns on lie closer than their error, the wave chooses again from 64 bits.
 //
 // A key for the choice is a double whose low 9 mantissa bits are replaced by
 // the expert's index (E <= 512), so that keys are distinct, a tie falls to
@@ -22,12 +23,10 @@
 
 namespace mx {
 
-constexpr int ROUTE_LANES = 16;                 // lanes that share a token
-constexpr int ROUTE_THREADS = 1024;
-constexpr int ROUTE_TOKENS = ROUTE_THREADS / ROUTE_LANES;  // tokens of one pass of a workgroup
 constexpr int ROUTE_MAX_EXPERTS = 512;
 constexpr int ROUTE_MAX_GROUPS = 32;
 constexpr int ROUTE_MAX_BLOCKS = 256;
+constexpr int ROUTE_TOKENS = 64;                // a workgroup's tokens are a multiple
 
 #define MX_NEG_INF (-__builtin_inf())
 
@@ -52,31 +51,62 @@ __device__ __forceinline__ double dpp(double v) {
   return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
 }
 
-template <typename F, typename T>
+// Larger and smaller of two values of which neither is NaN.  fmax and fmin
+// quiet a possible signalling NaN with an instruction of its own for every
+// operand that comes from a lane exchange or from bit operations, which the
+// sorting below mostly consists of.
+__device__ __forceinline__ double larger(double a, double b) {
+  double r;
+  asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+__device__ __forceinline__ double smaller(double a, double b) {
+  double r;
+  asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+__device__ __forceinline__ float larger(float a, float b) {
+  float r;
+  asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+
+// Over the L = 8 or 16 lanes that share a token.
+template <int L, typename F, typename T>
 __device__ __forceinline__ T row_reduce(T v, F f) {
   v = f(v, dpp<DPP_XOR1>(v));
   v = f(v, dpp<DPP_XOR2>(v));
   v = f(v, dpp<DPP_HALF_MIRROR>(v));
-  return f(v, dpp<DPP_MIRROR>(v));
+  return L == 8 ? v : f(v, dpp<DPP_MIRROR>(v));
 }
-template <typename T>
+template <int L, typename T>
 __device__ __forceinline__ T row_sum(T v) {
-  return row_reduce(v, [](T a, T b) { return a + b; });
+  return row_reduce<L>(v, [](T a, T b) { return a + b; });
 }
-__device__ __forceinline__ float row_max(float v) {
-  return row_reduce(v, [](float a, float b) { return fmaxf(a, b); });
-}
-__device__ __forceinline__ double row_max(double v) {
-  return row_reduce(v, [](double a, double b) { return fmax(a, b); });
+// Largest of numbers (no NaN).
+template <int L, typename T>
+__device__ __forceinline__ T row_max(T v) {
+  return row_reduce<L>(v, [](T a, T b) { return larger(a, b); });
 }
 
 // Key of value v with index i: NaN below every number, infinities beyond
-// every finite value, -0 as 0.
+// every finite value, -0 as 0.  A negative value holds the index itself, a
+// positive one its 9-bit complement, so that the lower index is the larger key.
 __device__ __forceinline__ double make_key(double v, int i) {
   v = v != v ? -1.7e308 : fmin(fmax(v + 0.0, -1.6e308), 1.6e308);
-  const uint64_t b = (uint64_t)__double_as_longlong(v) & ~(uint64_t)511;
-  const bool neg = (b >> 63) != 0;
-  return __longlong_as_double((long long)(b | (uint64_t)(neg ? i : 511 - i)));
+  const uint64_t b = (uint64_t)__double_as_longlong(v);
+  const uint32_t neg = (uint32_t)((int32_t)(b >> 32) >> 31);
+  const uint32_t low = ((uint32_t)b & ~511u) | ((511u - (uint32_t)i) ^ (neg & 511u));
+  return __longlong_as_double((long long)((b & 0xFFFFFFFF00000000ull) | low));
+}
+// The same for a 32-bit value below +inf that is not NaN nor -0: a double
+// made from it has its low 29 bits free.
+__device__ __forceinline__ double make_key32(float v, int i) {
+  const uint64_t b = (uint64_t)__double_as_longlong((double)v);
+  const uint32_t neg = (uint32_t)((int32_t)(b >> 32) >> 31);
+  const uint32_t low = (uint32_t)b | ((511u - (uint32_t)i) ^ (neg & 511u));
+  return __longlong_as_double(
+      (long long)((b & 0xFFFFFFFF00000000ull) | (v == -__builtin_inff() ? 0u : low)));
 }
 __device__ __forceinline__ int key_index(double k) {
   const uint64_t b = (uint64_t)__double_as_longlong(k);
@@ -111,23 +141,32 @@ __device__ __forceinline__ void store_logit(uint16_t* p, float v) {
   *p = (uint16_t)cvt_pk_bf16(v, v);
 }
 
-// Chunk c of a token's row held by lane l: experts (16 c + l) * 4 .. + 3;
-// -inf past the row.
-template <typename IN, int C>
+// Experts e0 .. e0 + 3 of a row; -inf past it.
+template <typename IN>
+__device__ __forceinline__ void load_chunk(const IN* __restrict__ row, int E, bool vec, int e0,
+                                           float x[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; i++) x[i] = -__builtin_inff();
+  if (vec) {
+    if (e0 < E) load_logit4(row + e0, x);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+      if (e0 + i < E) x[i] = load_logit(row + e0 + i);
+  }
+}
+
+// Chunk c of a token's row held by lane l: experts (L c + l) * 4 .. + 3.
+template <typename IN, int L, int C>
 __device__ __forceinline__ void load_row(const IN* __restrict__ row, int E, bool vec, int l,
                                          bool live, float x[C][4]) {
 #pragma unroll
   for (int c = 0; c < C; c++) {
-    const int e0 = (c * ROUTE_LANES + l) * 4;
-#pragma unroll
-    for (int i = 0; i < 4; i++) x[c][i] = -__builtin_inff();
-    if (!live) continue;
-    if (vec) {
-      if (e0 < E) load_logit4(row + e0, x[c]);
+    if (live) {
+      load_chunk(row, E, vec, (c * L + l) * 4, x[c]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; i++)
-        if (e0 + i < E) x[c][i] = load_logit(row + e0 + i);
+      for (int i = 0; i < 4; i++) x[c][i] = -__builtin_inff();
     }
   }
 }
@@ -136,205 +175,605 @@ __device__ __forceinline__ void load_row(const IN* __restrict__ row, int E, bool
 // +inf shares its weight among the infinite logits.
 __device__ __forceinline__ float exp_diff(float x, float m) { return x == m ? 1.0f : expf(x - m); }
 
+// 2^p for |p| <= 1022 to 2^-47 of its value, four bits more than a key keeps:
+// p = n + f with |f| <= 1/2 and the Taylor series of e^(f ln 2) to the 11th
+// power (remainder (ln 2 / 2)^12 / 12! = 2^-47.2).  A third of the library
+// function's instructions; all of the choice's 64-bit work.
+__device__ __forceinline__ double pow2_64(double n, double f) {
+  constexpr double L = 0.693147180559945309417;
+  constexpr double c2 = L * L / 2, c3 = c2 * L / 3, c4 = c3 * L / 4, c5 = c4 * L / 5, c6 = c5 * L / 6,
+                   c7 = c6 * L / 7, c8 = c7 * L / 8, c9 = c8 * L / 9, c10 = c9 * L / 10,
+                   c11 = c10 * L / 11;
+  double s = fma(c11, f, c10);
+  s = fma(s, f, c9);
+  s = fma(s, f, c8);
+  s = fma(s, f, c7);
+  s = fma(s, f, c6);
+  s = fma(s, f, c5);
+  s = fma(s, f, c4);
+  s = fma(s, f, c3);
+  s = fma(s, f, c2);
+  s = fma(s, f, L);
+  s = fma(s, f, 1.0);
+  return ldexp(s, (int)n);
+}
+// e^x; saturates at 2^-1022 and 2^1022.  NaN stays NaN.
+__device__ __forceinline__ double exp_64(double x) {
+  constexpr double LOG2E = 1.44269504088896340736;
+  constexpr double END = 1022.0 / LOG2E;
+  x = x != x ? x : fmin(fmax(x, -END), END);
+  const double n = rint(x * LOG2E);
+  return pow2_64(n, fma(x, LOG2E, -n));
+}
+// 1 / d for 1 <= d <= 2^1022: the hardware's estimate (at least 2^-20) after
+// two Newton steps, each of which squares the error.
+__device__ __forceinline__ double rcp_64(double d) {
+  double r = __builtin_amdgcn_rcp(d);
+  r = fma(fma(-d, r, 1.0), r, r);
+  return fma(fma(-d, r, 1.0), r, r);
+}
+
 struct RouteArgs {
   const void* logits;
   const float* bias;
   int64_t T;
-  int E, k, n_groups, top_groups, group_max, softmax, renorm, vec;
+  int E, k, n_groups, top_groups, group_max, groups_pow2, softmax, renorm, vec, vec_bias;
   float scale;
   float* weights;
   int32_t* experts;
   int64_t* offsets;
   int32_t* slots;
-  int32_t* hist;         // [blocks][E] counts of every workgroup's tokens
+  uint32_t* hist;        // [blocks][(E + 1) / 2] counts of every workgroup's tokens, two a word
   int tokens_per_block;
   int blocks;
 };
 
-// The chosen groups of a token, as a mask: bit g for group g.
-template <int C>
-__device__ __forceinline__ uint32_t choose_groups(const RouteArgs& a, const double key[C][4], int l) {
-  const int gs = a.E / a.n_groups;
-  double gk[ROUTE_MAX_GROUPS / ROUTE_LANES];
+// Compare-exchange: the larger key first.
+__device__ __forceinline__ void order(double& a, double& b) {
+  const double hi = larger(a, b);
+  b = smaller(a, b);
+  a = hi;
+}
+
+// A lane's N keys in falling order after every half is: a bitonic sequence
+// (first half falling, second rising) in log2(N) steps.
+template <int N>
+__device__ __forceinline__ void bitonic(double* v) {
 #pragma unroll
-  for (int r = 0; r < ROUTE_MAX_GROUPS / ROUTE_LANES; r++) gk[r] = MX_NEG_INF;
-  for (int g = 0; g < a.n_groups; g++) {
-    double b1 = MX_NEG_INF, b2 = MX_NEG_INF;
-    const int lo = g * gs, hi = lo + gs;
+  for (int d = N / 2; d > 0; d >>= 1)
+#pragma unroll
+    for (int j = 0; j < N; j++)
+      if (!(j & d)) order(v[j], v[j + d]);
+}
+
+// Two falling lists a, b of n keys into a: all 2 n of them while they fit KC,
+// otherwise the n largest (the larger of a[j] and b[n - 1 - j], a bitonic
+// sequence).
+template <int KC, int N>
+__device__ __forceinline__ void merge(double* a, const double* b) {
+  if constexpr (2 * N <= KC) {
+#pragma unroll
+    for (int j = 0; j < N; j++) a[N + j] = b[N - 1 - j];
+    bitonic<2 * N>(a);
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; j++) a[j] = larger(a[j], b[N - 1 - j]);
+    bitonic<N>(a);
+  }
+}
+
+template <int KC, int N, int CTRL>
+__device__ __forceinline__ void merge_lanes(double* a) {
+  double o[N];
+#pragma unroll
+  for (int j = 0; j < N; j++) o[j] = dpp<CTRL>(a[j]);
+  merge<KC, N>(a, o);
+}
+
+constexpr int grown(int n, int kc) { return 2 * n <= kc ? 2 * n : n; }
+
+__device__ __forceinline__ void sort4(double v[4]) {
+  order(v[0], v[1]);
+  order(v[2], v[3]);
+  order(v[0], v[2]);
+  order(v[1], v[3]);
+  order(v[1], v[2]);
+}
+
+// Descending list of the KC largest keys of the L lanes, in every lane, from
+// the lanes' sorted chunks: chunks are merged in a lane, then lanes.
+template <int L, int C, int KC>
+__device__ __forceinline__ void top_keys(const double key[C][4], double top[KC]) {
+  double half[C > 4 ? 2 : 1][KC];
+  constexpr int N1 = C >= 2 ? grown(4, KC) : 4;      // after pairs of chunks
+  constexpr int N2 = C >= 4 ? grown(N1, KC) : N1;    // after fours
+#pragma unroll
+  for (int h = 0; h < (C > 4 ? 2 : 1); h++) {
+    double pair[2][KC];
+#pragma unroll
+    for (int p = 0; p < (C >= 4 ? 2 : 1); p++) {
+      const int c = 4 * h + 2 * p;
+#pragma unroll
+      for (int i = 0; i < 4; i++) pair[p][i] = key[c][i];
+      if constexpr (C >= 2) merge<KC, 4>(pair[p], key[c + 1]);
+    }
+#pragma unroll
+    for (int j = 0; j < N1; j++) half[h][j] = pair[0][j];
+    if constexpr (C >= 4) merge<KC, N1>(half[h], pair[1]);
+  }
+  constexpr int N3 = C > 4 ? grown(N2, KC) : N2;
+#pragma unroll
+  for (int j = 0; j < N2; j++) top[j] = half[0][j];
+  if constexpr (C > 4) merge<KC, N2>(top, half[1]);
+  constexpr int N4 = grown(N3, KC), N5 = grown(N4, KC), N6 = grown(N5, KC), N7 = grown(N6, KC);
+  static_assert((L == 16 ? N7 : N6) == KC, "L lanes of four keys fill the list");
+  merge_lanes<KC, N3, DPP_XOR1>(top);
+  merge_lanes<KC, N4, DPP_XOR2>(top);
+  merge_lanes<KC, N5, DPP_HALF_MIRROR>(top);
+  if constexpr (L == 16) merge_lanes<KC, N6, DPP_MIRROR>(top);
+}
+
+// Best two of two falling pairs.
+__device__ __forceinline__ void top2(double& a1, double& a2, double b1, double b2) {
+  a2 = larger(smaller(a1, b1), larger(a2, b2));
+  a1 = larger(a1, b1);
+}
+__device__ __forceinline__ void top2(float& a1, float& a2, float b1, float b2) {
+  a2 = larger(__builtin_amdgcn_fmed3f(a1, b1, a2), b2);   // a1 >= a2: the median is min(a1, b1) or a2
+  a1 = larger(a1, b1);
+}
+template <int CTRL, typename T>
+__device__ __forceinline__ void top2_lanes(T& a1, T& a2) {
+  top2(a1, a2, dpp<CTRL>(a1), dpp<CTRL>(a2));
+}
+
+// A group's value from its best two 32-bit choice values b1 >= b2 (logits
+// where there is no bias: scored here, softmax up to a factor that the row's
+// groups share); -inf with no unmasked expert.
+template <bool SCORED>
+__device__ __forceinline__ float group_value(const RouteArgs& a, float b1, float b2, float m) {
+  constexpr float LOG2E = 1.44269504088896340736f;
+  if (a.group_max) return b1;
+  float v = b1, w = b2;
+  if (!SCORED) {
+    if (a.softmax) {
+      v = __builtin_amdgcn_exp2f((b1 - m) * LOG2E);
+      w = __builtin_amdgcn_exp2f((b2 - m) * LOG2E);
+    } else {
+      v = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(b1 * -LOG2E));
+      w = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(b2 * -LOG2E));
+    }
+  }
+  return b1 == -__builtin_inff() ? b1 : v + (b2 == -__builtin_inff() ? 0.0f : w);
+}
+
+// What the 32-bit choice of groups has to tell: how far the last chosen group
+// lies above the first left out, and whether more were taken than asked for
+// (equal values).
+struct GroupChoice {
+  float gap;
+  bool equal;
+};
+
+// Masks (-inf) the values of all but the top_groups best groups, where a group
+// is a power of two of chunks: the lanes of a group are neighbours in a row,
+// and log2 of their number of exchanges gives all groups' best two at once.
+template <int L, int C, bool SCORED>
+__device__ __forceinline__ GroupChoice keep_groups_pow2(const RouteArgs& a, float v[C][4], float m, int l) {
+  constexpr float NEG = -__builtin_inff();
+  const int chunks = a.E / a.n_groups / 4;           // a group's chunks
+  float b1[C], b2[C];
+#pragma unroll
+  for (int c = 0; c < C; c++) {
+    b1[c] = larger(v[c][0], v[c][1]);
+    b2[c] = -larger(-v[c][0], -v[c][1]);
+#pragma unroll
+    for (int i = 2; i < 4; i++) {
+      b2[c] = __builtin_amdgcn_fmed3f(b1[c], b2[c], v[c][i]);
+      b1[c] = larger(b1[c], v[c][i]);
+    }
+    if (chunks > 1) top2_lanes<DPP_XOR1>(b1[c], b2[c]);
+    if (chunks > 2) top2_lanes<DPP_XOR2>(b1[c], b2[c]);
+    if (chunks > 4) top2_lanes<DPP_HALF_MIRROR>(b1[c], b2[c]);
+    if (L == 16 && chunks > 8) top2_lanes<DPP_MIRROR>(b1[c], b2[c]);
+  }
+  if (chunks > L) {                        // a group of several rows of chunks
+    const int per = chunks / L;
+#pragma unroll
+    for (int c = 1; c < C; c++)
+      if (c & (per - 1)) top2(b1[c], b2[c], b1[c - 1], b2[c - 1]);
+#pragma unroll
+    for (int c = C - 2; c >= 0; c--)
+      if ((c + 1) & (per - 1)) b1[c] = b1[c + 1], b2[c] = b2[c + 1];
+  }
+  float g[C];
+  bool kept[C];
+#pragma unroll
+  for (int c = 0; c < C; c++) {
+    g[c] = group_value<SCORED>(a, b1[c], b2[c], m);
+    kept[c] = false;
+  }
+  float last = 0.0f, best = 0.0f;
+  for (int j = 0;; j++) {
+    last = best;
+    best = g[0];
+#pragma unroll
+    for (int c = 1; c < C; c++) best = larger(best, g[c]);
+    best = row_max<L>(best);
+    if (j == a.top_groups) break;
+#pragma unroll
+    for (int c = 0; c < C; c++) {
+      const bool hit = g[c] == best && best != NEG;
+      kept[c] |= hit;
+      g[c] = hit ? NEG : g[c];
+    }
+  }
+  int n = 0;
+#pragma unroll
+  for (int c = 0; c < C; c++) {
+    n += kept[c];
+#pragma unroll
+    for (int i = 0; i < 4; i++) v[c][i] = kept[c] ? v[c][i] : NEG;
+  }
+  GroupChoice r;
+  r.gap = last - best;
+  r.equal = row_sum<L>(n) > a.top_groups * chunks;
+  return r;
+}
+
+// The same for groups of any size, one after the other; lane l holds the
+// values of groups l, l + L, ...
+template <int L, int C, bool SCORED>
+__device__ __forceinline__ GroupChoice keep_groups(const RouteArgs& a, float v[C][4], float m, int l) {
+  constexpr float NEG = -__builtin_inff();
+  constexpr int R = ROUTE_MAX_GROUPS / L;
+  const int gs = a.E / a.n_groups;
+  float g[R];
+#pragma unroll
+  for (int r = 0; r < R; r++) g[r] = NEG;
+  for (int q = 0; q < a.n_groups; q++) {
+    float b1 = NEG, b2 = NEG;
+    const int lo = q * gs - 4 * l;
 #pragma unroll
     for (int c = 0; c < C; c++)
 #pragma unroll
       for (int i = 0; i < 4; i++) {
-        const int e = (c * ROUTE_LANES + l) * 4 + i;
-        const double v = e >= lo && e < hi ? key[c][i] : MX_NEG_INF;
-        b2 = fmax(b2, fmin(b1, v));
-        b1 = fmax(b1, v);
+        const float w = (unsigned)(c * L * 4 + i - lo) < (unsigned)gs ? v[c][i] : NEG;
+        b2 = __builtin_amdgcn_fmed3f(b1, b2, w);
+        b1 = larger(b1, w);
       }
-#define MX_TOP2(CTRL)                                       \
-  {                                                         \
-    const double o1 = dpp<CTRL>(b1), o2 = dpp<CTRL>(b2);    \
-    b2 = fmax(fmin(b1, o1), fmax(b2, o2));                  \
-    b1 = fmax(b1, o1);                                      \
-  }
-    MX_TOP2(DPP_XOR1) MX_TOP2(DPP_XOR2) MX_TOP2(DPP_HALF_MIRROR) MX_TOP2(DPP_MIRROR)
-#undef MX_TOP2
-    // a group with no unmasked expert stays at -inf
-    double v = key_value(b1);
-    if (!a.group_max && b2 != MX_NEG_INF) {
-      const bool nan = b1 < -1.65e308 || b2 < -1.65e308;
-      v = nan ? -1.7e308 : v + key_value(b2);
-    }
-    const double gkey = b1 == MX_NEG_INF ? MX_NEG_INF : make_key(v, g);
+    top2_lanes<DPP_XOR1>(b1, b2);
+    top2_lanes<DPP_XOR2>(b1, b2);
+    top2_lanes<DPP_HALF_MIRROR>(b1, b2);
+    if (L == 16) top2_lanes<DPP_MIRROR>(b1, b2);
+    const float value = group_value<SCORED>(a, b1, b2, m);
 #pragma unroll
-    for (int r = 0; r < ROUTE_MAX_GROUPS / ROUTE_LANES; r++)
-      if (g == r * ROUTE_LANES + l) gk[r] = gkey;
+    for (int r = 0; r < R; r++) g[r] = q == r * L + l ? value : g[r];
   }
+  const int row0 = (int)(threadIdx.x & 63) & ~(L - 1);
   uint32_t mask = 0;
-  for (int j = 0; j < a.top_groups; j++) {
-    double best = gk[0];
+  float last = 0.0f, best = 0.0f;
+  for (int j = 0;; j++) {
+    last = best;
+    best = g[0];
 #pragma unroll
-    for (int r = 1; r < ROUTE_MAX_GROUPS / ROUTE_LANES; r++) best = fmax(best, gk[r]);
-    best = row_max(best);
-    if (best != MX_NEG_INF) mask |= 1u << key_index(best);
+    for (int r = 1; r < R; r++) best = larger(best, g[r]);
+    best = row_max<L>(best);
+    if (j == a.top_groups) break;
 #pragma unroll
-    for (int r = 0; r < ROUTE_MAX_GROUPS / ROUTE_LANES; r++)
-      if (gk[r] == best) gk[r] = MX_NEG_INF;
+    for (int r = 0; r < R; r++) {
+      const bool hit = g[r] == best && best != NEG;
+      mask |= (uint32_t)(__ballot(hit) >> row0 & ((1u << L) - 1)) << (r * L);
+      g[r] = hit ? NEG : g[r];
+    }
   }
-  return mask;
-}
-
-// Descending list of the KC largest keys of the 16 lanes, in every lane.
-template <int C, int KC>
-__device__ __forceinline__ void top_keys(const double key[C][4], double top[KC]) {
-#pragma unroll
-  for (int j = 0; j < KC; j++) top[j] = MX_NEG_INF;
 #pragma unroll
   for (int c = 0; c < C; c++)
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      double v = key[c][i];
-#pragma unroll
-      for (int j = 0; j < KC; j++) {
-        const double hi = fmax(top[j], v);
-        v = fmin(top[j], v);
-        top[j] = hi;
-      }
+      const int q = ((c * L + l) * 4 + i) / gs;
+      v[c][i] = q < a.n_groups && (mask >> q & 1) ? v[c][i] : NEG;
     }
-  // two descending lists: the larger of a[j] and b[KC - 1 - j] are the KC
-  // largest of both, as a bitonic sequence; log2(KC) steps order it
-#define MX_MERGE(CTRL)                                                          \
-  {                                                                             \
-    double o[KC];                                                               \
-    _Pragma("unroll") for (int j = 0; j < KC; j++) o[j] = dpp<CTRL>(top[j]);    \
-    _Pragma("unroll") for (int j = 0; j < KC; j++)                              \
-      top[j] = fmax(top[j], o[KC - 1 - j]);                                     \
-    _Pragma("unroll") for (int d = KC / 2; d > 0; d >>= 1)                      \
-      _Pragma("unroll") for (int j = 0; j < KC; j++)                            \
-        if (!(j & d)) {                                                         \
-          const double hi = fmax(top[j], top[j + d]);                           \
-          top[j + d] = fmin(top[j], top[j + d]);                                \
-          top[j] = hi;                                                          \
-        }                                                                       \
-  }
-  MX_MERGE(DPP_XOR1) MX_MERGE(DPP_XOR2) MX_MERGE(DPP_HALF_MIRROR) MX_MERGE(DPP_MIRROR)
-#undef MX_MERGE
+  GroupChoice r;
+  r.gap = last - best;
+  r.equal = __popc(mask) > a.top_groups;
+  return r;
 }
 
-// One token of the 16 lanes: its experts and weights; returns lane l's choice
-// (-1: none, or l >= k).
-template <typename IN, int C, int KC, bool SCORED>
-__device__ __forceinline__ int route_token(const RouteArgs& a, int64_t t, bool live, int l) {
+// The 32-bit choice values of a lane's logits: the logits themselves, or with
+// a bias scores and bias, whose scores err bounds the error of:
+//   sigmoid: exp2 and reciprocal are off by one step each, the argument's
+//     rounding weighs s (1 - s) |x| < 0.23 steps, 1 + e half a step: under
+//     2^-22 for s <= 1; doubled.
+//   softmax: a score p <= 1 / sum is off by 1.5 |x - m| + 3 half steps from
+//     its exponential, where p |x - m| <= 1 / (e sum); its sum by as many on
+//     average (|x - m| averages under ln E + 1) and 4 C + 4 additions: under
+//     64 half steps of 1 / sum, 2^-18 / sum; doubled.
+// The scores of a group's best two logits (group_value): as these, with a sum
+// of 1.
+template <int L, int C, bool SCORED>
+__device__ __forceinline__ void choice_values(const RouteArgs& a, const float x[C][4], float m, int l,
+                                              float v[C][4], float& err) {
+  constexpr float NEG = -__builtin_inff();
+  constexpr float LOG2E = 1.44269504088896340736f;
+  if (!SCORED) {
+    err = 0x1p-21f;
+#pragma unroll
+    for (int c = 0; c < C; c++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) v[c][i] = x[c][i] + 0.0f;
+    return;
+  }
+  float b[C][4], inv = 1.0f;
+  load_row<float, L, C>(a.bias, a.E, a.vec_bias, l, true, b);
+  if (a.softmax) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; c++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        v[c][i] = __builtin_amdgcn_exp2f((x[c][i] - m) * LOG2E);
+        sum += v[c][i];
+      }
+    inv = __builtin_amdgcn_rcpf(row_sum<L>(sum));
+    err = 0x1p-17f * inv;
+  } else {
+#pragma unroll
+    for (int c = 0; c < C; c++)
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        v[c][i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x[c][i] * -LOG2E));
+    err = 0x1p-21f;
+  }
+#pragma unroll
+  for (int c = 0; c < C; c++)
+#pragma unroll
+    for (int i = 0; i < 4; i++) v[c][i] = x[c][i] == NEG ? NEG : fmaf(v[c][i], inv, b[c][i]);
+}
+
+// What the lanes know of a token once its experts are chosen.
+struct Choice {
+  double mine;     // lane l's chosen key, -inf for none
+  float m, sum;    // softmax: the row's largest logit and, where weights need it, its sum
+  bool nan;        // softmax: the row holds a NaN
+  bool again;      // the 32-bit values do not tell: choose from 64 bits
+};
+
+// The choice of one token from 32-bit values.
+// bias_max: the bias' largest magnitude, -inf aside; +inf with a NaN or +inf.
+template <typename IN, int L, int C, int KC, bool SCORED>
+__device__ __forceinline__ Choice choose(const RouteArgs& a, int64_t t, bool live, int l,
+                                         float bias_max) {
+  Choice r;
+  float x[C][4];
+  load_row<IN, L, C>((const IN*)a.logits + t * a.E, a.E, a.vec, l, live, x);
+  r.m = r.sum = 0.0f;
+  r.nan = false;
+  int odd = 0;                       // NaN and +inf take the 64-bit keys
+#pragma unroll
+  for (int c = 0; c < C; c++)
+#pragma unroll
+    for (int i = 0; i < 4; i++) odd |= !(x[c][i] <= 3.402823466e38f);
+  r.again = odd || (SCORED && !(bias_max < 1e30f));
+  if (a.softmax) {
+    r.m = -__builtin_inff();
+#pragma unroll
+    for (int c = 0; c < C; c++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) r.m = fmaxf(r.m, x[c][i]);   // passes over NaN
+    r.m = row_max<L>(r.m);
+    if (!a.renorm) {
+      float m = r.m;                 // kept here: the compiler would run the exponentials for every row
+      asm volatile("" : "+v"(m));
+#pragma unroll
+      for (int c = 0; c < C; c++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) r.sum += exp_diff(x[c][i], m);
+      r.sum = row_sum<L>(r.sum);
+    }
+  }
+
+  double key[C][4], top[KC];
+  float v[C][4], err;
+  choice_values<L, C, SCORED>(a, x, r.m, l, v, err);
+  const float near = 2.0f * (err + (1.0f + bias_max) * 0x1p-23f);  // twice the error of a value
+  if (a.n_groups > 1) {
+    const GroupChoice g = a.groups_pow2 ? keep_groups_pow2<L, C, SCORED>(a, v, r.m, l)
+                                        : keep_groups<L, C, SCORED>(a, v, r.m, l);
+    // sums of two values; the logits of single experts are exact
+    r.again |= g.equal || g.gap <= (!a.group_max ? 2.0f * near : SCORED ? near : 0.0f);
+  }
+#pragma unroll
+  for (int c = 0; c < C; c++) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) key[c][i] = make_key32(v[c][i], (c * L + l) * 4 + i);
+    sort4(key[c]);
+  }
+  top_keys<L, C, KC>(key, top);
+  if (SCORED) {
+    // chosen next to chosen, and the last of them next to the rest
+    double last = top[0];
+#pragma unroll
+    for (int j = 1; j < KC; j++) {
+      r.again |= j < a.k && top[j] != MX_NEG_INF && top[j - 1] - top[j] <= (double)near;
+      last = j < a.k ? top[j] : last;
+    }
+    const double edge = last - (double)near;
+    int at = 0;
+#pragma unroll
+    for (int c = 0; c < C; c++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) at += key[c][i] >= edge;
+    r.again |= last != MX_NEG_INF && row_sum<L>(at) != a.k;
+  }
+  r.mine = top[0];
+#pragma unroll
+  for (int j = 1; j < KC; j++) r.mine = l == j ? top[j] : r.mine;
+  r.mine = l < KC ? r.mine : MX_NEG_INF;
+  return r;
+}
+
+// Over all 64 lanes.
+template <typename F, typename T>
+__device__ __forceinline__ T wave_reduce(T v, F f) {
+  v = row_reduce<16>(v, f);
+  v = f(v, __shfl_xor(v, 16, 64));
+  return f(v, __shfl_xor(v, 32, 64));
+}
+template <typename T>
+__device__ __forceinline__ T wave_max(T v) {
+  return wave_reduce(v, [](T a, T b) { return larger(a, b); });
+}
+
+// The choice of one token by a whole wave from 64 bits, for the rows whose
+// 32-bit values do not tell: equal values fall to the lowest index, NaN below
+// every number.  It is seldom taken, but a workgroup waits for its last wave:
+// 64 lanes hold the row in two chunks each, so that no step repeats.  Every
+// lane gets the list.
+template <typename IN, int KC, bool SCORED>
+__device__ __forceinline__ void choose_exact(const RouteArgs& a, int64_t t, double top[KC], Choice& r) {
+  constexpr int L = 64, C = ROUTE_MAX_EXPERTS / (4 * L);
+  constexpr float NEG = -__builtin_inff();
+  int l = threadIdx.x & 63;
+  asm volatile("" : "+v"(l));            // nothing of this is kept for the tokens that do not need it
   const IN* row = (const IN*)a.logits + t * a.E;
   float x[C][4];
-  load_row<IN, C>(row, a.E, a.vec, l, live, x);
-
-  // the row's largest number, whether it holds a NaN, and softmax's sum
-  float m = -__builtin_inff();
+  load_row<IN, L, C>(row, a.E, a.vec, l, true, x);
+  float m = NEG;
   int nan = 0;
 #pragma unroll
   for (int c = 0; c < C; c++)
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      m = fmaxf(m, x[c][i]);
+      m = fmaxf(m, x[c][i]);             // passes over NaN
       nan |= x[c][i] != x[c][i];
     }
-  m = row_max(m);
-  nan = row_reduce(nan, [](int p, int q) { return p | q; });
+  r.m = m = wave_max(m);
+  r.nan = a.softmax && __any(nan);
+  r.sum = 0.0f;
 
-  double key[C][4];
-  float sum = 0.0f;
-  if (SCORED) {
-    double dsum = 1.0;
-    if (a.softmax) {
-      double part = 0.0;
+  // keys: logits without a bias, otherwise scores (softmax: z = exp(x - m),
+  // 1 for a logit at the largest, infinite ones among them, over their sum)
+  // and bias
+  double key[C][4], inv = 1.0;
+  if (a.softmax) {
+    double part = 0.0;
+#pragma unroll
+    for (int c = 0; c < C; c++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const double z = x[c][i] == m ? 1.0 : exp_64((double)x[c][i] - (double)m);
+        key[c][i] = z;
+        part += z == z && x[c][i] != NEG ? z : 0.0;
+      }
+    part = wave_reduce(part, [](double p, double q) { return p + q; });
+    r.sum = (float)part;
+    inv = rcp_64(fmax(part, 1.0));
+  } else if (SCORED) {
+#pragma unroll
+    for (int c = 0; c < C; c++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) key[c][i] = rcp_64(1.0 + exp_64(-(double)x[c][i]));
+  }
+  float b[C][4];
+  if (SCORED) load_row<float, L, C>(a.bias, a.E, a.vec_bias, l, true, b);
+#pragma unroll
+  for (int c = 0; c < C; c++)
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const double v = SCORED ? key[c][i] * inv + (double)b[c][i] : (double)x[c][i];
+      key[c][i] = x[c][i] == NEG || v == MX_NEG_INF ? MX_NEG_INF : make_key(v, (c * L + l) * 4 + i);
+    }
+
+  if (a.n_groups > 1) {
+    const int gs = a.E / a.n_groups;
+    double gk = MX_NEG_INF;              // lane q: the key of group q
+    for (int q = 0; q < a.n_groups; q++) {
+      double b1 = MX_NEG_INF, b2 = MX_NEG_INF;
 #pragma unroll
       for (int c = 0; c < C; c++)
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const double z = x[c][i] == m ? 1.0 : exp((double)x[c][i] - (double)m);
-          part += z == z ? z : 0.0;
+        for (int i = 0; i < 4; i++)
+          top2(b1, b2, (unsigned)((c * L + l) * 4 + i - q * gs) < (unsigned)gs ? key[c][i] : MX_NEG_INF,
+               MX_NEG_INF);
+      top2_lanes<DPP_XOR1>(b1, b2);
+      top2_lanes<DPP_XOR2>(b1, b2);
+      top2_lanes<DPP_HALF_MIRROR>(b1, b2);
+      top2_lanes<DPP_MIRROR>(b1, b2);
+      top2(b1, b2, __shfl_xor(b1, 16, 64), __shfl_xor(b2, 16, 64));
+      top2(b1, b2, __shfl_xor(b1, 32, 64), __shfl_xor(b2, 32, 64));
+      double v = key_value(b1), w = key_value(b2);
+      if (!a.group_max) {
+        const bool two = b2 != MX_NEG_INF;
+        const bool bad = b1 < -1.65e308 || (two && b2 < -1.65e308);   // NaN
+        if (!SCORED) {                                 // logits: score them
+          if (a.softmax) {
+            v = v >= m ? 1.0 : exp_64(v - m);
+            w = w >= m ? 1.0 : exp_64(w - m);
+          } else {
+            v = rcp_64(1.0 + exp_64(-v));
+            w = rcp_64(1.0 + exp_64(-w));
+          }
         }
-      dsum = 1.0 / row_sum(part);
+        v = bad ? -1.7e308 : v + (two ? w : 0.0);
+      }
+      if (l == q && b1 != MX_NEG_INF) gk = make_key(v, q);
+    }
+    uint32_t keep = 0;
+    for (int j = 0; j < a.top_groups; j++) {
+      const double best = wave_max(gk);
+      if (best != MX_NEG_INF) keep |= 1u << key_index(best);
+      if (gk == best) gk = MX_NEG_INF;
     }
 #pragma unroll
     for (int c = 0; c < C; c++)
 #pragma unroll
       for (int i = 0; i < 4; i++) {
-        const int e = (c * ROUTE_LANES + l) * 4 + i;
-        double v;
-        if (a.softmax)
-          v = (x[c][i] == m ? 1.0 : exp((double)x[c][i] - (double)m)) * dsum;
-        else
-          v = 1.0 / (1.0 + exp(-(double)x[c][i]));
-        if (a.bias && e < a.E) v += (double)a.bias[e];
-        key[c][i] = x[c][i] == -__builtin_inff() || v == MX_NEG_INF ? MX_NEG_INF : make_key(v, e);
-      }
-  } else {
-#pragma unroll
-    for (int c = 0; c < C; c++)
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const int e = (c * ROUTE_LANES + l) * 4 + i;
-        key[c][i] = x[c][i] == -__builtin_inff() ? MX_NEG_INF : make_key((double)x[c][i], e);
-      }
-  }
-  if (a.softmax && !a.renorm) {
-#pragma unroll
-    for (int c = 0; c < C; c++)
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const float z = exp_diff(x[c][i], m);
-        sum += z == z ? z : 0.0f;
-      }
-    sum = row_sum(sum);
-  }
-
-  if (a.n_groups > 1) {
-    const uint32_t keep = choose_groups<C>(a, key, l);
-    const int gs = a.E / a.n_groups;
-#pragma unroll
-    for (int c = 0; c < C; c++)
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const int g = ((c * ROUTE_LANES + l) * 4 + i) / gs;
-        if (g >= a.n_groups || !((keep >> g) & 1)) key[c][i] = MX_NEG_INF;
+        const int q = ((c * L + l) * 4 + i) / gs;
+        if (q >= a.n_groups || !(keep >> q & 1)) key[c][i] = MX_NEG_INF;
       }
   }
 
-  double top[KC];
-  top_keys<C, KC>(key, top);
-  double mine = top[0];
 #pragma unroll
-  for (int j = 1; j < KC; j++) mine = l == j ? top[j] : mine;
-  const bool has = live && l < a.k && l < KC && mine != MX_NEG_INF;
-  const int e = has ? key_index(mine) : -1;
+  for (int c = 0; c < C; c++) sort4(key[c]);
+  top_keys<16, C, KC>(key, top);         // of each row of 16 lanes
+#pragma unroll
+  for (int d = 16; d < 64; d <<= 1) {
+    double o[KC];
+#pragma unroll
+    for (int j = 0; j < KC; j++) o[j] = __shfl_xor(top[j], d, 64);
+    merge<KC, KC>(top, o);
+  }
+}
+
+// One token of L lanes: its experts and weights; returns lane l's choice
+// (-1: none, or l >= k).
+template <typename IN, int L, int C, int KC, bool SCORED>
+__device__ __forceinline__ int route_token(const RouteArgs& a, int64_t t, bool live, int l,
+                                           float bias_max) {
+  Choice r = choose<IN, L, C, KC, SCORED>(a, t, live, l, bias_max);
+  for (uint64_t todo = __ballot(live && r.again); todo != 0;) {
+    const int first = __ffsll((unsigned long long)todo) - 1, g = first / L;
+    todo &= ~(((1ull << L) - 1) << (g * L));
+    double top[KC];
+    Choice q;
+    choose_exact<IN, KC, SCORED>(a, __shfl(t, first, 64), top, q);
+    if ((int)(threadIdx.x & 63) / L == g) {
+      r.m = q.m, r.sum = q.sum, r.nan = q.nan;
+      r.mine = MX_NEG_INF;
+#pragma unroll
+      for (int j = 0; j < KC; j++) r.mine = l == j ? top[j] : r.mine;
+    }
+  }
+  const bool has = live && l < a.k && r.mine != MX_NEG_INF;
+  const int e = has ? key_index(r.mine) : -1;
 
   // the chosen scores; renormalised ones as ratios of terms that share a
   // factor, so that they hold where every chosen score underflows
-  const float xe = has ? load_logit(row + e) : -__builtin_inff();
+  const float xe = has ? load_logit((const IN*)a.logits + t * a.E + e) : -__builtin_inff();
   float w;
   if (a.renorm) {
-    const float big = row_max(xe);
+    const float big = row_reduce<L>(xe, [](float p, float q) { return fmaxf(p, q); });  // NaN aside
     float u;
     if (a.softmax) {
       u = exp_diff(xe, big);
@@ -343,11 +782,11 @@ __device__ __forceinline__ int route_token(const RouteArgs& a, int64_t t, bool l
       u = xe == -__builtin_inff() ? 0.0f : 1.0f / (expf(s) + expf(s - xe));
     }
     if (!has) u = 0.0f;
-    w = u / row_sum(u);
+    w = u / row_sum<L>(u);
   } else {
-    w = a.softmax ? exp_diff(xe, m) / sum : 1.0f / (1.0f + expf(-xe));
+    w = a.softmax ? exp_diff(xe, r.m) / r.sum : 1.0f / (1.0f + expf(-xe));
   }
-  if (a.softmax && nan) w = __builtin_nanf("");
+  if (r.nan) w = __builtin_nanf("");
   if (live && l < a.k) {
     a.weights[t * a.k + l] = has ? w * a.scale : 0.0f;
     a.experts[t * a.k + l] = e;
@@ -378,16 +817,21 @@ __device__ __forceinline__ void scan_experts(int* tot, int E) {
 // Rows of the choices [p0, p1) in the expert order: base[e] is the next free
 // row of expert e before them.  Wave w ranks 64 consecutive choices, equal
 // experts found by one ballot per bit of the expert's index.
+template <int THREADS>
 __device__ __forceinline__ void place_pairs(const int32_t* experts,
                                             int32_t* slots, int64_t p0, int64_t p1,
                                             int E, int* base, int* wave_cnt) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  constexpr int NW = ROUTE_THREADS / 64;
+  constexpr int NW = THREADS / 64;
   const int nbits = E > 1 ? 32 - __clz(E - 1) : 0;
-  for (int64_t q = p0; q < p1; q += ROUTE_THREADS) {
-    for (int i = threadIdx.x; i < NW * E; i += ROUTE_THREADS) wave_cnt[i] = 0;
-    __syncthreads();
+  for (int64_t q = p0; q < p1; q += THREADS) {
     const int64_t p = q + threadIdx.x;
+    const bool one = p1 - q <= 64;               // the first wave's alone: no counts to share
+    if (one && wave > 0) return;
+    if (!one) {
+      for (int i = threadIdx.x; i < NW * E; i += THREADS) wave_cnt[i] = 0;
+      __syncthreads();
+    }
     const int e = p < p1 ? experts[p] : -1;
     uint64_t same = __ballot(e >= 0);
     for (int b = 0; b < nbits; b++) {
@@ -395,9 +839,13 @@ __device__ __forceinline__ void place_pairs(const int32_t* experts,
       same &= (e >> b) & 1 ? set : ~set;
     }
     const int rank = __popcll(same & ((1ull << lane) - 1));
+    if (one) {
+      if (p < p1) slots[p] = e >= 0 ? base[e] + rank : -1;
+      return;
+    }
     if (e >= 0 && rank == 0) wave_cnt[wave * E + e] = __popcll(same);
     __syncthreads();
-    for (int x = threadIdx.x; x < E; x += ROUTE_THREADS) {
+    for (int x = threadIdx.x; x < E; x += THREADS) {
       int run = base[x];
       for (int w = 0; w < NW; w++) {
         const int n = wave_cnt[w * E + x];
@@ -414,65 +862,99 @@ __device__ __forceinline__ void place_pairs(const int32_t* experts,
 
 // Choices and weights of a workgroup's tokens and its count per expert; with
 // one workgroup, the expert order too.
-template <typename IN, int C, int KC, bool SCORED>
-__global__ void __launch_bounds__(ROUTE_THREADS) route_kernel(RouteArgs a) {
+template <typename IN, int L, int C, int KC, bool SCORED, int THREADS>
+__global__ void __launch_bounds__(THREADS) route_kernel(RouteArgs a) {
   __shared__ int cnt[ROUTE_MAX_EXPERTS + 1];
-  __shared__ int wave_cnt[ROUTE_THREADS / 64 * ROUTE_MAX_EXPERTS];
-  const int l = threadIdx.x & (ROUTE_LANES - 1);
-  for (int e = threadIdx.x; e < a.E; e += ROUTE_THREADS) cnt[e] = 0;
+  __shared__ int wave_cnt[THREADS / 64 * ROUTE_MAX_EXPERTS];
+  const int l = threadIdx.x & (L - 1);
+  for (int e = threadIdx.x; e < a.E; e += THREADS) cnt[e] = 0;
   __syncthreads();
   const int64_t t0 = (int64_t)blockIdx.x * a.tokens_per_block;
   const int64_t t1 = t0 + a.tokens_per_block < a.T ? t0 + a.tokens_per_block : a.T;
-  for (int64_t b = t0; b < t1; b += ROUTE_TOKENS) {
-    const int64_t t = b + threadIdx.x / ROUTE_LANES;
-    const int e = route_token<IN, C, KC, SCORED>(a, t < t1 ? t : t1 - 1, t < t1, l);
+  float bias_max = 0.0f;
+  if (SCORED) {
+    int odd = 0;
+    for (int e = l; e < a.E; e += L) {
+      const float b = a.bias[e];
+      odd |= !(b <= 3.402823466e38f);            // NaN or +inf
+      bias_max = fmaxf(bias_max, b == -__builtin_inff() ? 0.0f : fabsf(b));
+    }
+    bias_max = __any(odd) ? __builtin_inff() : row_max<L>(bias_max);
+  }
+  for (int64_t b = t0 + threadIdx.x / 64 * (64 / L); b < t1; b += THREADS / L) {
+    const int64_t t = b + (threadIdx.x & 63) / L;
+    // what follows from the lane alone (bounds, indices and groups of 4 C
+    // experts) would otherwise be kept across the loop, in more registers
+    // than there are
+    int lane = l;
+    asm volatile("" : "+v"(lane));
+    const int e = route_token<IN, L, C, KC, SCORED>(a, t < t1 ? t : t1 - 1, t < t1, lane, bias_max);
     if (e >= 0) atomicAdd(&cnt[e], 1);
   }
   __syncthreads();
   if (a.blocks > 1) {
-    for (int e = threadIdx.x; e < a.E; e += ROUTE_THREADS)
-      a.hist[(int64_t)blockIdx.x * a.E + e] = cnt[e];
+    // an expert's count is at most the workgroup's tokens: 16 bits
+    const int words = (a.E + 1) / 2;
+    for (int i = threadIdx.x; i < words; i += THREADS)
+      a.hist[(int64_t)blockIdx.x * words + i] =
+          (uint32_t)cnt[2 * i] | (2 * i + 1 < a.E ? (uint32_t)cnt[2 * i + 1] << 16 : 0u);
     return;
   }
   scan_experts(cnt, a.E);
   __syncthreads();
-  for (int e = threadIdx.x; e <= a.E; e += ROUTE_THREADS) a.offsets[e] = cnt[e];
-  __syncthreads();
-  place_pairs(a.experts, a.slots, t0 * a.k, t1 * a.k, a.E, cnt, wave_cnt);
+  for (int e = threadIdx.x; e <= a.E; e += THREADS) a.offsets[e] = cnt[e];
+  if (t1 * a.k > 64) __syncthreads();            // place_pairs moves the counts on
+  place_pairs<THREADS>(a.experts, a.slots, 0, t1 * a.k, a.E, cnt, wave_cnt);
 }
 
 // The expert order of workgroup b's choices: its base row per expert is the
 // expert's offset plus the counts of the workgroups before b.
-__global__ void __launch_bounds__(ROUTE_THREADS) route_place_kernel(RouteArgs a) {
+constexpr int PLACE_THREADS = 1024;
+__global__ void __launch_bounds__(PLACE_THREADS) route_place_kernel(RouteArgs a) {
   __shared__ int tot[ROUTE_MAX_EXPERTS + 1];
   __shared__ int base[ROUTE_MAX_EXPERTS];
-  __shared__ int wave_cnt[ROUTE_THREADS / 64 * ROUTE_MAX_EXPERTS];
-  for (int e = threadIdx.x; e < a.E; e += ROUTE_THREADS) tot[e] = base[e] = 0;
+  __shared__ int wave_cnt[PLACE_THREADS / 64 * ROUTE_MAX_EXPERTS];
+  for (int e = threadIdx.x; e < a.E; e += PLACE_THREADS) tot[e] = base[e] = 0;
   __syncthreads();
   const int b = blockIdx.x;
-  // thread = (segment of the workgroups, expert)
-  const int segs = ROUTE_THREADS / a.E;          // E <= 512: at least two
-  const int seg = (int)threadIdx.x / a.E, e = (int)threadIdx.x - seg * a.E;
+  // thread = (segment of the workgroups, two experts)
+  const int words = (a.E + 1) / 2;               // <= 256: four to 16 segments
+  const int segs = PLACE_THREADS / words < 16 ? PLACE_THREADS / words : 16;
+  const int seg = (int)threadIdx.x / words, i = (int)threadIdx.x - seg * words;
   if (seg < segs) {
-    int all = 0, before = 0;
-    for (int i = seg; i < a.blocks; i += segs) {
-      const int n = a.hist[(int64_t)i * a.E + e];
-      all += n;
-      before += i < b ? n : 0;
+    int all0 = 0, all1 = 0, before0 = 0, before1 = 0;
+    constexpr int BATCH = 16;                    // loads in flight: the counts come from other XCDs' L2
+    for (int w0 = seg; w0 < a.blocks; w0 += BATCH * segs) {
+      uint32_t n[BATCH];
+#pragma unroll
+      for (int u = 0; u < BATCH; u++) {
+        const int w = w0 + u * segs;
+        n[u] = w < a.blocks ? a.hist[(int64_t)w * words + i] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < BATCH; u++) {
+        const int n0 = (int)(n[u] & 0xFFFF), n1 = (int)(n[u] >> 16);
+        all0 += n0, all1 += n1;
+        before0 += w0 + u * segs < b ? n0 : 0, before1 += w0 + u * segs < b ? n1 : 0;
+      }
     }
-    atomicAdd(&tot[e], all);
-    atomicAdd(&base[e], before);
+    atomicAdd(&tot[2 * i], all0);
+    atomicAdd(&base[2 * i], before0);
+    if (2 * i + 1 < a.E) {
+      atomicAdd(&tot[2 * i + 1], all1);
+      atomicAdd(&base[2 * i + 1], before1);
+    }
   }
   __syncthreads();
   scan_experts(tot, a.E);
   __syncthreads();
-  for (int x = threadIdx.x; x < a.E; x += ROUTE_THREADS) base[x] += tot[x];
+  for (int x = threadIdx.x; x < a.E; x += PLACE_THREADS) base[x] += tot[x];
   if (b == 0)
-    for (int x = threadIdx.x; x <= a.E; x += ROUTE_THREADS) a.offsets[x] = tot[x];
+    for (int x = threadIdx.x; x <= a.E; x += PLACE_THREADS) a.offsets[x] = tot[x];
   __syncthreads();
   const int64_t t0 = (int64_t)b * a.tokens_per_block;
   const int64_t t1 = t0 + a.tokens_per_block < a.T ? t0 + a.tokens_per_block : a.T;
-  place_pairs(a.experts, a.slots, t0 * a.k, t1 * a.k, a.E, base, wave_cnt);
+  place_pairs<PLACE_THREADS>(a.experts, a.slots, t0 * a.k, t1 * a.k, a.E, base, wave_cnt);
 }
 
 // ---------------------------------------------------------------------------
@@ -496,8 +978,9 @@ struct RouteBackwardArgs {
 
 template <typename IN, int C>
 __global__ void __launch_bounds__(256) route_backward_kernel(RouteBackwardArgs a) {
-  const int l = threadIdx.x & (ROUTE_LANES - 1);
-  const int64_t t = ((int64_t)blockIdx.x * 256 + threadIdx.x) / ROUTE_LANES;
+  constexpr int L = 16;
+  const int l = threadIdx.x & (L - 1);
+  const int64_t t = ((int64_t)blockIdx.x * 256 + threadIdx.x) / L;
   const bool live = t < a.T;
   const int64_t tt = live ? t : a.T - 1;
   const IN* row = (const IN*)a.logits + tt * a.E;
@@ -511,7 +994,7 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteBackwardArgs a
   float m = -__builtin_inff(), sum = 0.0f;
   float d = 0.0f, dot = 0.0f;                  // lane l's choice's own term; the row's common term
   if (dense) {
-    load_row<IN, C>(row, a.E, a.vec, l, true, x);
+    load_row<IN, L, C>(row, a.E, a.vec, l, true, x);
     int nan = 0;
 #pragma unroll
     for (int c = 0; c < C; c++)
@@ -520,8 +1003,8 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteBackwardArgs a
         m = fmaxf(m, x[c][i]);
         nan |= x[c][i] != x[c][i];
       }
-    m = row_max(m);
-    nan = row_reduce(nan, [](int p, int q) { return p | q; });
+    m = row_max<L>(m);
+    nan = row_reduce<L>(nan, [](int p, int q) { return p | q; });
 #pragma unroll
     for (int c = 0; c < C; c++)
 #pragma unroll
@@ -529,7 +1012,7 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteBackwardArgs a
         x[c][i] = x[c][i] == -__builtin_inff() ? 0.0f : exp_diff(x[c][i], m);
         sum += x[c][i];
       }
-    sum = row_sum(sum);
+    sum = row_sum<L>(sum);
     const float inv = sum > 0.0f || nan ? 1.0f / sum : 0.0f;   // a row of masked experts: no gradient
 #pragma unroll
     for (int c = 0; c < C; c++)
@@ -537,9 +1020,9 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteBackwardArgs a
       for (int i = 0; i < 4; i++) x[c][i] *= inv;
     const float p = has && xe != -__builtin_inff() ? exp_diff(xe, m) * inv : 0.0f;
     d = has ? a.scale * g * p : 0.0f;
-    dot = row_sum(d);
+    dot = row_sum<L>(d);
   } else if (a.renorm) {
-    const float big = row_max(xe);
+    const float big = row_max<L>(xe);
     float u = 0.0f;
     if (has && xe != -__builtin_inff()) {
       if (a.softmax) {
@@ -549,9 +1032,9 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteBackwardArgs a
         u = 1.0f / (expf(s) + expf(s - xe));
       }
     }
-    const float S = row_sum(u);
+    const float S = row_sum<L>(u);
     const float aj = S == 0.0f ? 0.0f : u / S;
-    const float G = row_sum(g * aj);
+    const float G = row_sum<L>(g * aj);
     d = a.scale * aj * (g - G);
     if (!a.softmax) d *= 1.0f / (1.0f + expf(xe));
   } else {
@@ -565,7 +1048,7 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteBackwardArgs a
   for (int c = 0; c < C; c++)
 #pragma unroll
     for (int i = 0; i < 4; i++) out[c][i] = dense ? -x[c][i] * dot : 0.0f;
-  const int lane0 = (int)(threadIdx.x & 63) & ~(ROUTE_LANES - 1);
+  const int lane0 = (int)(threadIdx.x & 63) & ~(L - 1);
   for (int j = 0; j < a.k; j++) {
     const int ej = __shfl(e, lane0 + j, 64);
     const float dj = __shfl(d, lane0 + j, 64);
@@ -573,13 +1056,13 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteBackwardArgs a
     for (int c = 0; c < C; c++)
 #pragma unroll
       for (int i = 0; i < 4; i++)
-        out[c][i] += (c * ROUTE_LANES + l) * 4 + i == ej ? dj : 0.0f;
+        out[c][i] += (c * L + l) * 4 + i == ej ? dj : 0.0f;
   }
   if (!live) return;
   IN* dst = (IN*)a.dlogits + t * a.E;
 #pragma unroll
   for (int c = 0; c < C; c++) {
-    const int e0 = (c * ROUTE_LANES + l) * 4;
+    const int e0 = (c * L + l) * 4;
     if (a.vec) {
       if (e0 < a.E) store_logit4(dst + e0, out[c]);
     } else {
@@ -597,6 +1080,7 @@ static void route_split(int64_t T, int* blocks, int* tokens_per_block) {
   int64_t per = (T + ROUTE_MAX_BLOCKS - 1) / ROUTE_MAX_BLOCKS;
   per = (per + ROUTE_TOKENS - 1) / ROUTE_TOKENS * ROUTE_TOKENS;
   if (per < ROUTE_TOKENS) per = ROUTE_TOKENS;
+  if (per > 32768) per = 32768;                  // counts of 16 bits
   *tokens_per_block = (int)per;
   *blocks = (int)((T + per - 1) / per);
 }
@@ -604,27 +1088,41 @@ static void route_split(int64_t T, int* blocks, int* tokens_per_block) {
 size_t route_workspace(int64_t T, int64_t E) {
   int blocks, per;
   route_split(T, &blocks, &per);
-  return blocks > 1 ? sizeof(int32_t) * (size_t)blocks * (size_t)E : 0;
+  return blocks > 1 ? sizeof(uint32_t) * (size_t)blocks * (size_t)((E + 1) / 2) : 0;
 }
 
-template <typename IN, int C, int KC>
-static void launch_route_kc(bool scored, const RouteArgs& a, hipStream_t stream) {
-  if (scored)
-    hipLaunchKernelGGL((route_kernel<IN, C, KC, true>), dim3(a.blocks), dim3(ROUTE_THREADS), 0, stream, a);
+// Threads by registers: 1024 leave 128 to each, 768 170, 512 256.  Up to 16
+// tokens, 256.
+template <typename IN, int L, int C, int KC, bool SCORED, int THREADS>
+static void launch_route_threads(const RouteArgs& a, hipStream_t stream) {
+  if (a.T <= 16)
+    hipLaunchKernelGGL((route_kernel<IN, L, C, KC, SCORED, 256>), dim3(1), dim3(256), 0, stream, a);
   else
-    hipLaunchKernelGGL((route_kernel<IN, C, KC, false>), dim3(a.blocks), dim3(ROUTE_THREADS), 0, stream, a);
+    hipLaunchKernelGGL((route_kernel<IN, L, C, KC, SCORED, THREADS>), dim3(a.blocks), dim3(THREADS), 0,
+                       stream, a);
 }
-template <typename IN, int C>
-static void launch_route_c(bool scored, const RouteArgs& a, hipStream_t stream) {
-  if (a.k <= 8) launch_route_kc<IN, C, 8>(scored, a, stream);
-  else launch_route_kc<IN, C, 16>(scored, a, stream);
+template <typename IN, int L, int C, int KC>
+static void launch_route_lanes(bool scored, const RouteArgs& a, hipStream_t stream) {
+  constexpr int SCORED_THREADS = C <= 4 ? 1024 : L == 8 ? 768 : 512;
+  if (scored) launch_route_threads<IN, L, C, KC, true, SCORED_THREADS>(a, stream);
+  else launch_route_threads<IN, L, C, KC, false, 1024>(a, stream);
 }
+// Lanes to a token: eight, where they hold its logits (32 each) and its
+// choices; merging lists of lanes is most of the work, and eight lanes take
+// one step less of it for twice the tokens of a wave.
 template <typename IN>
 static void launch_route_in(bool scored, const RouteArgs& a, hipStream_t stream) {
-  if (a.E <= 64) launch_route_c<IN, 1>(scored, a, stream);
-  else if (a.E <= 128) launch_route_c<IN, 2>(scored, a, stream);
-  else if (a.E <= 256) launch_route_c<IN, 4>(scored, a, stream);
-  else launch_route_c<IN, 8>(scored, a, stream);
+  if (a.k <= 8) {
+    if (a.E <= 64) launch_route_lanes<IN, 8, 2, 8>(scored, a, stream);
+    else if (a.E <= 128) launch_route_lanes<IN, 8, 4, 8>(scored, a, stream);
+    else if (a.E <= 256) launch_route_lanes<IN, 8, 8, 8>(scored, a, stream);
+    else launch_route_lanes<IN, 16, 8, 8>(scored, a, stream);
+  } else {
+    if (a.E <= 64) launch_route_lanes<IN, 16, 1, 16>(scored, a, stream);
+    else if (a.E <= 128) launch_route_lanes<IN, 16, 2, 16>(scored, a, stream);
+    else if (a.E <= 256) launch_route_lanes<IN, 16, 4, 16>(scored, a, stream);
+    else launch_route_lanes<IN, 16, 8, 16>(scored, a, stream);
+  }
 }
 
 hipError_t launch_route(int softmax, int f32, const void* logits, const float* bias, int64_t T,
@@ -636,22 +1134,25 @@ hipError_t launch_route(int softmax, int f32, const void* logits, const float* b
   a.n_groups = (int)n_groups, a.top_groups = (int)top_groups, a.group_max = group_max;
   a.softmax = softmax, a.renorm = renorm, a.scale = scale;
   a.weights = weights, a.experts = experts, a.offsets = offsets, a.slots = slots;
-  a.hist = (int32_t*)workspace;
+  a.hist = (uint32_t*)workspace;
   // four logits at once where every row starts on their alignment
   a.vec = E % 4 == 0 && ((uintptr_t)logits & (f32 ? 15 : 7)) == 0;
+  const int64_t chunks = E / n_groups / 4;
+  a.groups_pow2 = n_groups > 1 && E % (4 * n_groups) == 0 && (chunks & (chunks - 1)) == 0;
   route_split(T, &a.blocks, &a.tokens_per_block);
-  const bool scored = bias != nullptr || (n_groups > 1 && !group_max);
+  a.vec_bias = E % 4 == 0 && ((uintptr_t)bias & 15) == 0;
+  const bool scored = bias != nullptr;
   if (f32) launch_route_in<float>(scored, a, stream);
   else launch_route_in<uint16_t>(scored, a, stream);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.blocks == 1) return e;
-  hipLaunchKernelGGL(route_place_kernel, dim3(a.blocks), dim3(ROUTE_THREADS), 0, stream, a);
+  hipLaunchKernelGGL(route_place_kernel, dim3(a.blocks), dim3(PLACE_THREADS), 0, stream, a);
   return hipGetLastError();
 }
 
 template <typename IN>
 static void launch_route_backward_in(const RouteBackwardArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)((a.T * ROUTE_LANES + 255) / 256));
+  const dim3 grid((unsigned)((a.T * 16 + 255) / 256));
   if (a.E <= 64) hipLaunchKernelGGL((route_backward_kernel<IN, 1>), grid, dim3(256), 0, stream, a);
   else if (a.E <= 128) hipLaunchKernelGGL((route_backward_kernel<IN, 2>), grid, dim3(256), 0, stream, a);
   else if (a.E <= 256) hipLaunchKernelGGL((route_backward_kernel<IN, 4>), grid, dim3(256), 0, stream, a);

@@ -32,22 +32,24 @@ def _order(v):
 def choose(x, k, score, bias=None, n_groups=1, top_groups=1, group_value="top2"):
     """experts [T, k], -1 where none is left."""
     T, E = x.shape
-    v = scores(x, score)
-    if bias is None and (n_groups == 1 or group_value == "max"):
-        v = x.copy()                   # the same order, without the scores' rounding
+    # without a bias experts are in their logits' order, which the scores keep
+    v = np.where(np.isneginf(x), NEG, x)
+    value = scores(x, score)
     if bias is not None:
         with np.errstate(all="ignore"):
-            v = v + bias
-    v = np.where(np.isneginf(x), NEG, v)
+            v = value = np.where(np.isneginf(x), NEG, value + bias)
     if n_groups > 1:
         by = v.reshape(T * n_groups, E // n_groups)
         o = _order(by)
         best = np.take_along_axis(by, o[:, :1], 1)[:, 0]
         val = best
-        if E // n_groups > 1 and group_value == "top2":
-            second = np.take_along_axis(by, o[:, 1:2], 1)[:, 0]
-            with np.errstate(all="ignore"):
-                val = np.where(np.isneginf(second), best, best + second)
+        if group_value == "top2":
+            vals = np.where(np.isneginf(v), NEG, value).reshape(by.shape)
+            val = np.take_along_axis(vals, o[:, :1], 1)[:, 0]
+            if E // n_groups > 1:
+                second = np.take_along_axis(vals, o[:, 1:2], 1)[:, 0]
+                with np.errstate(all="ignore"):
+                    val = np.where(np.isneginf(second), val, val + second)
         rank = np.argsort(_order(val.reshape(T, n_groups)), axis=1)
         v = np.where(np.repeat(rank < top_groups, E // n_groups, axis=1), v, NEG)
     o = _order(v)[:, :k]
