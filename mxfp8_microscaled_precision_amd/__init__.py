@@ -798,7 +798,7 @@ def grad_norm(tensors):
     FP32 tensor on the device."""
     tensors = list(tensors)
     n, ptrs, sizes, codes = _tensor_list(tensors)
-    device = tensors[0].device if tensors else "cuda"
+    device = tensors[0].device if tensors else _torch().device("cuda")
     norm, ws, nws = _norm_buffers(n, device)
     _check(mx_grad_norm(n, ptrs, sizes, codes, _ptr(norm), _ptr(ws), nws, _stream(device)))
     return norm
@@ -810,7 +810,7 @@ def grad_clip(tensors, max_norm: float):
     0-d FP32 tensor on the device.  Tensors of the list must not overlap."""
     tensors = list(tensors)
     n, ptrs, sizes, codes = _tensor_list(tensors)
-    device = tensors[0].device if tensors else "cuda"
+    device = tensors[0].device if tensors else _torch().device("cuda")
     norm, ws, nws = _norm_buffers(n, device)
     _check(mx_grad_clip(n, ptrs, sizes, codes, max_norm, _ptr(norm), _ptr(ws), nws, _stream(device)))
     return norm

@@ -92,6 +92,23 @@ def test_bias_decides_and_weights_do_not_see_it(score):
     assert not (host(r.experts) == 3).any()
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups", [(64, 8, 1), (256, 8, 8), (60, 16, 4), (512, 8, 1)])
+def test_values_closer_than_32_bits(score, E, k, groups):
+    """Biases that bring all choice values within a few 2^-25 of each other:
+    only 64-bit values order them."""
+    rng = np.random.default_rng(E)
+    x = torch.from_numpy(rng.normal(size=E).astype(np.float32)).repeat(40, 1)
+    s = P.scores(x[:1].double().numpy(), score)[0]
+    bias = torch.from_numpy((0.75 - s).astype(np.float32))
+    perm = torch.from_numpy(np.stack([rng.permutation(E) for _ in range(40)]))
+    _check(x, k, score, bias, groups, max(1, groups // 2))
+    # rows of which only some are close, among ordinary ones
+    y = torch.gather(x, 1, perm)
+    y[::3] = x[::3]
+    _check(y, k, score, bias, groups, max(1, groups // 2))
+
+
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 @pytest.mark.parametrize("bias", [False, True])
 def test_ties_go_to_the_lowest_index(dtype, bias):
