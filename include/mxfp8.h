@@ -415,7 +415,7 @@ mx_status mx_combine_backward(const void* dout, const void* y, int64_t T, int64_
  * added in 64 bits in a fixed order and rounded once.  tensors, numels and
  * dtypes are HOST arrays of n device pointers, element counts and element
  * types; they are read during the call only.  workspace: DEVICE scratch of
- * mx_grad_norm_workspace_size(n) bytes.  Requires fewer than 2^45 bytes in
+ * mx_grad_norm_workspace_size(n) bytes.  Requires fewer than 2^42 bytes in
  * all.  n == 0 gives norm 0. */
 mx_status mx_grad_norm(int64_t n, const void* const* tensors, const int64_t* numels,
                        const mx_dtype* dtypes, float* norm, void* workspace,

@@ -120,8 +120,8 @@ mx_status check_tensors(int64_t n, const void* const* tensors, const int64_t* nu
     const uintptr_t size = dtypes[i] == MX_DTYPE_F32 ? 4 : 2;
     if (numels[i] > 0 && (uintptr_t)tensors[i] % size != 0)
       return fail(MX_ERR_INVALID_ARG, "tensor %lld is not aligned to its elements", (long long)i);
-    if (numels[i] >= (int64_t(1) << 45) || (bytes += numels[i] * (int64_t)size) >= (int64_t(1) << 45))
-      return fail(MX_ERR_UNSUPPORTED_SHAPE, "the tensors hold 2^45 bytes or more");
+    if (numels[i] >= (int64_t(1) << 42) || (bytes += numels[i] * (int64_t)size) >= (int64_t(1) << 42))
+      return fail(MX_ERR_UNSUPPORTED_SHAPE, "the tensors hold 2^42 bytes or more");
   }
   if (!apart || n < 2) return MX_OK;
   struct Span {

@@ -37,6 +37,7 @@ struct GradPiece {
   int n;
   bool f32, vec;
 };
+template <int BYTES>
 __device__ __forceinline__ GradPiece grad_piece(const GradTable& a, int piece) {
   int lo = 0, hi = a.count - 1;
   while (lo < hi) {
@@ -46,7 +47,7 @@ __device__ __forceinline__ GradPiece grad_piece(const GradTable& a, int piece) {
   }
   GradPiece g;
   g.f32 = a.t[lo].f32 != 0;
-  const int per = g.f32 ? GRAD_PIECE / 4 : GRAD_PIECE / 2;
+  const int per = g.f32 ? BYTES / 4 : BYTES / 2;
   const int64_t at = (int64_t)(piece - a.t[lo].first) * per;
   const int64_t left = a.t[lo].n - at;
   g.n = left < per ? (int)left : per;
@@ -60,6 +61,41 @@ __device__ __forceinline__ double square(float f, double acc) {
   return fma(d, d, acc);
 }
 __device__ __forceinline__ float bf_of(uint32_t bits) { return __uint_as_float(bits << 16); }
+
+__device__ __forceinline__ double square4(uint4 v, bool f32, double acc) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    if (f32) {
+      acc = square(__uint_as_float(w[i]), acc);
+    } else {
+      acc = square(__uint_as_float(w[i] << 16), acc);
+      acc = square(__uint_as_float(w[i] & 0xFFFF0000u), acc);
+    }
+  }
+  return acc;
+}
+
+// The coefficient stays in 64 bits: a norm past FP32's range has one that
+// FP32 holds with few bits or none.
+__device__ __forceinline__ float scaled(float g, double coef) { return (float)((double)g * coef); }
+__device__ __forceinline__ uint4 scaled4(uint4 v, bool f32, double coef) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; i++)
+    w[i] = f32 ? __float_as_uint(scaled(__uint_as_float(w[i]), coef))
+               : cvt_pk_bf16(scaled(__uint_as_float(w[i] << 16), coef),
+                             scaled(__uint_as_float(w[i] & 0xFFFF0000u), coef));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void scale1(char* p, int i, bool f32, double coef) {
+  if (f32) {
+    ((float*)p)[i] = scaled(((const float*)p)[i], coef);
+  } else {
+    const float f = scaled(bf_of(((const uint16_t*)p)[i]), coef);
+    ((uint16_t*)p)[i] = (uint16_t)cvt_pk_bf16(f, f);
+  }
+}
 
 // Sum over a workgroup, in every thread, in a fixed order.
 __device__ __forceinline__ double block_sum(double v, double* part) {
@@ -77,7 +113,7 @@ __global__ void __launch_bounds__(GRAD_THREADS) grad_square_kernel(GradTable a, 
   __shared__ double part[GRAD_THREADS / 64];
   double acc = 0.0;
   for (int piece = blockIdx.x; piece < a.pieces; piece += gridDim.x) {
-    const GradPiece g = grad_piece(a, piece);
+    const GradPiece g = grad_piece<GRAD_PIECE>(a, piece);
     const int each = g.f32 ? 4 : 8, whole = g.vec ? g.n / each : 0;
     uint4 v[GRAD_LOADS];
 #pragma unroll
@@ -86,18 +122,7 @@ __global__ void __launch_bounds__(GRAD_THREADS) grad_square_kernel(GradTable a, 
       v[u] = i < whole ? load_stream16((const uint4*)g.p + i) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int u = 0; u < GRAD_LOADS; u++) {
-      const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        if (g.f32) {
-          acc = square(__uint_as_float(w[i]), acc);
-        } else {
-          acc = square(__uint_as_float(w[i] << 16), acc);
-          acc = square(__uint_as_float(w[i] & 0xFFFF0000u), acc);
-        }
-      }
-    }
+    for (int u = 0; u < GRAD_LOADS; u++) acc = square4(v[u], g.f32, acc);
     for (int i = whole * each + threadIdx.x; i < g.n; i += GRAD_THREADS)
       acc = square(g.f32 ? ((const float*)g.p)[i] : bf_of(((const uint16_t*)g.p)[i]), acc);
   }
@@ -105,15 +130,61 @@ __global__ void __launch_bounds__(GRAD_THREADS) grad_square_kernel(GradTable a, 
   if (threadIdx.x == 0) sums[blockIdx.x] = s;
 }
 
+// Short lists: one workgroup sums and scales in a single launch, a wave to a
+// piece, of 4 KiB here.  CLIP as below.
+constexpr int GRAD_SHORT_THREADS = 1024;
+constexpr int GRAD_SHORT_PIECE = 4096;
+template <bool CLIP>
+__global__ void __launch_bounds__(GRAD_SHORT_THREADS)
+grad_short_kernel(GradTable a, float max_norm, float* norm) {
+  constexpr int WAVES = GRAD_SHORT_THREADS / 64, LOADS = GRAD_SHORT_PIECE / 16 / 64;
+  __shared__ double part[WAVES];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  double acc = 0.0;
+  for (int piece = wave; piece < a.pieces; piece += WAVES) {
+    const GradPiece g = grad_piece<GRAD_SHORT_PIECE>(a, piece);
+    const int each = g.f32 ? 4 : 8, whole = g.vec ? g.n / each : 0;
+    uint4 v[LOADS];
+#pragma unroll
+    for (int u = 0; u < LOADS; u++)
+      v[u] = lane + 64 * u < whole ? ((const uint4*)g.p)[lane + 64 * u] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int u = 0; u < LOADS; u++) acc = square4(v[u], g.f32, acc);
+    for (int i = whole * each + lane; i < g.n; i += 64)
+      acc = square(g.f32 ? ((const float*)g.p)[i] : bf_of(((const uint16_t*)g.p)[i]), acc);
+  }
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) acc += __shfl_xor(acc, m, 64);
+  if (lane == 0) part[wave] = acc;
+  __syncthreads();
+  double sum = 0.0;
+#pragma unroll
+  for (int w = 0; w < WAVES; w++) sum += part[w];
+  const double total = sqrt(sum);
+  if (threadIdx.x == 0) *norm = (float)total;
+  if (!CLIP) return;
+  const double coef = (double)max_norm / (total + 1e-6);
+  if (coef >= 1.0) return;                     // nothing to scale; a NaN goes on
+  for (int piece = wave; piece < a.pieces; piece += WAVES) {
+    const GradPiece g = grad_piece<GRAD_SHORT_PIECE>(a, piece);
+    const int each = g.f32 ? 4 : 8, whole = g.vec ? g.n / each : 0;
+    uint4 v[LOADS];
+#pragma unroll
+    for (int u = 0; u < LOADS; u++)
+      v[u] = lane + 64 * u < whole ? ((const uint4*)g.p)[lane + 64 * u] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int u = 0; u < LOADS; u++)
+      if (lane + 64 * u < whole) ((uint4*)g.p)[lane + 64 * u] = scaled4(v[u], g.f32, coef);
+    for (int i = whole * each + lane; i < g.n; i += 64) scale1(g.p, i, g.f32, coef);
+  }
+}
+
 __device__ __forceinline__ double total_norm(const double* sums, int n, double* part) {
   double v = 0.0;
   for (int i = threadIdx.x; i < n; i += GRAD_THREADS) v += sums[i];
   return sqrt(block_sum(v, part));
 }
-
-// The coefficient stays in 64 bits: a norm past FP32's range has one that
-// FP32 holds with few bits or none.
-__device__ __forceinline__ float scaled(float g, double coef) { return (float)((double)g * coef); }
 
 __global__ void __launch_bounds__(GRAD_THREADS)
 grad_norm_kernel(const double* sums, int n, float* norm) {
@@ -129,8 +200,9 @@ grad_scale_kernel(GradTable a, const double* sums, int n, float max_norm, float*
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)v;
   const double coef = (double)max_norm / (v + 1e-6);
   if (coef >= 1.0) return;                    // nothing to scale; a NaN goes on
-  for (int piece = blockIdx.x; piece < a.pieces; piece += gridDim.x) {
-    const GradPiece g = grad_piece(a, piece);
+  // the pieces that were read last come first: they are still in the caches
+  for (int at = blockIdx.x; at < a.pieces; at += gridDim.x) {
+    const GradPiece g = grad_piece<GRAD_PIECE>(a, a.pieces - 1 - at);
     const int each = g.f32 ? 4 : 8, whole = g.vec ? g.n / each : 0;
     uint4 v4[GRAD_LOADS];
 #pragma unroll
@@ -141,23 +213,10 @@ grad_scale_kernel(GradTable a, const double* sums, int n, float max_norm, float*
 #pragma unroll
     for (int u = 0; u < GRAD_LOADS; u++) {
       const int i = u * GRAD_THREADS + threadIdx.x;
-      uint32_t w[4] = {v4[u].x, v4[u].y, v4[u].z, v4[u].w};
-#pragma unroll
-      for (int j = 0; j < 4; j++)
-        w[j] = g.f32 ? __float_as_uint(scaled(__uint_as_float(w[j]), coef))
-                     : cvt_pk_bf16(scaled(__uint_as_float(w[j] << 16), coef),
-                                   scaled(__uint_as_float(w[j] & 0xFFFF0000u), coef));
-      if (i < whole) ((uint4*)g.p)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      const uint4 w = scaled4(v4[u], g.f32, coef);
+      if (i < whole) ((uint4*)g.p)[i] = w;
     }
-    for (int i = whole * each + threadIdx.x; i < g.n; i += GRAD_THREADS) {
-      if (g.f32) {
-        ((float*)g.p)[i] = scaled(((const float*)g.p)[i], coef);
-      } else {
-        uint16_t* p = (uint16_t*)g.p + i;
-        const float f = scaled(bf_of(*p), coef);
-        *p = (uint16_t)cvt_pk_bf16(f, f);
-      }
-    }
+    for (int i = whole * each + threadIdx.x; i < g.n; i += GRAD_THREADS) scale1(g.p, i, g.f32, coef);
   }
 }
 
@@ -169,12 +228,12 @@ grad_scale_kernel(GradTable a, const double* sums, int n, float max_norm, float*
 // the next tensor.  Empty tensors are left out.  The caller bounds the list's
 // bytes so that pieces are numbered in 32 bits.
 static int64_t grad_table(int64_t i0, int64_t n, void* const* tensors, const int64_t* numels,
-                          const int* f32, GradTable* a) {
+                          const int* f32, int bytes, GradTable* a) {
   a->count = 0;
   int64_t pieces = 0, i = i0;
   for (; i < n && a->count < GRAD_TENSORS; i++) {
     if (numels[i] == 0) continue;
-    const int64_t per = f32[i] ? GRAD_PIECE / 4 : GRAD_PIECE / 2;
+    const int64_t per = f32[i] ? bytes / 4 : bytes / 2;
     GradTensor& t = a->t[a->count++];
     t.p = tensors[i], t.n = numels[i], t.first = (int32_t)pieces, t.f32 = f32[i];
     pieces += (numels[i] + per - 1) / per;
@@ -182,6 +241,8 @@ static int64_t grad_table(int64_t i0, int64_t n, void* const* tensors, const int
   a->pieces = (int)pieces;
   return i;
 }
+
+constexpr int GRAD_SHORT_PIECES = 32;
 
 static int grad_grid(const GradTable& a) { return a.pieces < GRAD_BLOCKS ? a.pieces : GRAD_BLOCKS; }
 
@@ -195,20 +256,29 @@ hipError_t launch_grad(int64_t n, void* const* tensors, const int64_t* numels, c
   double* sums = (double*)workspace;
   int filled = 0;
   GradTable a;
+  if (grad_table(0, n, tensors, numels, f32, GRAD_SHORT_PIECE, &a) == n && a.pieces <= GRAD_SHORT_PIECES) {
+    if (clip)
+      hipLaunchKernelGGL(grad_short_kernel<true>, dim3(1), dim3(GRAD_SHORT_THREADS), 0, stream, a,
+                         max_norm, norm);
+    else
+      hipLaunchKernelGGL(grad_short_kernel<false>, dim3(1), dim3(GRAD_SHORT_THREADS), 0, stream, a,
+                         max_norm, norm);
+    return hipGetLastError();
+  }
   for (int64_t i = 0; i < n;) {
-    i = grad_table(i, n, tensors, numels, f32, &a);
+    i = grad_table(i, n, tensors, numels, f32, GRAD_PIECE, &a);
     if (a.count == 0) break;
     const int grid = grad_grid(a);
     hipLaunchKernelGGL(grad_square_kernel, dim3(grid), dim3(GRAD_THREADS), 0, stream, a, sums + filled);
     filled += grid;
   }
-  if (!clip || filled == 0) {
+  if (!clip) {
     hipLaunchKernelGGL(grad_norm_kernel, dim3(1), dim3(GRAD_THREADS), 0, stream, sums, filled, norm);
     return hipGetLastError();
   }
   bool first = true;
   for (int64_t i = 0; i < n;) {
-    i = grad_table(i, n, tensors, numels, f32, &a);
+    i = grad_table(i, n, tensors, numels, f32, GRAD_PIECE, &a);
     if (a.count == 0) break;
     hipLaunchKernelGGL(grad_scale_kernel, dim3(grad_grid(a)), dim3(GRAD_THREADS), 0, stream, a, sums,
                        filled, max_norm, first ? norm : nullptr);

@@ -10,59 +10,13 @@
 // read (or written) once and its k expert rows are written (or read) once,
 // so no row number has to be inverted.  A slot outside [0, T k) is skipped:
 // bad slots give wrong rows but never a bad access.
-#include "mx_device.h"
 #include "mx_kernels.h"
+#include "mx_rows.h"
 
 namespace mx {
 
 constexpr int MOVE_THREADS = 256;
 constexpr int MOVE_SPAN = 512;          // elements of a row that a wave holds, 8 a lane
-
-// Eight elements of a row as packed BF16 pairs.  VEC: lane l holds elements
-// 8 l .. 8 l + 7 of the span (rows of a multiple of 8 elements on 16-byte
-// alignment); otherwise elements l, l + 64, ..., l + 448, one at a time.
-template <bool VEC>
-__device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c0, int lane, int64_t H) {
-  if (VEC) {
-    const int64_t c = c0 + 8 * lane;
-    return c < H ? load_stream16(row + c) : make_uint4(0, 0, 0, 0);
-  }
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const int64_t c = c0 + 128 * i + lane, d = c + 64;
-    const uint32_t lo = c < H ? row[c] : 0, hi = d < H ? row[d] : 0;
-    w[i] = lo | hi << 16;
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-template <bool VEC>
-__device__ __forceinline__ void store8(uint16_t* row, int64_t c0, int lane, int64_t H, uint4 v) {
-  if (VEC) {
-    const int64_t c = c0 + 8 * lane;
-    if (c < H) *(uint4*)(row + c) = v;
-    return;
-  }
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const int64_t c = c0 + 128 * i + lane, d = c + 64;
-    if (c < H) row[c] = (uint16_t)w[i];
-    if (d < H) row[d] = (uint16_t)(w[i] >> 16);
-  }
-}
-
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-
-__device__ __forceinline__ void unpack8(uint4 v, float f[8]) {
-  f[0] = bf_lo(v.x), f[1] = bf_hi(v.x), f[2] = bf_lo(v.y), f[3] = bf_hi(v.y);
-  f[4] = bf_lo(v.z), f[5] = bf_hi(v.z), f[6] = bf_lo(v.w), f[7] = bf_hi(v.w);
-}
-__device__ __forceinline__ uint4 pack8(const float f[8]) {
-  return make_uint4(cvt_pk_bf16(f[0], f[1]), cvt_pk_bf16(f[2], f[3]), cvt_pk_bf16(f[4], f[5]),
-                    cvt_pk_bf16(f[6], f[7]));
-}
 
 // Rows of the expert order that hold a choice.
 __device__ __forceinline__ int64_t rows_used(const int64_t* offsets, int E, int64_t P) {
@@ -83,31 +37,49 @@ __device__ __forceinline__ int64_t wave_id() {
   return (int64_t)blockIdx.x * (MOVE_THREADS / 64) + w;
 }
 
+// Zero rows first, first + step, ... below P.
+__device__ __forceinline__ void zero_rows(uint16_t* y, int64_t first, int64_t step, const MoveArgs& a,
+                                          int lane) {
+  const u32x4 zero = {0, 0, 0, 0};
+  for (int64_t r = first; r < a.P; r += step)
+    for (int64_t c = 8 * lane; c < a.H; c += MOVE_SPAN) {
+      if (c + 8 <= a.H) store_bf16x8<true, false>(y + r * a.H, c, a.H, zero);
+      else store_bf16x8<false, false>(y + r * a.H, c, a.H, zero);
+    }
+}
+
+template <bool WHOLE, bool STREAM>
+__device__ __forceinline__ void dispatch_span(const MoveArgs& a, int64_t t, int64_t c,
+                                              const uint16_t* x, uint16_t* y) {
+  const u32x4 v = load_bf16x8<WHOLE>(x + t * a.H, c, a.H);
+  for (int j = 0; j < a.k; j++) {
+    const int64_t s = a.slots[t * a.k + j];
+    if (s >= 0 && s < a.P) store_bf16x8<WHOLE, STREAM>(y + s * a.H, c, a.H, v);
+  }
+}
+
 // One wave per (token, span); the rows past the used ones are zeroed by all
 // waves in turn.
-template <bool VEC>
+template <bool STREAM>
 __global__ void __launch_bounds__(MOVE_THREADS)
 dispatch_kernel(MoveArgs a, const uint16_t* __restrict__ x, uint16_t* __restrict__ y) {
   const int lane = threadIdx.x & 63;
   const int64_t id = wave_id(), n = a.T * a.spans;
   if (id < n) {
-    const int64_t t = id / a.spans, c0 = (id - t * a.spans) * MOVE_SPAN;
-    const uint4 v = load8<VEC>(x + t * a.H, c0, lane, a.H);
-    for (int j = 0; j < a.k; j++) {
-      const int64_t s = a.slots[t * a.k + j];
-      if (s >= 0 && s < a.P) store8<VEC>(y + s * a.H, c0, lane, a.H, v);
-    }
+    const int64_t t = id / a.spans, c = (id - t * a.spans) * MOVE_SPAN + 8 * lane;
+    if (c + 8 <= a.H) dispatch_span<true, STREAM>(a, t, c, x, y);
+    else if (c < a.H) dispatch_span<false, STREAM>(a, t, c, x, y);
   }
   const int64_t waves = (int64_t)gridDim.x * (MOVE_THREADS / 64);
-  for (int64_t r = rows_used(a.offsets, a.E, a.P) + id; r < a.P; r += waves)
-    for (int64_t c0 = 0; c0 < a.H; c0 += MOVE_SPAN)
-      store8<VEC>(y + r * a.H, c0, lane, a.H, make_uint4(0, 0, 0, 0));
+  zero_rows(y, rows_used(a.offsets, a.E, a.P) + id, waves, a, lane);
 }
 
 // The same, quantised in 1x32 blocks: four lanes hold a block, which is
-// quantised once and written to every row of its token.  H % 32 == 0; VEC as
-// above (a block never straddles spans).
-template <int EL>
+// quantised once and written to every row of its token.  H % 32 == 0, so a
+// block never straddles spans.  (16 elements a lane, with 16-byte payload and
+// whole-word scale stores, measured 143 us against 132 at 16384 tokens x 8 x
+// 4096, 76 against 81 at x 2 x 7168, the same below.)
+template <int EL, bool STREAM>
 __global__ void __launch_bounds__(MOVE_THREADS)
 dispatch_quant_kernel(MoveArgs a, const uint16_t* __restrict__ x, uint8_t* __restrict__ q,
                       uint8_t* __restrict__ s) {
@@ -123,7 +95,9 @@ dispatch_quant_kernel(MoveArgs a, const uint16_t* __restrict__ x, uint8_t* __res
     for (int j = 0; j < a.k; j++) {
       const int64_t r = a.slots[t * a.k + j];
       if (r >= 0 && r < a.P && live) {
-        *(uint2*)(q + r * a.H + c) = o;
+        u32x2* dst = (u32x2*)(q + r * a.H + c);
+        if (STREAM) __builtin_nontemporal_store((u32x2){o.x, o.y}, dst);
+        else *dst = (u32x2){o.x, o.y};
         if ((lane & 3) == 0) s[r * S + (c >> 5)] = (uint8_t)sb;
       }
     }
@@ -135,41 +109,100 @@ dispatch_quant_kernel(MoveArgs a, const uint16_t* __restrict__ x, uint8_t* __res
   }
 }
 
+template <bool WHOLE>
+__device__ __forceinline__ void combine_span(const MoveArgs& a, int64_t t, int64_t c, const uint16_t* y,
+                                             const float* weights, const uint16_t* residual,
+                                             uint16_t* out) {
+  float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  // eight rows in flight
+  for (int j0 = 0; j0 < a.k; j0 += 8) {
+    u32x4 v[8];
+    float w[8];
+#pragma unroll
+    for (int u = 0; u < 8; u++) {
+      const int j = j0 + u;
+      const int64_t s = j < a.k ? a.slots[t * a.k + j] : -1;
+      const bool in = s >= 0 && s < a.P;
+      v[u] = (u32x4){0, 0, 0, 0};
+      w[u] = in && weights ? weights[t * a.k + j] : 1.0f;
+      if (in) v[u] = load_bf16x8<WHOLE>(y + s * a.H, c, a.H);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; u++) {
+      float f[8];
+      unpack8(v[u], f);
+#pragma unroll
+      for (int i = 0; i < 8; i++) acc[i] = fmaf(w[u], f[i], acc[i]);
+    }
+  }
+  if (residual) {
+    float f[8];
+    unpack8(load_bf16x8<WHOLE>(residual + t * a.H, c, a.H), f);
+#pragma unroll
+    for (int i = 0; i < 8; i++) acc[i] += f[i];
+  }
+  store_bf16x8<WHOLE, false>(out + t * a.H, c, a.H, pack8(acc));
+}
+
 // One wave per (token, span): the k rows' pieces are added in 32 bits, in
 // the order of the choices, and rounded once.
-template <bool VEC>
 __global__ void __launch_bounds__(MOVE_THREADS)
 combine_kernel(MoveArgs a, const uint16_t* __restrict__ y, const float* __restrict__ weights,
                const uint16_t* residual, uint16_t* out) {   // out may be residual
   const int lane = threadIdx.x & 63;
   const int64_t id = wave_id();
   if (id >= a.T * a.spans) return;
-  const int64_t t = id / a.spans, c0 = (id - t * a.spans) * MOVE_SPAN;
-  float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 4
-  for (int j = 0; j < a.k; j++) {
-    const int64_t s = a.slots[t * a.k + j];
-    if (s < 0 || s >= a.P) continue;
-    const float w = weights ? weights[t * a.k + j] : 1.0f;
-    float f[8];
-    unpack8(load8<VEC>(y + s * a.H, c0, lane, a.H), f);
-#pragma unroll
-    for (int i = 0; i < 8; i++) acc[i] = fmaf(w, f[i], acc[i]);
-  }
-  if (residual) {
-    float f[8];
-    unpack8(load8<VEC>(residual + t * a.H, c0, lane, a.H), f);
-#pragma unroll
-    for (int i = 0; i < 8; i++) acc[i] += f[i];
-  }
-  store8<VEC>(out + t * a.H, c0, lane, a.H, pack8(acc));
+  const int64_t t = id / a.spans, c = (id - t * a.spans) * MOVE_SPAN + 8 * lane;
+  if (c + 8 <= a.H) combine_span<true>(a, t, c, y, weights, residual, out);
+  else if (c < a.H) combine_span<false>(a, t, c, y, weights, residual, out);
 }
 
 constexpr int MOVE_MAX_K = 16;
 
-// One workgroup per token; its waves take spans in turn, and the k products
-// <do, y> are summed over lanes and then waves in a fixed order.
-template <bool VEC, int KC>
+template <bool WHOLE, int KC, bool STREAM>
+__device__ __forceinline__ void combine_backward_span(const MoveArgs& a, int64_t t, int64_t c,
+                                                      const uint16_t* dout, const uint16_t* y,
+                                                      const float* weights, uint16_t* dy,
+                                                      float dot[KC]) {
+  float d[8];
+  unpack8(load_bf16x8<WHOLE>(dout + t * a.H, c, a.H), d);
+#pragma unroll
+  for (int j = 0; j < KC; j++) {
+    const int64_t s = j < a.k ? a.slots[t * a.k + j] : -1;
+    if (s < 0 || s >= a.P) continue;
+    const float w = weights[t * a.k + j];
+    float f[8], g[8];
+    unpack8(load_bf16x8<WHOLE>(y + s * a.H, c, a.H), f);
+#pragma unroll
+    for (int i = 0; i < 8; i++) dot[j] = fmaf(d[i], f[i], dot[j]), g[i] = w * d[i];
+    store_bf16x8<WHOLE, STREAM>(dy + s * a.H, c, a.H, pack8(g));
+  }
+}
+
+// Sums of N values over the 64 lanes: lane l gets the sum of value l % N.  A
+// step halves what each lane holds while it has several values, exchanging the
+// half it gives up (N - 1 exchanges), and adds the rest up (log2(64 / N) more).
+template <int N>
+__device__ __forceinline__ float lane_sums(float* v, int lane) {
+#pragma unroll
+  for (int n = N / 2; n > 0; n >>= 1) {
+    const bool upper = (lane & n) != 0;
+#pragma unroll
+    for (int j = 0; j < n; j++) {
+      const float give = upper ? v[j] : v[j + n];
+      v[j] = (upper ? v[j + n] : v[j]) + __shfl_xor(give, n, 64);
+    }
+  }
+  float s = v[0];
+#pragma unroll
+  for (int m = N; m < 64; m <<= 1) s += __shfl_xor(s, m, 64);
+  return s;
+}
+
+// One workgroup per token, of a wave per span up to four; its waves take spans
+// in turn, and the k products <do, y> are summed over lanes and then waves in
+// a fixed order.
+template <int KC, bool STREAM>
 __global__ void __launch_bounds__(MOVE_THREADS)
 combine_backward_kernel(MoveArgs a, const uint16_t* __restrict__ dout,
                         const uint16_t* __restrict__ y, const float* __restrict__ weights,
@@ -181,40 +214,22 @@ combine_backward_kernel(MoveArgs a, const uint16_t* __restrict__ dout,
   float dot[KC];
 #pragma unroll
   for (int j = 0; j < KC; j++) dot[j] = 0.0f;
-  for (int64_t c0 = wave * MOVE_SPAN; c0 < a.H; c0 += MOVE_THREADS / 64 * MOVE_SPAN) {
-    float d[8];
-    unpack8(load8<VEC>(dout + t * a.H, c0, lane, a.H), d);
-#pragma unroll
-    for (int j = 0; j < KC; j++) {
-      const int64_t s = j < a.k ? a.slots[t * a.k + j] : -1;
-      if (s < 0 || s >= a.P) continue;
-      const float w = weights[t * a.k + j];
-      float f[8], g[8];
-      unpack8(load8<VEC>(y + s * a.H, c0, lane, a.H), f);
-#pragma unroll
-      for (int i = 0; i < 8; i++) dot[j] = fmaf(d[i], f[i], dot[j]), g[i] = w * d[i];
-      store8<VEC>(dy + s * a.H, c0, lane, a.H, pack8(g));
-    }
+  const int waves = (int)(blockDim.x >> 6);
+  for (int64_t c0 = wave * MOVE_SPAN; c0 < a.H; c0 += waves * MOVE_SPAN) {
+    const int64_t c = c0 + 8 * lane;
+    if (c + 8 <= a.H) combine_backward_span<true, KC, STREAM>(a, t, c, dout, y, weights, dy, dot);
+    else if (c < a.H) combine_backward_span<false, KC, STREAM>(a, t, c, dout, y, weights, dy, dot);
   }
-#pragma unroll
-  for (int j = 0; j < KC; j++) {
-    float v = dot[j];
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m, 64);
-    if (lane == 0) part[wave][j] = v;
-  }
+  const float sum = lane_sums<KC>(dot, lane);
+  if (lane < KC) part[wave][lane] = sum;
   __syncthreads();
   if ((int)threadIdx.x < a.k) {
     float v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < MOVE_THREADS / 64; w++) v += part[w][threadIdx.x];
+    for (int w = 0; w < waves; w++) v += part[w][threadIdx.x];
     const int64_t s = a.slots[t * a.k + threadIdx.x];
     dweights[t * a.k + threadIdx.x] = s >= 0 && s < a.P ? v : 0.0f;
   }
-  const int64_t waves = (int64_t)gridDim.x * (MOVE_THREADS / 64);
-  for (int64_t r = rows_used(a.offsets, a.E, a.P) + t * (MOVE_THREADS / 64) + wave; r < a.P; r += waves)
-    for (int64_t c0 = 0; c0 < a.H; c0 += MOVE_SPAN)
-      store8<VEC>(dy + r * a.H, c0, lane, a.H, make_uint4(0, 0, 0, 0));
+  zero_rows(dy, rows_used(a.offsets, a.E, a.P) + t * waves + wave, (int64_t)gridDim.x * waves, a, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -231,14 +246,21 @@ static MoveArgs move_args(int64_t T, int64_t H, int64_t k, int64_t E, const int6
 static dim3 move_grid(const MoveArgs& a) {
   return dim3((unsigned)((a.T * a.spans + MOVE_THREADS / 64 - 1) / (MOVE_THREADS / 64)));
 }
-// Whole 16-byte pieces in every row of every operand.
-static bool move_vec(int64_t H, uintptr_t ptrs) { return H % 8 == 0 && (ptrs & 15) == 0; }
+// Expert rows of at least `least` bytes in whole 128-byte lines are written
+// past the caches; rows that share a line with the next are merged in L2.
+// Measured, plain against streaming stores: dispatch 133 / 122 us at 16384
+// tokens x 2 x 7168, 17.6 / 16.1 at 4096 x 4 x 2048, 122 / 126 at 65536 x 8 x
+// 512; quantising 135 / 127 at 16384 x 8 x 4096, 58 / 67 at 65536 x 8 x 512;
+// combine's gradient 474 / 447 and 239 / 224 there, 55 / 65 at 8192 x 8 x 1000.
+static bool stream_rows(int64_t row_bytes, const void* y, int64_t least) {
+  return row_bytes >= least && row_bytes % 128 == 0 && (uintptr_t)y % 128 == 0;
+}
 
 hipError_t launch_dispatch(const void* x, int64_t T, int64_t H, int64_t k, int64_t E,
                            const int64_t* offsets, const int32_t* slots, void* y,
                            hipStream_t stream) {
   const MoveArgs a = move_args(T, H, k, E, offsets, slots);
-  if (move_vec(H, (uintptr_t)x | (uintptr_t)y))
+  if (stream_rows(2 * H, y, 4096))
     hipLaunchKernelGGL(dispatch_kernel<true>, move_grid(a), dim3(MOVE_THREADS), 0, stream, a,
                        (const uint16_t*)x, (uint16_t*)y);
   else
@@ -247,16 +269,22 @@ hipError_t launch_dispatch(const void* x, int64_t T, int64_t H, int64_t k, int64
   return hipGetLastError();
 }
 
+template <int EL>
+static void launch_dq(const MoveArgs& a, const void* x, void* q, void* s, hipStream_t stream) {
+  if (stream_rows(a.H, q, 4096))
+    hipLaunchKernelGGL((dispatch_quant_kernel<EL, true>), move_grid(a), dim3(MOVE_THREADS), 0, stream, a,
+                       (const uint16_t*)x, (uint8_t*)q, (uint8_t*)s);
+  else
+    hipLaunchKernelGGL((dispatch_quant_kernel<EL, false>), move_grid(a), dim3(MOVE_THREADS), 0, stream, a,
+                       (const uint16_t*)x, (uint8_t*)q, (uint8_t*)s);
+}
+
 hipError_t launch_dispatch_quant(int elem, const void* x, int64_t T, int64_t H, int64_t k, int64_t E,
                                  const int64_t* offsets, const int32_t* slots, void* q, void* s,
                                  hipStream_t stream) {
   const MoveArgs a = move_args(T, H, k, E, offsets, slots);
-  if (elem == ELEM_E5M2)
-    hipLaunchKernelGGL(dispatch_quant_kernel<ELEM_E5M2>, move_grid(a), dim3(MOVE_THREADS), 0, stream,
-                       a, (const uint16_t*)x, (uint8_t*)q, (uint8_t*)s);
-  else
-    hipLaunchKernelGGL(dispatch_quant_kernel<ELEM_E4M3>, move_grid(a), dim3(MOVE_THREADS), 0, stream,
-                       a, (const uint16_t*)x, (uint8_t*)q, (uint8_t*)s);
+  if (elem == ELEM_E5M2) launch_dq<ELEM_E5M2>(a, x, q, s, stream);
+  else launch_dq<ELEM_E4M3>(a, x, q, s, stream);
   return hipGetLastError();
 }
 
@@ -264,19 +292,16 @@ hipError_t launch_combine(const void* y, int64_t T, int64_t H, int64_t k, const 
                           const float* weights, const void* residual, void* out,
                           hipStream_t stream) {
   const MoveArgs a = move_args(T, H, k, 0, nullptr, slots);
-  if (move_vec(H, (uintptr_t)y | (uintptr_t)residual | (uintptr_t)out))
-    hipLaunchKernelGGL(combine_kernel<true>, move_grid(a), dim3(MOVE_THREADS), 0, stream, a,
-                       (const uint16_t*)y, weights, (const uint16_t*)residual, (uint16_t*)out);
-  else
-    hipLaunchKernelGGL(combine_kernel<false>, move_grid(a), dim3(MOVE_THREADS), 0, stream, a,
-                       (const uint16_t*)y, weights, (const uint16_t*)residual, (uint16_t*)out);
+  hipLaunchKernelGGL(combine_kernel, move_grid(a), dim3(MOVE_THREADS), 0, stream, a,
+                     (const uint16_t*)y, weights, (const uint16_t*)residual, (uint16_t*)out);
   return hipGetLastError();
 }
 
-template <bool VEC, int KC>
+template <int KC, bool STREAM>
 static void launch_cb(const MoveArgs& a, const void* dout, const void* y, const float* weights,
                       void* dy, float* dweights, hipStream_t stream) {
-  hipLaunchKernelGGL((combine_backward_kernel<VEC, KC>), dim3((unsigned)a.T), dim3(MOVE_THREADS), 0,
+  const int waves = a.spans < 1 ? 1 : a.spans < MOVE_THREADS / 64 ? a.spans : MOVE_THREADS / 64;
+  hipLaunchKernelGGL((combine_backward_kernel<KC, STREAM>), dim3((unsigned)a.T), dim3(64 * waves), 0,
                      stream, a, (const uint16_t*)dout, (const uint16_t*)y, weights, (uint16_t*)dy,
                      dweights);
 }
@@ -286,13 +311,12 @@ hipError_t launch_combine_backward(const void* dout, const void* y, int64_t T, i
                                    const float* weights, void* dy, float* dweights,
                                    hipStream_t stream) {
   const MoveArgs a = move_args(T, H, k, E, offsets, slots);
-  const bool vec = move_vec(H, (uintptr_t)dout | (uintptr_t)y | (uintptr_t)dy);
-  if (k <= 8) {
-    if (vec) launch_cb<true, 8>(a, dout, y, weights, dy, dweights, stream);
-    else launch_cb<false, 8>(a, dout, y, weights, dy, dweights, stream);
+  if (stream_rows(2 * H, dy, 1024)) {
+    if (k <= 8) launch_cb<8, true>(a, dout, y, weights, dy, dweights, stream);
+    else launch_cb<16, true>(a, dout, y, weights, dy, dweights, stream);
   } else {
-    if (vec) launch_cb<true, 16>(a, dout, y, weights, dy, dweights, stream);
-    else launch_cb<false, 16>(a, dout, y, weights, dy, dweights, stream);
+    if (k <= 8) launch_cb<8, false>(a, dout, y, weights, dy, dweights, stream);
+    else launch_cb<16, false>(a, dout, y, weights, dy, dweights, stream);
   }
   return hipGetLastError();
 }

@@ -18,8 +18,8 @@
 // the expert's index (E <= 512), so that keys are distinct, a tie falls to
 // the lowest index and one v_max_f64 / v_min_f64 pair moves value and index
 // together.  A 32-bit logit keeps all its bits; a 64-bit v keeps 43.
-#include "mx_device.h"
 #include "mx_kernels.h"
+#include "mx_rows.h"
 
 namespace mx {
 
@@ -117,53 +117,28 @@ __device__ __forceinline__ double key_value(double k) {
   return __longlong_as_double((long long)((uint64_t)__double_as_longlong(k) & ~(uint64_t)511));
 }
 
-__device__ __forceinline__ float load_logit(const float* p) { return *p; }
-__device__ __forceinline__ float load_logit(const uint16_t* p) {
-  return __uint_as_float((uint32_t)*p << 16);
-}
-__device__ __forceinline__ void load_logit4(const float* p, float v[4]) {
-  const float4 a = *(const float4*)p;
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-}
-__device__ __forceinline__ void load_logit4(const uint16_t* p, float v[4]) {
-  const uint2 a = *(const uint2*)p;
-  v[0] = __uint_as_float(a.x << 16), v[1] = __uint_as_float(a.x & 0xFFFF0000u);
-  v[2] = __uint_as_float(a.y << 16), v[3] = __uint_as_float(a.y & 0xFFFF0000u);
-}
-__device__ __forceinline__ void store_logit4(float* p, const float v[4]) {
-  *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
-}
-__device__ __forceinline__ void store_logit4(uint16_t* p, const float v[4]) {
-  *(uint2*)p = make_uint2(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]));
-}
-__device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_logit(uint16_t* p, float v) {
-  *p = (uint16_t)cvt_pk_bf16(v, v);
-}
-
 // Experts e0 .. e0 + 3 of a row; -inf past it.
 template <typename IN>
-__device__ __forceinline__ void load_chunk(const IN* __restrict__ row, int E, bool vec, int e0,
-                                           float x[4]) {
+__device__ __forceinline__ void load_chunk(const IN* __restrict__ row, int E, int e0, float x[4]) {
 #pragma unroll
   for (int i = 0; i < 4; i++) x[i] = -__builtin_inff();
-  if (vec) {
-    if (e0 < E) load_logit4(row + e0, x);
-  } else {
+  if (e0 + 4 <= E) {
+    load4(row + e0, x);
+  } else if (e0 < E) {
 #pragma unroll
-    for (int i = 0; i < 4; i++)
-      if (e0 + i < E) x[i] = load_logit(row + e0 + i);
+    for (int i = 0; i < 3; i++)
+      if (e0 + i < E) x[i] = load1(row + e0 + i);
   }
 }
 
 // Chunk c of a token's row held by lane l: experts (L c + l) * 4 .. + 3.
 template <typename IN, int L, int C>
-__device__ __forceinline__ void load_row(const IN* __restrict__ row, int E, bool vec, int l,
-                                         bool live, float x[C][4]) {
+__device__ __forceinline__ void load_row(const IN* __restrict__ row, int E, int l, bool live,
+                                         float x[C][4]) {
 #pragma unroll
   for (int c = 0; c < C; c++) {
     if (live) {
-      load_chunk(row, E, vec, (c * L + l) * 4, x[c]);
+      load_chunk(row, E, (c * L + l) * 4, x[c]);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; i++) x[c][i] = -__builtin_inff();
@@ -217,7 +192,7 @@ struct RouteArgs {
   const void* logits;
   const float* bias;
   int64_t T;
-  int E, k, n_groups, top_groups, group_max, groups_pow2, softmax, renorm, vec, vec_bias;
+  int E, k, n_groups, top_groups, group_max, groups_pow2, softmax, renorm;
   float scale;
   float* weights;
   int32_t* experts;
@@ -505,7 +480,7 @@ __device__ __forceinline__ void choice_values(const RouteArgs& a, const float x[
     return;
   }
   float b[C][4], inv = 1.0f;
-  load_row<float, L, C>(a.bias, a.E, a.vec_bias, l, true, b);
+  load_row<float, L, C>(a.bias, a.E, l, true, b);
   if (a.softmax) {
     float sum = 0.0f;
 #pragma unroll
@@ -546,7 +521,7 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, int64_t t, bool liv
                                          float bias_max) {
   Choice r;
   float x[C][4];
-  load_row<IN, L, C>((const IN*)a.logits + t * a.E, a.E, a.vec, l, live, x);
+  load_row<IN, L, C>((const IN*)a.logits + t * a.E, a.E, l, live, x);
   r.m = r.sum = 0.0f;
   r.nan = false;
   int odd = 0;                       // NaN and +inf take the 64-bit keys
@@ -638,7 +613,7 @@ __device__ __forceinline__ void choose_exact(const RouteArgs& a, int64_t t, doub
   asm volatile("" : "+v"(l));            // nothing of this is kept for the tokens that do not need it
   const IN* row = (const IN*)a.logits + t * a.E;
   float x[C][4];
-  load_row<IN, L, C>(row, a.E, a.vec, l, true, x);
+  load_row<IN, L, C>(row, a.E, l, true, x);
   float m = NEG;
   int nan = 0;
 #pragma unroll
@@ -676,7 +651,7 @@ __device__ __forceinline__ void choose_exact(const RouteArgs& a, int64_t t, doub
       for (int i = 0; i < 4; i++) key[c][i] = rcp_64(1.0 + exp_64(-(double)x[c][i]));
   }
   float b[C][4];
-  if (SCORED) load_row<float, L, C>(a.bias, a.E, a.vec_bias, l, true, b);
+  if (SCORED) load_row<float, L, C>(a.bias, a.E, l, true, b);
 #pragma unroll
   for (int c = 0; c < C; c++)
 #pragma unroll
@@ -770,7 +745,7 @@ __device__ __forceinline__ int route_token(const RouteArgs& a, int64_t t, bool l
 
   // the chosen scores; renormalised ones as ratios of terms that share a
   // factor, so that they hold where every chosen score underflows
-  const float xe = has ? load_logit((const IN*)a.logits + t * a.E + e) : -__builtin_inff();
+  const float xe = has ? load1((const IN*)a.logits + t * a.E + e) : -__builtin_inff();
   float w;
   if (a.renorm) {
     const float big = row_reduce<L>(xe, [](float p, float q) { return fmaxf(p, q); });  // NaN aside
@@ -972,7 +947,7 @@ struct RouteBackwardArgs {
   const int32_t* experts;
   void* dlogits;
   int64_t T;
-  int E, k, softmax, renorm, vec;
+  int E, k, softmax, renorm;
   float scale;
 };
 
@@ -989,12 +964,12 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteBackwardArgs a
   if (e >= a.E) e = -1;
   const bool has = e >= 0;
   const float g = has ? a.dweights[tt * a.k + l] : 0.0f;
-  const float xe = has ? load_logit(row + e) : -__builtin_inff();
+  const float xe = has ? load1(row + e) : -__builtin_inff();
   float x[C][4];
   float m = -__builtin_inff(), sum = 0.0f;
   float d = 0.0f, dot = 0.0f;                  // lane l's choice's own term; the row's common term
   if (dense) {
-    load_row<IN, L, C>(row, a.E, a.vec, l, true, x);
+    load_row<IN, L, C>(row, a.E, l, true, x);
     int nan = 0;
 #pragma unroll
     for (int c = 0; c < C; c++)
@@ -1063,12 +1038,12 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteBackwardArgs a
 #pragma unroll
   for (int c = 0; c < C; c++) {
     const int e0 = (c * L + l) * 4;
-    if (a.vec) {
-      if (e0 < a.E) store_logit4(dst + e0, out[c]);
+    if (e0 + 4 <= a.E) {
+      store4(dst + e0, out[c]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; i++)
-        if (e0 + i < a.E) store_logit(dst + e0 + i, out[c][i]);
+      for (int i = 0; i < 3; i++)
+        if (e0 + i < a.E) store1(dst + e0 + i, out[c][i]);
     }
   }
 }
@@ -1135,12 +1110,9 @@ hipError_t launch_route(int softmax, int f32, const void* logits, const float* b
   a.softmax = softmax, a.renorm = renorm, a.scale = scale;
   a.weights = weights, a.experts = experts, a.offsets = offsets, a.slots = slots;
   a.hist = (uint32_t*)workspace;
-  // four logits at once where every row starts on their alignment
-  a.vec = E % 4 == 0 && ((uintptr_t)logits & (f32 ? 15 : 7)) == 0;
   const int64_t chunks = E / n_groups / 4;
   a.groups_pow2 = n_groups > 1 && E % (4 * n_groups) == 0 && (chunks & (chunks - 1)) == 0;
   route_split(T, &a.blocks, &a.tokens_per_block);
-  a.vec_bias = E % 4 == 0 && ((uintptr_t)bias & 15) == 0;
   const bool scored = bias != nullptr;
   if (f32) launch_route_in<float>(scored, a, stream);
   else launch_route_in<uint16_t>(scored, a, stream);
@@ -1165,8 +1137,6 @@ hipError_t launch_route_backward(int softmax, int f32, int64_t T, int64_t E, int
   RouteBackwardArgs a;
   a.dweights = dweights, a.logits = logits, a.experts = experts, a.dlogits = dlogits;
   a.T = T, a.E = (int)E, a.k = (int)k, a.softmax = softmax, a.renorm = renorm, a.scale = scale;
-  const uintptr_t align = f32 ? 15 : 7;
-  a.vec = E % 4 == 0 && (((uintptr_t)logits | (uintptr_t)dlogits) & align) == 0;
   if (f32) launch_route_backward_in<float>(a, stream);
   else launch_route_backward_in<uint16_t>(a, stream);
   return hipGetLastError();

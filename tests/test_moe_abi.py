@@ -112,8 +112,8 @@ def test_grad_validation(max_norm):
     assert _grad([64], [4], [2], max_norm) == INVALID                 # unknown type
     assert _grad([66], [4], [1], max_norm) == INVALID                 # FP32 off its alignment
     assert _grad([65], [4], [0], max_norm) == INVALID                 # BF16 off its alignment
-    assert _grad([64], [1 << 45], [0], max_norm) == SHAPE
-    assert _grad([64, 1 << 46], [1 << 43, 1 << 43], [1, 1], max_norm) == SHAPE
+    assert _grad([64], [1 << 41], [0], max_norm) == SHAPE
+    assert _grad([64, 1 << 46], [1 << 39, 1 << 39], [1, 1], max_norm) == SHAPE
     assert _grad([64], [4], [1], max_norm, norm=0) == INVALID
     assert _grad([64], [4], [1], max_norm, ws=0) == INVALID
     assert _grad([64], [4], [1], max_norm, nws=8) == INVALID
