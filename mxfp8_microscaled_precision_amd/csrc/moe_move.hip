@@ -65,13 +65,14 @@ __global__ void __launch_bounds__(MOVE_THREADS)
 dispatch_kernel(MoveArgs a, const uint16_t* __restrict__ x, uint16_t* __restrict__ y) {
   const int lane = threadIdx.x & 63;
   const int64_t id = wave_id(), n = a.T * a.spans;
+  const int64_t used = rows_used(a.offsets, a.E, a.P);
   if (id < n) {
     const int64_t t = id / a.spans, c = (id - t * a.spans) * MOVE_SPAN + 8 * lane;
     if (c + 8 <= a.H) dispatch_span<true, STREAM>(a, t, c, x, y);
     else if (c < a.H) dispatch_span<false, STREAM>(a, t, c, x, y);
   }
   const int64_t waves = (int64_t)gridDim.x * (MOVE_THREADS / 64);
-  zero_rows(y, rows_used(a.offsets, a.E, a.P) + id, waves, a, lane);
+  zero_rows(y, used + id, waves, a, lane);
 }
 
 // The same, quantised in 1x32 blocks: four lanes hold a block, which is
@@ -85,7 +86,7 @@ dispatch_quant_kernel(MoveArgs a, const uint16_t* __restrict__ x, uint8_t* __res
                       uint8_t* __restrict__ s) {
   const int lane = threadIdx.x & 63;
   const int64_t id = wave_id(), n = a.T * a.spans;
-  const int64_t S = a.H / 32;
+  const int64_t S = a.H / 32, used = rows_used(a.offsets, a.E, a.P);
   if (id < n) {
     const int64_t t = id / a.spans, c = (id - t * a.spans) * MOVE_SPAN + 8 * lane;
     const bool live = c < a.H;                    // whole quads in or out
@@ -103,7 +104,7 @@ dispatch_quant_kernel(MoveArgs a, const uint16_t* __restrict__ x, uint8_t* __res
     }
   }
   const int64_t waves = (int64_t)gridDim.x * (MOVE_THREADS / 64);
-  for (int64_t r = rows_used(a.offsets, a.E, a.P) + id; r < a.P; r += waves) {
+  for (int64_t r = used + id; r < a.P; r += waves) {
     for (int64_t c = 8 * lane; c < a.H; c += MOVE_SPAN) *(uint2*)(q + r * a.H + c) = make_uint2(0, 0);
     for (int64_t c = lane; c < S; c += 64) s[r * S + c] = 0;
   }
@@ -157,8 +158,6 @@ combine_kernel(MoveArgs a, const uint16_t* __restrict__ y, const float* __restri
   else if (c < a.H) combine_span<false>(a, t, c, y, weights, residual, out);
 }
 
-constexpr int MOVE_MAX_K = 16;
-
 template <bool WHOLE, int KC, bool STREAM>
 __device__ __forceinline__ void combine_backward_span(const MoveArgs& a, int64_t t, int64_t c,
                                                       const uint16_t* dout, const uint16_t* y,
@@ -166,16 +165,30 @@ __device__ __forceinline__ void combine_backward_span(const MoveArgs& a, int64_t
                                                       float dot[KC]) {
   float d[8];
   unpack8(load_bf16x8<WHOLE>(dout + t * a.H, c, a.H), d);
+  // eight rows in flight
 #pragma unroll
-  for (int j = 0; j < KC; j++) {
-    const int64_t s = j < a.k ? a.slots[t * a.k + j] : -1;
-    if (s < 0 || s >= a.P) continue;
-    const float w = weights[t * a.k + j];
-    float f[8], g[8];
-    unpack8(load_bf16x8<WHOLE>(y + s * a.H, c, a.H), f);
+  for (int j0 = 0; j0 < KC; j0 += 8) {
+    if (j0 >= a.k) break;
+    int64_t s[8];
+    u32x4 v[8];
 #pragma unroll
-    for (int i = 0; i < 8; i++) dot[j] = fmaf(d[i], f[i], dot[j]), g[i] = w * d[i];
-    store_bf16x8<WHOLE, STREAM>(dy + s * a.H, c, a.H, pack8(g));
+    for (int u = 0; u < 8; u++) {
+      const int j = j0 + u;
+      s[u] = j < a.k ? a.slots[t * a.k + j] : -1;
+      if (s[u] >= a.P) s[u] = -1;
+      v[u] = (u32x4){0, 0, 0, 0};
+      if (s[u] >= 0) v[u] = load_bf16x8<WHOLE>(y + s[u] * a.H, c, a.H);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; u++) {
+      if (s[u] < 0) continue;
+      const float w = weights[t * a.k + j0 + u];
+      float f[8], g[8];
+      unpack8(v[u], f);
+#pragma unroll
+      for (int i = 0; i < 8; i++) dot[j0 + u] = fmaf(d[i], f[i], dot[j0 + u]), g[i] = w * d[i];
+      store_bf16x8<WHOLE, STREAM>(dy + s[u] * a.H, c, a.H, pack8(g));
+    }
   }
 }
 
@@ -199,18 +212,21 @@ __device__ __forceinline__ float lane_sums(float* v, int lane) {
   return s;
 }
 
-// One workgroup per token, of a wave per span up to four; its waves take spans
+// One workgroup per token, of a wave per span up to WAVES; its waves take spans
 // in turn, and the k products <do, y> are summed over lanes and then waves in
 // a fixed order.
-template <int KC, bool STREAM>
-__global__ void __launch_bounds__(MOVE_THREADS)
+template <int KC, bool STREAM, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES)
 combine_backward_kernel(MoveArgs a, const uint16_t* __restrict__ dout,
                         const uint16_t* __restrict__ y, const float* __restrict__ weights,
                         uint16_t* __restrict__ dy, float* __restrict__ dweights) {
-  __shared__ float part[MOVE_THREADS / 64][MOVE_MAX_K];
+  __shared__ float part[WAVES][KC];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int64_t t = blockIdx.x;
+  // what the end needs, asked for now: one token alone waits for every load
+  const int64_t used = rows_used(a.offsets, a.E, a.P);
+  const int64_t slot = (int)threadIdx.x < a.k ? a.slots[t * a.k + threadIdx.x] : -1;
   float dot[KC];
 #pragma unroll
   for (int j = 0; j < KC; j++) dot[j] = 0.0f;
@@ -226,10 +242,9 @@ combine_backward_kernel(MoveArgs a, const uint16_t* __restrict__ dout,
   if ((int)threadIdx.x < a.k) {
     float v = 0.0f;
     for (int w = 0; w < waves; w++) v += part[w][threadIdx.x];
-    const int64_t s = a.slots[t * a.k + threadIdx.x];
-    dweights[t * a.k + threadIdx.x] = s >= 0 && s < a.P ? v : 0.0f;
+    dweights[t * a.k + threadIdx.x] = slot >= 0 && slot < a.P ? v : 0.0f;
   }
-  zero_rows(dy, rows_used(a.offsets, a.E, a.P) + t * waves + wave, (int64_t)gridDim.x * waves, a, lane);
+  zero_rows(dy, used + t * waves + wave, (int64_t)gridDim.x * waves, a, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -297,13 +312,21 @@ hipError_t launch_combine(const void* y, int64_t T, int64_t H, int64_t k, const 
   return hipGetLastError();
 }
 
+// Four waves to a token fill the chip from 1024 tokens on; fewer tokens take
+// their spans side by side.
+template <int KC, bool STREAM, int WAVES>
+static void launch_cb_waves(const MoveArgs& a, const void* dout, const void* y, const float* weights,
+                            void* dy, float* dweights, hipStream_t stream) {
+  const int waves = a.spans < 1 ? 1 : a.spans < WAVES ? a.spans : WAVES;
+  hipLaunchKernelGGL((combine_backward_kernel<KC, STREAM, WAVES>), dim3((unsigned)a.T), dim3(64 * waves),
+                     0, stream, a, (const uint16_t*)dout, (const uint16_t*)y, weights, (uint16_t*)dy,
+                     dweights);
+}
 template <int KC, bool STREAM>
 static void launch_cb(const MoveArgs& a, const void* dout, const void* y, const float* weights,
                       void* dy, float* dweights, hipStream_t stream) {
-  const int waves = a.spans < 1 ? 1 : a.spans < MOVE_THREADS / 64 ? a.spans : MOVE_THREADS / 64;
-  hipLaunchKernelGGL((combine_backward_kernel<KC, STREAM>), dim3((unsigned)a.T), dim3(64 * waves), 0,
-                     stream, a, (const uint16_t*)dout, (const uint16_t*)y, weights, (uint16_t*)dy,
-                     dweights);
+  if (a.T < 1024) launch_cb_waves<KC, STREAM, 16>(a, dout, y, weights, dy, dweights, stream);
+  else launch_cb_waves<KC, STREAM, 4>(a, dout, y, weights, dy, dweights, stream);
 }
 
 hipError_t launch_combine_backward(const void* dout, const void* y, int64_t T, int64_t H, int64_t k,
