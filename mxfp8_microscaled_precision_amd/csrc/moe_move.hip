@@ -6,7 +6,9 @@
 //   combine           o[t] = r[t] + sum_j w_tj y[slot]
 //   combine backward  dy[slot] = w_tj do[t],  dw_tj = <do[t], y[slot]>
 //
-// All are bound by HBM bandwidth.  Every kernel walks tokens: a token's row is
+// All are bound by HBM bandwidth: 16384 tokens x 8 x 4096 take 245 us to
+// dispatch (4.9 TB/s), 128 quantised (5.4), 207 to combine (5.8), 445 for its
+// gradient (5.1); a 1 GiB copy runs at 5.1.  Every kernel walks tokens: a token's row is
 // read (or written) once and its k expert rows are written (or read) once,
 // so no row number has to be inverted.  A slot outside [0, T k) is skipped:
 // bad slots give wrong rows but never a bad access.

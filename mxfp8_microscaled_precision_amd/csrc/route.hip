@@ -18,6 +18,10 @@
 // the expert's index (E <= 512), so that keys are distinct, a tie falls to
 // the lowest index and one v_max_f64 / v_min_f64 pair moves value and index
 // together.  A 32-bit logit keeps all its bits; a 64-bit v keeps 43.
+//
+// Bound by instructions where E is large and by its two dependent launches
+// where it is small: 65536 x 256 logits with bias and groups take 54 us (14 at
+// the rate of a copy), 16384 x 64 10 us, one token 4.7.
 #include "mx_kernels.h"
 #include "mx_rows.h"
 
@@ -25,7 +29,7 @@ namespace mx {
 
 constexpr int ROUTE_MAX_EXPERTS = 512;
 constexpr int ROUTE_MAX_GROUPS = 32;
-constexpr int ROUTE_MAX_BLOCKS = 256;
+constexpr int ROUTE_MAX_BLOCKS = 256;           // one to a compute unit; each sums the counts of all
 constexpr int ROUTE_TOKENS = 64;                // a workgroup's tokens are a multiple
 
 #define MX_NEG_INF (-__builtin_inf())
