@@ -666,6 +666,7 @@ __device__ __forceinline__ void choose_exact(const RouteArgs& a, int64_t t, doub
 
   if (a.n_groups > 1) {
     const int gs = a.E / a.n_groups;
+    const double top_logit = fmin((double)m, 1.5e308);   // a key holds a +inf logit as 1.6e308
     double gk = MX_NEG_INF;              // lane q: the key of group q
     for (int q = 0; q < a.n_groups; q++) {
       double b1 = MX_NEG_INF, b2 = MX_NEG_INF;
@@ -687,8 +688,8 @@ __device__ __forceinline__ void choose_exact(const RouteArgs& a, int64_t t, doub
         const bool bad = b1 < -1.65e308 || (two && b2 < -1.65e308);   // NaN
         if (!SCORED) {                                 // logits: score them
           if (a.softmax) {
-            v = v >= m ? 1.0 : exp_64(v - m);
-            w = w >= m ? 1.0 : exp_64(w - m);
+            v = v >= top_logit ? 1.0 : exp_64(v - m);
+            w = w >= top_logit ? 1.0 : exp_64(w - m);
           } else {
             v = rcp_64(1.0 + exp_64(-v));
             w = rcp_64(1.0 + exp_64(-w));

@@ -284,3 +284,28 @@ def test_refusals():
     ]:
         with pytest.raises(kind):
             call()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("value", ["top2", "max"])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("E,n", [(64, 4), (60, 4), (256, 2), (512, 2), (200, 8)])
+def test_infinite_logits_in_later_groups(score, value, bias, E, n):
+    """A group with a +inf logit beats the groups without one, wherever it
+    stands: groups of a few chunks, of odd sizes, and of several rows of
+    chunks."""
+    x = _logits(12, E, E + n, mask=0.2)
+    inf, gs = float("inf"), E // n
+    x[0, E - 3] = inf                             # in the last group
+    x[1, gs + 1] = x[1, E - 1] = inf              # in two groups (in one where there are two)
+    x[2, E - 2:] = inf                            # two in one group,
+    x[2, 1] = inf                                 # one in another
+    x[3] = -inf
+    x[3, E - 1] = inf                             # the only expert left
+    x[4, E - 1] = inf
+    x[4, 0] = float("nan")
+    x[5, gs] = inf
+    b = torch.from_numpy(np.random.default_rng(2).normal(size=E).astype(np.float32)) if bias else None
+    for top_groups in (1, 2):
+        for renormalize in (True, False):
+            _check(x, 4, score, b, n, top_groups, value, renormalize)
