@@ -154,9 +154,10 @@ __device__ __forceinline__ void load_row(const IN* __restrict__ row, int E, int 
 // +inf shares its weight among the infinite logits.
 __device__ __forceinline__ float exp_diff(float x, float m) { return x == m ? 1.0f : expf(x - m); }
 
-// 2^p for |p| <= 1022 to 2^-47 of its value, four bits more than a key keeps:
-// p = n + f with |f| <= 1/2 and the Taylor series of e^(f ln 2) to the 11th
-// power (remainder (ln 2 / 2)^12 / 12! = 2^-47.2).  A third of the library
+// 2^(n + f) for whole n and |f| <= 1/2 to 2^-46.7 of its value (2^-1074 where
+// that is more), three bits more than a key keeps: the Taylor series of
+// e^(f ln 2) to the 11th power, whose remainder (ln 2 / 2)^12 / 12! = 2^-47.2
+// weighs 2^-46.7 where the value is sqrt(1/2).  A third of the library
 // function's instructions; all of the choice's 64-bit work.
 __device__ __forceinline__ double pow2_64(double n, double f) {
   constexpr double L = 0.693147180559945309417;
@@ -176,20 +177,26 @@ __device__ __forceinline__ double pow2_64(double n, double f) {
   s = fma(s, f, 1.0);
   return ldexp(s, (int)n);
 }
-// e^x; saturates at 2^-1022 and 2^1022.  NaN stays NaN.
+// e^x for x <= 0; 0 below 2^-1075.  NaN stays NaN.  The rounding of log2(e)
+// adds |x| 2^-54 of the value: 2^-44.5 at the end of the normal numbers.
 __device__ __forceinline__ double exp_64(double x) {
   constexpr double LOG2E = 1.44269504088896340736;
-  constexpr double END = 1022.0 / LOG2E;
-  x = x != x ? x : fmin(fmax(x, -END), END);
+  x = x != x ? x : fmax(x, -800.0);
   const double n = rint(x * LOG2E);
   return pow2_64(n, fma(x, LOG2E, -n));
 }
-// 1 / d for 1 <= d <= 2^1022: the hardware's estimate (at least 2^-20) after
-// two Newton steps, each of which squares the error.
+// 1 / d for 1 <= d <= 512: the hardware's estimate (at least 2^-20) after two
+// Newton steps, each of which squares the error.
 __device__ __forceinline__ double rcp_64(double d) {
   double r = __builtin_amdgcn_rcp(d);
   r = fma(fma(-d, r, 1.0), r, r);
   return fma(fma(-d, r, 1.0), r, r);
+}
+// 1 / (1 + e^-x), by e^-|x| so that small scores keep their bits and
+// nothing saturates.
+__device__ __forceinline__ double sigmoid_64(double x) {
+  const double e = exp_64(-fabs(x)), r = rcp_64(1.0 + e);
+  return x < 0.0 ? e * r : r;
 }
 
 struct RouteArgs {
@@ -652,7 +659,7 @@ __device__ __forceinline__ void choose_exact(const RouteArgs& a, int64_t t, doub
 #pragma unroll
     for (int c = 0; c < C; c++)
 #pragma unroll
-      for (int i = 0; i < 4; i++) key[c][i] = rcp_64(1.0 + exp_64(-(double)x[c][i]));
+      for (int i = 0; i < 4; i++) key[c][i] = sigmoid_64((double)x[c][i]);
   }
   float b[C][4];
   if (SCORED) load_row<float, L, C>(a.bias, a.E, l, true, b);
@@ -691,8 +698,8 @@ __device__ __forceinline__ void choose_exact(const RouteArgs& a, int64_t t, doub
             v = v >= top_logit ? 1.0 : exp_64(v - m);
             w = w >= top_logit ? 1.0 : exp_64(w - m);
           } else {
-            v = rcp_64(1.0 + exp_64(-v));
-            w = rcp_64(1.0 + exp_64(-w));
+            v = sigmoid_64(v);
+            w = sigmoid_64(w);
           }
         }
         v = bad ? -1.7e308 : v + (two ? w : 0.0);

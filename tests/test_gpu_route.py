@@ -309,3 +309,29 @@ def test_infinite_logits_in_later_groups(score, value, bias, E, n):
     for top_groups in (1, 2):
         for renormalize in (True, False):
             _check(x, 4, score, b, n, top_groups, value, renormalize)
+
+
+@pytest.mark.parametrize("E,n", [(64, 4), (60, 4), (256, 2)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_scores_that_underflow_add_nothing_to_a_group(score, E, n):
+    """Scores below 2^-1075 are 0 in 64 bits: a group of two such is worth no
+    more than a group of one, and the lower index wins."""
+    gs = E // n
+    x = torch.full((4, E), -float("inf"))
+    x[:, -1] = 0.0                                # the last group's score is not 0
+    x[0, 0] = x[1, 1] = -800.0                    # group 0: one score of 0
+    if n > 2:
+        x[0, gs] = x[0, gs + 1] = -850.0          # group 1: two
+        x[1, gs:2 * gs] = torch.finfo(torch.float32).min
+    x[2, :gs] = -2000.0
+    x[3, 0] = -700.0                              # e^-700 > 2 e^-701, both above 2^-1022
+    if n > 2:
+        x[3, gs] = x[3, gs + 1] = -701.0
+    for bias in (None, torch.zeros(E)):
+        _check(x, 3, score, bias, n, 2)
+    if score == "softmax" and n > 2:              # e^-720 > 2 e^-725, both below 2^-1022
+        x = torch.full((2, E), -float("inf"))
+        x[:, -1] = 0.0
+        x[0, 0] = x[1, gs] = -720.0
+        x[0, gs] = x[0, gs + 1] = x[1, 0] = x[1, 1] = -725.0
+        _check(x, 3, score, None, n, 2)
