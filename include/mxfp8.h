@@ -367,7 +367,7 @@ size_t mx_route_workspace_size(int64_t T, int64_t E);
 /* Gradient of mx_route's weights with respect to the logits, for the choice
  * that was made (experts [T, top_k], -1 skipped): dlogits [T, E] of dtype
  * from dweights [T, top_k] FP32.  The bias has no gradient.  An experts entry
- * outside [0, E) is skipped.  Requires T * 16 < 2^32 besides mx_route's
+ * outside [0, E) is skipped.  Requires T <= 2^28 - 16 besides mx_route's
  * limits.  T == 0 is a no-op. */
 mx_status mx_route_backward(mx_score score, mx_dtype dtype, const float* dweights,
                             const void* logits, const int32_t* experts, int64_t T, int64_t E,
@@ -380,7 +380,7 @@ mx_status mx_route_backward(mx_score score, mx_dtype dtype, const float* dweight
  * the device and trusted: a slot outside [0, T * top_k) is skipped and
  * offsets[E] is clamped, so bad ones give wrong rows but never a bad access.
  * Its gradient is mx_combine of dy with weights = NULL.  Requires 1 <= E <=
- * 512, 1 <= top_k <= 16, T * top_k < 2^31, T * ceil(H / 512) < 2^26.
+ * 512, 1 <= top_k <= 16, T * top_k < 2^31, T * ceil(H / 512) <= 2^26 - 4.
  * T == 0 or H == 0 is a no-op. */
 mx_status mx_dispatch(const void* x, int64_t T, int64_t H, int64_t top_k, int64_t E,
                       const int64_t* offsets, const int32_t* slots, void* y, hipStream_t stream);

@@ -78,6 +78,9 @@ bool row_tiles_too_large(int64_t R) { return ((R + 127) / 128) * 512 >= (int64_t
 // rows * cap bytes, out-of-range loads flagged by bit 31).
 constexpr int64_t K_LIMIT = (int64_t(1) << 31) / 256;
 
+// Work-items of one launch, in whole workgroups of 256: fewer than 2^32.
+constexpr int64_t MAX_WORK_ITEMS = (int64_t(1) << 32) - 256;
+
 constexpr int64_t MAX_EXPERTS = 512, MAX_TOP_K = 16, MAX_EXPERT_GROUPS = 32;
 
 // Sizes that routing, dispatch and combine share.
@@ -97,9 +100,9 @@ mx_status check_move(int64_t T, int64_t H, int64_t E, int64_t top_k) {
   const mx_status st = check_routing(T, E, top_k);
   if (st != MX_OK) return st;
   if (H < 0) return fail(MX_ERR_INVALID_ARG, "negative row length %lld", (long long)H);
-  // one wave per token and 512 elements, fewer than 2^32 work-items
+  // one wave per token and 512 elements
   if (H > (int64_t(1) << 40) || mul_overflows(T, H / 512 + 1) ||
-      T * ((H + 511) / 512) >= (int64_t(1) << 26))
+      T * ((H + 511) / 512) > MAX_WORK_ITEMS / 64)
     return fail(MX_ERR_UNSUPPORTED_SHAPE, "%lld tokens of %lld elements exceed one launch grid",
                 (long long)T, (long long)H);
   return MX_OK;
@@ -588,7 +591,7 @@ mx_status mx_route_backward(mx_score score, mx_dtype dtype, const float* dweight
   mx_status st = check_score(score, dtype);
   if (st == MX_OK) st = check_routing(T, E, top_k);
   if (st != MX_OK) return st;
-  if (T >= (int64_t(1) << 28))
+  if (T > MAX_WORK_ITEMS / 16)                    // 16 lanes to a token
     return fail(MX_ERR_UNSUPPORTED_SHAPE, "%lld tokens exceed one launch grid", (long long)T);
   if (T == 0) return MX_OK;
   if (!dweights || !logits || !experts || !dlogits)
@@ -662,7 +665,7 @@ mx_status mx_combine_backward(const void* dout, const void* y, int64_t T, int64_
   g_err[0] = '\0';
   mx_status st = check_move(T, H, E, top_k);
   if (st != MX_OK) return st;
-  if (T >= (int64_t(1) << 24))
+  if (T > MAX_WORK_ITEMS / 256)                   // a workgroup to a token
     return fail(MX_ERR_UNSUPPORTED_SHAPE, "%lld tokens exceed one launch grid", (long long)T);
   if (T == 0) return MX_OK;
   if (!offsets || !slots || !weights || !dweights || (H > 0 && (!dout || !y || !dy)))

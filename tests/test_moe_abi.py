@@ -156,3 +156,29 @@ def test_binding_refuses_cpu_tensors_and_unknown_names():
                  lambda: mx.route_backward(x, x, x)):
         with pytest.raises(TypeError):
             call()
+
+
+# Sizes at which a launch grid, rounded up to whole workgroups of 256
+# work-items, would hold 2^32 of them.  The last size that fits is told from
+# the first that does not by what comes next: the check for NULL pointers.
+
+@pytest.mark.parametrize("over,status", [(0, INVALID), (1, SHAPE), (2, SHAPE), (3, SHAPE)])
+def test_move_grid_limit(over, status):
+    T = (1 << 26) - 4 + over                                              # rows of 512: one wave a token
+    assert mx.mx_dispatch(0, T, 512, 1, 8, 0, 0, 0, 0) == status
+    assert mx.mx_dispatch_quant(0, 0, T, 512, 1, 8, 0, 0, 0, 0, 0) == status
+    assert mx.mx_combine(0, T, 512, 1, 0, 0, 0, 0, 0) == status
+    # three waves a token: 3 T <= 2^26 - 4
+    assert mx.mx_dispatch(0, 22369620 + over, 1025, 1, 8, 0, 0, 0, 0) == status
+
+
+@pytest.mark.parametrize("over,status", [(0, INVALID), (1, SHAPE), (15, SHAPE)])
+def test_route_backward_grid_limit(over, status):
+    T = (1 << 28) - 16 + over
+    assert mx.mx_route_backward(0, 1, 0, 0, 0, T, 8, 1, 1, 1.0, 0, 0) == status
+
+
+@pytest.mark.parametrize("over,status", [(0, INVALID), (1, SHAPE)])
+def test_combine_backward_grid_limit(over, status):
+    T = (1 << 24) - 1 + over                                              # a workgroup a token
+    assert mx.mx_combine_backward(0, 0, T, 64, 1, 8, 0, 0, 0, 0, 0, 0) == status
