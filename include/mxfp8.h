@@ -397,7 +397,8 @@ mx_status mx_dispatch_quant(mx_elem_type elem, const void* x, int64_t T, int64_t
 /* Expert rows back to the tokens: out[t] = residual[t] + sum_j w[t][j]
  * y[slots[t][j]], added in FP32 in the order of the choices and rounded once.
  * y: BF16 [T * top_k, H]; weights: FP32 [T, top_k] or NULL for ones;
- * residual: BF16 [T, H] or NULL; out: BF16 [T, H], may be residual itself.
+ * residual: BF16 [T, H] or NULL; out: BF16 [T, H], may be residual itself and
+ * shares no other memory with an input (MX_ERR_INVALID_ARG).
  * A slot outside [0, T * top_k) adds nothing.  Limits as mx_dispatch. */
 mx_status mx_combine(const void* y, int64_t T, int64_t H, int64_t top_k, const int32_t* slots,
                      const float* weights, const void* residual, void* out, hipStream_t stream);

@@ -726,7 +726,8 @@ def dispatch_quant(x, routing, elem: str = "e4m3"):
 def combine(y, routing, residual=None, weighted: bool = True, out=None):
     """Expert rows back to the tokens: y BF16 [T k, H] -> BF16 [T, H],
     out[t] = residual[t] + sum_j weights[t, j] y[slots[t, j]] (weights of one
-    with weighted=False).  out may be residual."""
+    with weighted=False).  out may be residual itself; other memory of the
+    inputs it may not share."""
     torch = _torch()
     T, k, _ = _routed(routing, weighted)
     _need(y, torch.bfloat16, "y", 2)

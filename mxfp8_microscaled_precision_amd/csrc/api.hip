@@ -108,6 +108,11 @@ mx_status check_move(int64_t T, int64_t H, int64_t E, int64_t top_k) {
   return MX_OK;
 }
 
+bool share_memory(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  return a && b && (uintptr_t)a < (uintptr_t)b + (uintptr_t)b_bytes &&
+         (uintptr_t)b < (uintptr_t)a + (uintptr_t)a_bytes;
+}
+
 // The tensors of a gradient list; with `apart`, that no two share memory.
 mx_status check_tensors(int64_t n, const void* const* tensors, const int64_t* numels,
                         const mx_dtype* dtypes, bool apart) {
@@ -651,6 +656,13 @@ mx_status mx_combine(const void* y, int64_t T, int64_t H, int64_t top_k, const i
   if (st != MX_OK) return st;
   if (T == 0 || H == 0) return MX_OK;
   if (!y || !slots || !out) return fail(MX_ERR_INVALID_ARG, "y, slots or out is NULL");
+  // waves read while others have written; an element of the residual is read
+  // by the lane that writes its place, before it does
+  const int64_t row = 2 * H, P = T * top_k;
+  if (share_memory(out, T * row, y, P * row) || share_memory(out, T * row, slots, 4 * P) ||
+      share_memory(out, T * row, weights, 4 * P) ||
+      (out != residual && share_memory(out, T * row, residual, T * row)))
+    return fail(MX_ERR_INVALID_ARG, "out shares memory with an input (only residual itself may be out)");
   int dev;
   st = current_device(&dev);
   if (st != MX_OK) return st;

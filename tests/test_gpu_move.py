@@ -233,3 +233,17 @@ def test_refusals():
     ]:
         with pytest.raises(kind):
             call()
+
+
+def test_combine_refuses_an_output_that_shares_memory():
+    """With one choice y and out have one shape, and views overlap in part."""
+    r, _, _, _ = _routing(4, 8, 1, 1)
+    buf = torch.zeros((6, 64), dtype=torch.bfloat16, device="cuda")
+    y, res = buf[:4], torch.zeros((5, 64), dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: mx.combine(y, r, out=y), lambda: mx.combine(y, r, out=buf[2:]),
+                 lambda: mx.combine(y, r, res[:4], out=res[1:])):
+        with pytest.raises(mx.MXError, match="shares memory"):
+            call()
+    mx.combine(y[:4], r, res[:4], out=res[:4])
+    two = torch.zeros((8, 64), dtype=torch.bfloat16, device="cuda")       # neighbours do not overlap
+    mx.combine(two[:4], r, out=two[4:])

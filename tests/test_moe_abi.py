@@ -182,3 +182,23 @@ def test_route_backward_grid_limit(over, status):
 def test_combine_backward_grid_limit(over, status):
     T = (1 << 24) - 1 + over                                              # a workgroup a token
     assert mx.mx_combine_backward(0, 0, T, 64, 1, 8, 0, 0, 0, 0, 0, 0) == status
+
+
+@pytest.mark.parametrize("where", ["start", "end", "inside", "same"])
+def test_combine_refuses_an_output_that_shares_memory(where):
+    """y is read by other waves after out's rows are written, so out may not
+    share memory with y, slots or weights, nor with a part of residual."""
+    # T = 4, H = 64, k = 2: out and residual 512 bytes, y 1024, slots and weights 32
+    far = {"y": 0x100000, "slots": 0x200000, "weights": 0x300000, "residual": 0x400000}
+    size = {"y": 1024, "slots": 32, "weights": 32, "residual": 512}
+
+    def call(out):
+        return mx.mx_combine(far["y"], 4, 64, 2, far["slots"], far["weights"], far["residual"], out, 0)
+
+    for name in far:
+        lo, hi = far[name], far[name] + size[name]
+        out = {"start": lo - 510, "end": hi - 2, "inside": lo + 2, "same": lo}[where]
+        if name == "residual" and where == "same":
+            continue                                                      # allowed, whole
+        assert call(out) == INVALID, name
+        assert "shares memory" in mx.mx_last_error()
