@@ -291,6 +291,12 @@ def _stream(device):
     return torch._C._cuda_getCurrentRawStream(index)
 
 
+def _written(tensors):
+    """Counts a write into a caller's tensors, so that a backward pass that
+    has saved one raises instead of using the new values."""
+    _torch().autograd.graph.increment_version(tensors)
+
+
 def _need(t, dtype, name, ndim=None):
     torch = _torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -736,14 +742,17 @@ def combine(y, routing, residual=None, weighted: bool = True, out=None):
     if residual is not None:
         _need(residual, torch.bfloat16, "residual", 2)
         _shape(residual, (T, H), "residual")
-    if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=y.device)
-    else:
+    given = out is not None
+    if given:
         _need(out, torch.bfloat16, "out", 2)
         _shape(out, (T, H), "out")
+    else:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=y.device)
     _check(mx_combine(_ptr(y), T, H, k, _ptr(routing.slots),
                       _ptr(routing.weights) if weighted else None, _ptr(residual), _ptr(out),
                       _stream(y.device)))
+    if given:
+        _written(out)
     return out
 
 
@@ -816,4 +825,5 @@ def grad_clip(tensors, max_norm: float):
     device = tensors[0].device if tensors else _torch().device("cuda")
     norm, ws, nws = _norm_buffers(n, device)
     _check(mx_grad_clip(n, ptrs, sizes, codes, max_norm, _ptr(norm), _ptr(ws), nws, _stream(device)))
+    _written(tensors)
     return norm

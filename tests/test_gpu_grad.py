@@ -141,3 +141,24 @@ def test_refusals():
         with pytest.raises(kind):
             call()
     mx.grad_norm([a, a])              # reading twice is no fault
+
+
+def test_clipping_is_seen_by_autograd():
+    """Scaling a tensor that a backward pass has saved makes that pass raise,
+    as for any write in place; reading its norm does not.  Tensors of
+    inference mode have no version and are clipped as they are."""
+    t = torch.full((100,), 2.0, device="cuda")
+    u = torch.full((40000,), 2.0, device="cuda").to(torch.bfloat16)
+    w = torch.ones((100,), device="cuda", requires_grad=True)
+    loss = (w * t).sum()
+    versions = t._version, u._version
+    mx.grad_norm([t, u])
+    assert (t._version, u._version) == versions
+    mx.grad_clip([t, u], 1.0)
+    assert t._version > versions[0] and u._version > versions[1]
+    with pytest.raises(RuntimeError, match="inplace"):
+        loss.backward()
+    with torch.inference_mode():
+        free = torch.full((100,), 2.0, device="cuda")
+    assert float(mx.grad_clip([free], 1.0)) == 20.0
+    assert (free < 2.0).all()

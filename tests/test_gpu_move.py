@@ -247,3 +247,22 @@ def test_combine_refuses_an_output_that_shares_memory():
     mx.combine(y[:4], r, res[:4], out=res[:4])
     two = torch.zeros((8, 64), dtype=torch.bfloat16, device="cuda")       # neighbours do not overlap
     mx.combine(two[:4], r, out=two[4:])
+
+
+def test_combine_into_a_tensor_is_seen_by_autograd():
+    """Writing into a tensor that a backward pass has saved makes that pass
+    raise, as for any write in place; tensors of inference mode have no
+    version and are taken as they are."""
+    r, _, _, _ = _routing(4, 8, 2, 1)
+    y, out = _bf16((8, 64), 1).cuda(), torch.zeros((4, 64), dtype=torch.bfloat16, device="cuda")
+    w = torch.ones((4, 64), dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    loss = (w * out).sum()
+    version = out._version
+    want = mx.combine(y, r)
+    assert torch.equal(mx.combine(y, r, out=out), want)
+    assert out._version > version
+    with pytest.raises(RuntimeError, match="inplace"):
+        loss.backward()
+    with torch.inference_mode():
+        free = torch.zeros_like(out)
+    assert torch.equal(mx.combine(y, r, out=free), want)
