@@ -378,7 +378,8 @@ mx_status mx_route_backward(mx_score score, mx_dtype dtype, const float* dweight
  * rows offsets[E] .. T * top_k - 1 zero.  x: BF16 [T, H], y: BF16
  * [T * top_k, H]; offsets, slots as mx_route writes them.  They are read on
  * the device and trusted: a slot outside [0, T * top_k) is skipped and
- * offsets[E] is clamped, so bad ones give wrong rows but never a bad access.
+ * offsets[E] is clamped, so bad ones give wrong rows but never a bad access,
+ * and a row below offsets[E] that no slot names is left unwritten.
  * Its gradient is mx_combine of dy with weights = NULL.  Requires 1 <= E <=
  * 512, 1 <= top_k <= 16, T * top_k < 2^31, T * ceil(H / 512) <= 2^26 - 4.
  * T == 0 or H == 0 is a no-op. */

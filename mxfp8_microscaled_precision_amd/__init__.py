@@ -592,7 +592,8 @@ class Routing(NamedTuple):
 
     weights [T, k] FP32, experts [T, k] INT32 (-1: no expert left), offsets
     [E + 1] INT64 (``grouped_gemm``'s), slots [T, k] INT32: the row of each
-    choice in the expert order, -1 where there is none.
+    choice in the expert order, -1 where there is none; the choices' rows are
+    0 .. offsets[E] - 1, each taken once.
     """
     weights: Any
     experts: Any
@@ -699,8 +700,14 @@ def _routed(routing, weights: bool = False):
 
 def dispatch(x, routing):
     """Token rows in the expert order: x BF16 [T, H] -> BF16 [T k, H] with
-    row slots[t, j] = x[t]; rows that no choice takes are zero.  Its gradient
-    is ``combine(dy, routing, weighted=False)``."""
+    row slots[t, j] = x[t], rows offsets[E] and on zero.  Its gradient is
+    ``combine(dy, routing, weighted=False)``.
+
+    The rows below offsets[E] are the choices', as ``route`` lays them out.  A
+    choice taken out of slots alone (-1) leaves its row there unwritten, with
+    what the memory held: the experts' products and weight gradients would
+    read it.  To drop choices, number the ones left anew, in offsets and
+    slots."""
     torch = _torch()
     T, k, E = _routed(routing)
     _need(x, torch.bfloat16, "x", 2)
@@ -714,7 +721,8 @@ def dispatch(x, routing):
 
 def dispatch_quant(x, routing, elem: str = "e4m3"):
     """``quant(dispatch(x, routing), "row", elem)`` in one pass: (q [T k, H]
-    u8, s [T k, H/32] u8), ``grouped_gemm``'s a and sa."""
+    u8, s [T k, H/32] u8), ``grouped_gemm``'s a and sa.  offsets and slots as
+    for ``dispatch``."""
     torch = _torch()
     if elem not in ELEM_TYPES:
         raise ValueError(f"unknown element type {elem!r}; expected one of {list(ELEM_TYPES)}")
@@ -759,7 +767,7 @@ def combine(y, routing, residual=None, weighted: bool = True, out=None):
 def combine_backward(dout, y, routing):
     """Gradient of ``combine``: (dy BF16 [T k, H], dweights FP32 [T, k]) from
     dout BF16 [T, H] and the y that was combined.  The residual's gradient is
-    dout."""
+    dout.  offsets and slots as for ``dispatch``, whose zero rows dy has."""
     torch = _torch()
     T, k, E = _routed(routing, True)
     _need(dout, torch.bfloat16, "dout", 2)

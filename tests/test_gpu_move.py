@@ -266,3 +266,26 @@ def test_combine_into_a_tensor_is_seen_by_autograd():
     with torch.inference_mode():
         free = torch.zeros_like(out)
     assert torch.equal(mx.combine(y, r, out=free), want)
+
+
+def test_choices_dropped_and_numbered_anew():
+    """A choice taken out of slots alone leaves the rows of the others as they
+    are; numbered anew, the rows that are left over are zero."""
+    r, _, slots, w = _routing(50, 8, 2, 4)
+    x, y = _bf16((50, 64), 1), _bf16((100, 64), 2)
+    e = host(r.experts).copy()
+    e[::7, 1] = -1
+    holes = np.where(e < 0, -1, slots)
+    named = holes[holes >= 0]
+    want = P.dispatch(bits(x), holes)
+    got = bits(mx.dispatch(x.cuda(), r._replace(slots=dev(holes))))
+    np.testing.assert_array_equal(got[named], want[named])
+    off, anew = P.layout(e, 8)
+    rr = mx.Routing(dev(np.where(e < 0, 0.0, w).astype(np.float32)), dev(e), dev(off), dev(anew))
+    np.testing.assert_array_equal(bits(mx.dispatch(x.cuda(), rr)), P.dispatch(bits(x), anew))
+    used = int(off[-1])
+    q, s = mx.dispatch_quant(x.cuda(), rr)
+    dy, dw = mx.combine_backward(x.cuda(), y.cuda(), rr)
+    assert used == named.size < 100
+    assert not host(q[used:]).any() and not host(s[used:]).any() and not host(dy[used:].float()).any()
+    assert (host(dw)[e < 0] == 0).all()
