@@ -263,15 +263,26 @@ static MoveArgs move_args(int64_t T, int64_t H, int64_t k, int64_t E, const int6
 static dim3 move_grid(const MoveArgs& a) {
   return dim3((unsigned)((a.T * a.spans + MOVE_THREADS / 64 - 1) / (MOVE_THREADS / 64)));
 }
-// Expert rows of at least `least` bytes in whole 128-byte lines are written
-// past the caches; rows that share a line with the next are merged in L2.
-// Measured, plain against streaming stores: dispatch 133 / 122 us at 16384
-// tokens x 2 x 7168, 17.6 / 16.1 at 4096 x 4 x 2048, 122 / 126 at 65536 x 8 x
-// 512; quantising 135 / 127 at 16384 x 8 x 4096, 58 / 67 at 65536 x 8 x 512;
-// combine's gradient 474 / 447 and 239 / 224 there, 55 / 65 at 8192 x 8 x 1000.
-static bool stream_rows(int64_t row_bytes, const void* y, int64_t least) {
-  return row_bytes >= least && row_bytes % 128 == 0 && (uintptr_t)y % 128 == 0;
+// Expert rows in whole 128-byte lines may be written past the caches; rows
+// that share a line with the next are merged in L2.
+static bool whole_lines(int64_t row_bytes, const void* y) {
+  return row_bytes % 128 == 0 && (uintptr_t)y % 128 == 0;
 }
+// BF16 rows are, from `least` bytes on.  Measured, plain against streaming
+// stores: dispatch 133 / 122 us at 16384 tokens x 2 x 7168, 17.6 / 16.1 at 4096
+// x 4 x 2048, 122 / 126 at 65536 x 8 x 512; combine's gradient 474 / 447 and
+// 239 / 224 there, 55 / 65 at 8192 x 8 x 1000.
+static bool stream_rows(int64_t row_bytes, const void* y, int64_t least) {
+  return row_bytes >= least && whole_lines(row_bytes, y);
+}
+// A quantised payload is, from where the 256 MiB last-level cache stops holding
+// it, whatever its rows' length (512 to 7168 bytes) and number of choices (1 to
+// 12).  Measured, plain against streaming stores: with 8 choices and rows of
+// 1024 bytes 29.2 / 32.2 us at 112 MiB, 47.4 / 54.3 at 200, 68.6 / 71.5 at 280,
+// 124 / 113 at 448; of 4096 bytes 29.6 / 31.5, 46.6 / 53.3, 69.1 / 73.3, 118 /
+// 112; with 4 choices 78.7 / 82.0 at 280, 101 / 94 at 320.  Below 64 MiB either
+// is ahead by up to 10%.
+constexpr int64_t QUANT_STREAM_BYTES = (int64_t)300 << 20;
 
 hipError_t launch_dispatch(const void* x, int64_t T, int64_t H, int64_t k, int64_t E,
                            const int64_t* offsets, const int32_t* slots, void* y,
@@ -288,7 +299,7 @@ hipError_t launch_dispatch(const void* x, int64_t T, int64_t H, int64_t k, int64
 
 template <int EL>
 static void launch_dq(const MoveArgs& a, const void* x, void* q, void* s, hipStream_t stream) {
-  if (stream_rows(a.H, q, 4096))
+  if (a.P * a.H >= QUANT_STREAM_BYTES && whole_lines(a.H, q))
     hipLaunchKernelGGL((dispatch_quant_kernel<EL, true>), move_grid(a), dim3(MOVE_THREADS), 0, stream, a,
                        (const uint16_t*)x, (uint8_t*)q, (uint8_t*)s);
   else

@@ -289,3 +289,21 @@ def test_choices_dropped_and_numbered_anew():
     assert used == named.size < 100
     assert not host(q[used:]).any() and not host(s[used:]).any() and not host(dy[used:].float()).any()
     assert (host(dw)[e < 0] == 0).all()
+
+
+@pytest.mark.parametrize("T,k,H", [(20000, 8, 2048), (41001, 8, 992), (26011, 3, 4224)])
+@pytest.mark.parametrize("elem", ["e4m3", "e5m2"])
+def test_dispatch_quant_past_the_cache(T, k, H, elem):
+    """Payloads of over 300 MiB, rows in whole lines and not: the
+    bytes of quantising the dispatched rows, and zeros past them."""
+    g = torch.Generator(device="cuda").manual_seed(H)
+    e = torch.rand((T, 16), generator=g, device="cuda").argsort(1)[:, :k].to(torch.int32)
+    e[::5, k - 1] = -1
+    off, slots = P.layout(host(e), 16)
+    r = mx.Routing(torch.zeros((T, k), device="cuda"), e.contiguous(), dev(off), dev(slots))
+    x = torch.randn((T, H), generator=g, device="cuda").to(torch.bfloat16)
+    q, s = mx.dispatch_quant(x, r, elem)
+    y = mx.dispatch(x, r)
+    rq, rs = mx.quant(y, "row", elem)
+    assert torch.equal(q, rq) and torch.equal(s, rs)
+    assert not q[int(off[-1]):].any()
