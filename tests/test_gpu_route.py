@@ -335,3 +335,36 @@ def test_scores_that_underflow_add_nothing_to_a_group(score, E, n):
         x[0, 0] = x[1, gs] = -720.0
         x[0, gs] = x[0, gs + 1] = x[1, 0] = x[1, 1] = -725.0
         _check(x, 3, score, None, n, 2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,n,tn", [
+    (700, 64, 8, 1, 1), (1500, 256, 8, 8, 4), (333, 60, 5, 6, 2), (200, 512, 12, 1, 1),
+])
+def test_bfloat16_logits_with_a_bias(score, T, E, k, n, tn):
+    """BF16 logits tie often; the bias orders what they leave equal."""
+    x = _logits(T, E, T + E, "bfloat16", mask=0.05)
+    bias = torch.from_numpy((0.05 * np.random.default_rng(k).normal(size=E)).astype(np.float32))
+    _check(x, k, score, bias, n, tn, scale=2.5)
+    _check(x, k, score, bias, n, tn, "max", renormalize=False)
+    _check(x, k, score, (bias * 64).round() / 64, n, tn)    # a bias of few values: ties again
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_groups_with_a_bias_over_many_workgroups(dtype):
+    x = _logits(20011, 128, 6, dtype, mask=0.02)
+    bias = torch.from_numpy((0.1 * np.random.default_rng(3).normal(size=128)).astype(np.float32))
+    _check(x, 8, "sigmoid", bias, 8, 4, scale=2.5)
+    _check(x, 6, "softmax", bias, 4, 2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,n", [(128, 2), (256, 2), (512, 2), (512, 4), (192, 3)])
+def test_groups_of_several_rows_of_chunks(score, E, n):
+    """Groups longer than the lanes of a token hold side by side."""
+    x = _logits(300, E, n, mask=0.1)
+    bias = torch.from_numpy((0.1 * np.random.default_rng(E).normal(size=E)).astype(np.float32))
+    for b in (None, bias):
+        for value in ("top2", "max"):
+            _check(x, 8, score, b, n, n - 1, value)
+            _check(x, 12, score, b, n, 1, value)
