@@ -2,14 +2,20 @@
 //
 //   n = sqrt(sum over all tensors of g^2),  g *= min(1, max_norm / (n + 1e-6))
 //
-// Bound by HBM bandwidth: the norm of 2.1 GB takes 325 us (6.5 TB/s), clipping
-// it 1170 (three passes, 5.4 TB/s).  The tensors are cut into pieces of 32 KiB; a launch
-// takes up to GRAD_TENSORS tensors, whose addresses travel in the kernel's
-// arguments (no table in device memory, so a captured graph holds them), and
-// its workgroups take pieces in turn.  Squares are added in 64 bits: they
-// neither overflow nor underflow for any finite gradient, and the norm and
-// the scaled gradients are rounded once.  Every workgroup writes its sum to the workspace and the sums
-// are added in a fixed order, so the norm is the same on every run.
+// Bound by HBM bandwidth: the norm of 2.1 GB takes 328 us (6.5 TB/s), clipping
+// it 1157 (three passes, 5.5 TB/s).  The tensors are cut into pieces of 32 KiB;
+// a launch takes up to GRAD_TENSORS tensors, whose addresses travel in the
+// kernel's arguments (no table in device memory, so a captured graph holds
+// them), and its workgroups take pieces in turn.  Squares are added in 64 bits:
+// they neither overflow nor underflow for any finite gradient, and the norm and
+// the scaled gradients are rounded once.  Every workgroup writes its sum to the
+// workspace and the sums are added in a fixed order, so the norm is the same on
+// every run.
+//
+// A tensor that does not start on 16 bytes is read and written element by
+// element: 1157 us for the norm of 2.1 GB of BF16 and 2680 to clip it, 681 and
+// 1634 of FP32.  Every workgroup that scales adds up the sums of all launches,
+// which grows with the square of a list's length past 160 tensors.
 #include "mx_device.h"
 #include "mx_kernels.h"
 

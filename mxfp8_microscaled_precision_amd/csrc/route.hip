@@ -19,9 +19,11 @@
 // the lowest index and one v_max_f64 / v_min_f64 pair moves value and index
 // together.  A 32-bit logit keeps all its bits; a 64-bit v keeps 43.
 //
-// Bound by instructions where E is large and by its two dependent launches
-// where it is small: 65536 x 256 logits with bias and groups take 54 us (14 at
-// the rate of a copy), 16384 x 64 10 us, one token 4.7.
+// Bound by instructions where E is large: 65536 x 256 logits with bias and
+// groups take 55 us (14 at the rate of a copy), of which the vector units work
+// 73% of route_kernel's 45 and 46% of the place kernel's 10.  By latency where
+// it is small: 16384 x 64 take 10 us, the units working 42% and 33% of two
+// kernels of 5.5 and 4.6; one token 4.8, where filling 64 floats takes 3.9.
 #include "mx_kernels.h"
 #include "mx_rows.h"
 
@@ -468,13 +470,15 @@ __device__ __forceinline__ GroupChoice keep_groups(const RouteArgs& a, float v[C
 
 // The 32-bit choice values of a lane's logits: the logits themselves, or with
 // a bias scores and bias, whose scores err bounds the error of:
-//   sigmoid: exp2 and reciprocal are off by one step each, the argument's
-//     rounding weighs s (1 - s) |x| < 0.23 steps, 1 + e half a step: under
-//     2^-22 for s <= 1; doubled.
-//   softmax: a score p <= 1 / sum is off by 1.5 |x - m| + 3 half steps from
-//     its exponential, where p |x - m| <= 1 / (e sum); its sum by as many on
-//     average (|x - m| averages under ln E + 1) and 4 C + 4 additions: under
-//     64 half steps of 1 / sum, 2^-18 / sum; doubled.
+//   sigmoid: exp2 and reciprocal are off by one step each; the argument's
+//     rounding and log2(e)'s (0.22 half steps) weigh s (1 - s) |x| < 0.23 of
+//     1.22 half steps, 1 + e half a step: under 2^-22 for s <= 1; doubled.
+//   softmax: an exponential is off by 2.2 |x - m| half steps (difference,
+//     product, log2(e)) and a step of its own.  For a score p <= 1 / sum, where
+//     p |x - m| <= 1 / (e sum), that and the reciprocal's step make under 5 half
+//     steps of 1 / sum.  The sum is off by the exponentials' mean, where
+//     |x - m| averages at most ln E: under 16 half steps; and by at most 4 C +
+//     4 = 36 additions.  Under 64 half steps of 1 / sum, 2^-18 / sum; doubled.
 // The scores of a group's best two logits (group_value): as these, with a sum
 // of 1.
 template <int L, int C, bool SCORED>
@@ -1078,8 +1082,11 @@ size_t route_workspace(int64_t T, int64_t E) {
   return blocks > 1 ? sizeof(uint32_t) * (size_t)blocks * (size_t)((E + 1) / 2) : 0;
 }
 
-// Threads by registers: 1024 leave 128 to each, 768 170, 512 256.  Up to 16
-// tokens, 256.
+// Threads by a token's logits in a lane, 4 C, which most of the registers
+// hold: 1024 threads leave 128 to each, 768 170, 512 256.  Two variants of 9 to
+// 16 choices (KC = 16) need more than that leaves: C = 4 with a bias spills 17
+// (32768 x 256, top 12: 40.8 us), C = 8 without one 4 (32768 x 512, top 12:
+// 44.9; top 8, which does not, 36.4).  Up to 16 tokens, 256.
 template <typename IN, int L, int C, int KC, bool SCORED, int THREADS>
 static void launch_route_threads(const RouteArgs& a, hipStream_t stream) {
   if (a.T <= 16)
