@@ -77,7 +77,8 @@ typedef enum mx_quant_mode {
  * against 57344: the smallest e with amax <= 57344 * 2^e. */
 typedef enum mx_elem_type {
     MX_ELEM_E4M3 = 0,
-    MX_ELEM_E5M2 = 1
+    MX_ELEM_E5M2 = 1,
+    MX_ELEM_E2M1 = 4 /* 4 bits, two to a byte; for the calls that name it only */
 } mx_elem_type;
 
 /* Which product of a linear layer a GEMM call computes (operand roles).
@@ -434,6 +435,101 @@ mx_status mx_grad_clip(int64_t n, void* const* tensors, const int64_t* numels,
 /* Bytes of device workspace mx_grad_norm and mx_grad_clip need for n
  * tensors.  Pure host function, no HIP call; 0 for n <= 0. */
 size_t mx_grad_norm_workspace_size(int64_t n);
+
+/* ---------------------------------------------------------------------------
+ * 4-bit weights and 8-bit activation checkpoints.
+ *
+ * OCP E2M1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 as codes 0 .. 7, the sign in bit 3; two
+ * codes to a byte, element 2 i of a row in the low half of byte i.  With E2M1
+ * the scale keeps the rceil rule against 6.  E2M1 has no NaN: a block holding
+ * NaN or Inf gets scale 0xFF, which makes every product and every restored
+ * value of it NaN, and payload 0x77.
+ *
+ * Payload and BF16 pointers of these calls must be 16-byte aligned
+ * (MX_ERR_INVALID_ARG).
+ * ------------------------------------------------------------------------- */
+
+/* Dynamic MX quantisation to E2M1 of `batch` contiguous BF16 [rows, cols]
+ * matrices (the pages train routed experts in 4-bit MX: torchtitan-npu
+ * MXFP8/HiF8 tutorial, step-2 environment table, ENABLE_MXFP4_QAT):
+ *   ROW_1x32:  q [batch, rows, cols/2],   s [batch, rows, cols/32]
+ *   COL_1x32:  q_t [batch, cols, rows/2], s_t [batch, cols, rows/32]
+ *   DUAL_AXIS: both from one read of x
+ * Shape rules as mx_quant_batched.  32x32 tiles are not offered
+ * (MX_ERR_INVALID_ARG): their backward product reads the weight transposed,
+ * across the bytes that hold two codes. */
+mx_status mx_quant4(mx_quant_mode mode, const void* x, int64_t batch, int64_t rows, int64_t cols,
+                    void* q, void* s, void* q_t, void* s_t, hipStream_t stream);
+
+/* An MX tensor in row blocks back to BF16: y [rows, cols] = payload * 2^(s -
+ * 127), rounded to nearest even where BF16 does not hold it; NaN in a block
+ * of scale 0xFF.  elem: E4M3, E5M2 or E2M1 (q then [rows, cols/2]); s [rows,
+ * cols/32].  Requires cols % 32 == 0.  rows == 0 or cols == 0 is a no-op. */
+mx_status mx_dequant(mx_elem_type elem, const void* q, const void* s, int64_t rows, int64_t cols,
+                     void* y, hipStream_t stream);
+
+/* Product with a 4-bit weight: C = A * B^T, FP32 accumulation, BF16 result.
+ *   a: [M, K] E4M3 or E5M2, or [M, K/2] E2M1 (a_elem), sa [M, K/32];
+ *   b: E2M1 [N, K/2], sb [N, K/32];  c: BF16 [M, N], sharing no memory with
+ *   the operands (MX_ERR_INVALID_ARG).
+ * The forward product takes mx_quant4's row blocks of the weight, the
+ * backward one its column blocks.  Requires K % 32 == 0, K < 2^23, N < 2^28.
+ * K == 0 writes zeros; M == 0 or N == 0 is a no-op. */
+mx_status mx_gemm4(mx_elem_type a_elem, int64_t M, int64_t N, int64_t K, const void* a,
+                   const void* sa, const void* b, const void* sb, void* c, hipStream_t stream);
+
+/* mx_gemm4 over per-expert token groups: rows offsets[g] .. offsets[g+1] - 1
+ * of c are those of a times b[g]^T, b [G, N, K/2], sb [G, N, K/32].  offsets:
+ * DEVICE int64 [G+1] as in mx_grouped_gemm; rows from offsets[G] on are left
+ * as they were.  Requires 1 <= G <= 512 besides mx_gemm4's rules. */
+mx_status mx_grouped_gemm4(mx_elem_type a_elem, int64_t G, const int64_t* offsets, int64_t T,
+                           int64_t N, int64_t K, const void* a, const void* sa, const void* b,
+                           const void* sb, void* c, hipStream_t stream);
+
+/* SwiGLU between an MLP's two products, its result quantised: x BF16 [T, 2F],
+ * gates in columns 0 .. F - 1, up values in F .. 2F - 1;
+ * h = g / (1 + exp(-g)) * u, in FP32 and rounded to BF16.
+ *   q [T, F] payload of elem (E4M3 or E5M2), s [T, F/32]: the bytes of
+ *   mx_quant_elem(MX_QUANT_ROW_1x32, elem) of h, the down product's operand.
+ *   ckpt_q [T, 2F], ckpt_s [T, 2F/32]: x itself in row blocks of ckpt_elem,
+ *   the 8-bit checkpoint for the backward pass; both NULL for none.
+ * Where sigmoid(g) is below 2^-126 it counts as 0.  Requires F % 32 == 0, F <
+ * 2^33.  T == 0 or F == 0 is a no-op. */
+mx_status mx_swiglu_quant(mx_elem_type elem, mx_elem_type ckpt_elem, const void* x, int64_t T,
+                          int64_t F, void* q, void* s, void* ckpt_q, void* ckpt_s,
+                          hipStream_t stream);
+
+/* Gradient of h with respect to x, at the x that the checkpoint holds (as
+ * mx_dequant restores it): dx [T, 2F] from dh BF16 [T, F],
+ *   dg = dh u p (1 + g (1 - p)),  du = dh g p,  p = 1 / (1 + exp(-g)),
+ * in FP32 and rounded to BF16.  Limits as mx_swiglu_quant. */
+mx_status mx_swiglu_backward(mx_elem_type ckpt_elem, const void* dh, const void* ckpt_q,
+                             const void* ckpt_s, int64_t T, int64_t F, void* dx, hipStream_t stream);
+
+/* mx_swiglu_backward with dx's rows quantised on the way: q [T, 2F] payload of
+ * elem (E4M3 or E5M2), s [T, 2F/32], the bytes of mx_quant_elem(
+ * MX_QUANT_ROW_1x32, elem) of the BF16 dx: the operand of the product that
+ * gives the layer input's gradient, and the checkpoint that
+ * mx_requant_grouped_col makes the weight gradient's operand of. */
+mx_status mx_swiglu_backward_quant(mx_elem_type ckpt_elem, mx_elem_type elem, const void* dh,
+                                   const void* ckpt_q, const void* ckpt_s, int64_t T, int64_t F,
+                                   void* q, void* s, hipStream_t stream);
+
+/* Column blocks of an MX tensor that is held in row blocks: a forward
+ * product's operand, kept as the 8-bit checkpoint, becomes the operand of the
+ * weight gradient.  q [rows, cols] payload of elem (E4M3 or E5M2), s [rows,
+ * cols/32] -> q_t [cols, rows] payload of out_elem, s_t [cols, rows/32]: the
+ * bytes of mx_quant_elem(MX_QUANT_COL_1x32, out_elem) of the BF16 values that
+ * mx_dequant restores.  Shape rules as mx_quant's column mode. */
+mx_status mx_requant_col(mx_elem_type elem, mx_elem_type out_elem, const void* q, const void* s,
+                         int64_t rows, int64_t cols, void* q_t, void* s_t, hipStream_t stream);
+
+/* mx_requant_col with blocks that restart at every group offset: the bytes of
+ * mx_quant_grouped_col_elem(out_elem) of the restored values, q_t [C, cap],
+ * s_t [C, cap/32].  Layout, limits and offsets as mx_quant_grouped_col. */
+mx_status mx_requant_grouped_col(mx_elem_type elem, mx_elem_type out_elem, const void* q,
+                                 const void* s, int64_t T, int64_t C, int64_t G,
+                                 const int64_t* offsets, void* q_t, void* s_t, hipStream_t stream);
 
 #ifdef __cplusplus
 }

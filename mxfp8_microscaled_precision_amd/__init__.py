@@ -7,8 +7,11 @@ entry points; ``quant``, ``quant_batched``, ``quant_grouped_col``, ``gemm``,
 ``grouped_gemm``, ``grouped_gemm_wgrad``, ``process_quant_result`` and, around
 the experts' products, ``route``, ``route_backward``, ``dispatch``,
 ``dispatch_quant``, ``combine``, ``combine_backward``, ``grad_norm`` and
-``grad_clip`` marshal torch CUDA tensors (device memory and the current stream
-only) into those calls.  Every step of the computation runs in
+``grad_clip`` and, for 4-bit weights and 8-bit checkpoints, ``quant4``,
+``dequant``, ``gemm4``, ``grouped_gemm4``, ``swiglu_quant``,
+``swiglu_backward``, ``swiglu_backward_quant``, ``requant_col`` and
+``requant_grouped_col`` marshal torch CUDA tensors (device memory and the
+current stream only) into those calls.  Every step of the computation runs in
 the HIP kernels; there is no CPU fallback: without the built library, or on a
 device other than gfx950, every call raises.
 """
@@ -34,6 +37,10 @@ __all__ = [
     "mx_grad_norm_workspace_size", "Routing", "route", "route_backward", "dispatch",
     "dispatch_quant", "combine", "combine_backward", "grad_norm", "grad_clip", "SCORES",
     "GROUP_VALUES",
+    "mx_quant4", "mx_dequant", "mx_gemm4", "mx_grouped_gemm4", "mx_swiglu_quant",
+    "mx_swiglu_backward", "mx_swiglu_backward_quant", "mx_requant_col", "mx_requant_grouped_col",
+    "quant4", "dequant", "gemm4", "grouped_gemm4", "swiglu_quant", "swiglu_backward",
+    "swiglu_backward_quant", "requant_col", "requant_grouped_col", "OPERAND_ELEMS",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmxfp8.so")
@@ -43,6 +50,7 @@ QUANT_MODES = {"row": 0, "col": 1, "dual": 2, "32x32": 3}
 GEMM_LAYOUTS = {"fprop": 0, "dgrad": 1, "wgrad": 2}
 BSCALE_KINDS = {"1x32": 0, "32x32": 1}
 ELEM_TYPES = {"e4m3": 0, "e5m2": 1}
+OPERAND_ELEMS = {**ELEM_TYPES, "e2m1": 4}  # element types that a product's or a restored operand has
 SCORES = {"softmax": 0, "sigmoid": 1}
 GROUP_VALUES = {"top2": 0, "max": 1}
 
@@ -128,6 +136,24 @@ def lib() -> ctypes.CDLL:
         L.mx_grad_clip.argtypes = [i64, vp, vp, vp, f32, vp, vp, sz, vp]
         L.mx_grad_norm_workspace_size.restype = sz
         L.mx_grad_norm_workspace_size.argtypes = [i64]
+        L.mx_quant4.restype = c_int
+        L.mx_quant4.argtypes = [c_int, vp, i64, i64, i64, vp, vp, vp, vp, vp]
+        L.mx_dequant.restype = c_int
+        L.mx_dequant.argtypes = [c_int, vp, vp, i64, i64, vp, vp]
+        L.mx_gemm4.restype = c_int
+        L.mx_gemm4.argtypes = [c_int, i64, i64, i64, vp, vp, vp, vp, vp, vp]
+        L.mx_grouped_gemm4.restype = c_int
+        L.mx_grouped_gemm4.argtypes = [c_int, i64, vp, i64, i64, i64, vp, vp, vp, vp, vp, vp]
+        L.mx_swiglu_quant.restype = c_int
+        L.mx_swiglu_quant.argtypes = [c_int, c_int, vp, i64, i64, vp, vp, vp, vp, vp]
+        L.mx_swiglu_backward.restype = c_int
+        L.mx_swiglu_backward.argtypes = [c_int, vp, vp, vp, i64, i64, vp, vp]
+        L.mx_swiglu_backward_quant.restype = c_int
+        L.mx_swiglu_backward_quant.argtypes = [c_int, c_int, vp, vp, vp, i64, i64, vp, vp, vp]
+        L.mx_requant_col.restype = c_int
+        L.mx_requant_col.argtypes = [c_int, c_int, vp, vp, i64, i64, vp, vp, vp]
+        L.mx_requant_grouped_col.restype = c_int
+        L.mx_requant_grouped_col.argtypes = [c_int, c_int, vp, vp, i64, i64, i64, vp, vp, vp, vp]
         _lib = L
     return _lib
 
@@ -263,6 +289,42 @@ def mx_grad_clip(n, tensors, numels, dtypes, max_norm, norm, workspace, workspac
 
 def mx_grad_norm_workspace_size(n) -> int:
     return lib().mx_grad_norm_workspace_size(n)
+
+
+def mx_quant4(mode, x, batch, rows, cols, q, s, q_t, s_t, stream) -> int:
+    return lib().mx_quant4(mode, x, batch, rows, cols, q, s, q_t, s_t, stream)
+
+
+def mx_dequant(elem, q, s, rows, cols, y, stream) -> int:
+    return lib().mx_dequant(elem, q, s, rows, cols, y, stream)
+
+
+def mx_gemm4(a_elem, M, N, K, a, sa, b, sb, c, stream) -> int:
+    return lib().mx_gemm4(a_elem, M, N, K, a, sa, b, sb, c, stream)
+
+
+def mx_grouped_gemm4(a_elem, G, offsets, T, N, K, a, sa, b, sb, c, stream) -> int:
+    return lib().mx_grouped_gemm4(a_elem, G, offsets, T, N, K, a, sa, b, sb, c, stream)
+
+
+def mx_swiglu_quant(elem, ckpt_elem, x, T, F, q, s, ckpt_q, ckpt_s, stream) -> int:
+    return lib().mx_swiglu_quant(elem, ckpt_elem, x, T, F, q, s, ckpt_q, ckpt_s, stream)
+
+
+def mx_swiglu_backward(ckpt_elem, dh, ckpt_q, ckpt_s, T, F, dx, stream) -> int:
+    return lib().mx_swiglu_backward(ckpt_elem, dh, ckpt_q, ckpt_s, T, F, dx, stream)
+
+
+def mx_swiglu_backward_quant(ckpt_elem, elem, dh, ckpt_q, ckpt_s, T, F, q, s, stream) -> int:
+    return lib().mx_swiglu_backward_quant(ckpt_elem, elem, dh, ckpt_q, ckpt_s, T, F, q, s, stream)
+
+
+def mx_requant_col(elem, out_elem, q, s, rows, cols, q_t, s_t, stream) -> int:
+    return lib().mx_requant_col(elem, out_elem, q, s, rows, cols, q_t, s_t, stream)
+
+
+def mx_requant_grouped_col(elem, out_elem, q, s, T, C, G, offsets, q_t, s_t, stream) -> int:
+    return lib().mx_requant_grouped_col(elem, out_elem, q, s, T, C, G, offsets, q_t, s_t, stream)
 
 
 def _check(status: int):
@@ -835,3 +897,229 @@ def grad_clip(tensors, max_norm: float):
     _check(mx_grad_clip(n, ptrs, sizes, codes, max_norm, _ptr(norm), _ptr(ws), nws, _stream(device)))
     _written(tensors)
     return norm
+
+
+# ---------------------------------------------------------------------------
+# 4-bit weights and 8-bit activation checkpoints
+# ---------------------------------------------------------------------------
+
+def _elem(name, known, what="element type"):
+    if name not in known:
+        raise ValueError(f"unknown {what} {name!r}; expected one of {list(known)}")
+    return known[name]
+
+
+def _out(out, shape, device):
+    """(result tensor, whether the caller gave it) of a BF16 product."""
+    torch = _torch()
+    if out is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=device), False
+    _need(out, torch.bfloat16, "out", len(shape))
+    _shape(out, shape, "out")
+    return out, True
+
+
+def quant4(x, mode: str = "row"):
+    """Dynamic MX quantisation of a BF16 [rows, cols] tensor, or of a stack
+    [B, rows, cols], to 4 bits (E2M1, two codes to a byte, element 2i in the
+    low half of byte i).
+
+    mode "row"  -> (q [rows, cols/2], s [rows, cols/32])
+         "col"  -> (q_t [cols, rows/2], s_t [cols, rows/32])
+         "dual" -> (q, s, q_t, s_t)
+    each with a leading B for a stack.
+    """
+    torch = _torch()
+    if mode not in QUANT_MODES or mode == "32x32":
+        raise ValueError(f"unknown 4-bit quantisation mode {mode!r}; expected 'row', 'col' or 'dual'")
+    _need(x, torch.bfloat16, "x")
+    if x.dim() not in (2, 3):
+        raise ValueError(f"x must have 2 or 3 dims, got {x.dim()}")
+    R, C = x.shape[-2:]
+    lead = tuple(x.shape[:-2])
+    q = s = qt = st = None
+    if mode != "col":
+        q = torch.empty(lead + (R, C // 2), dtype=torch.uint8, device=x.device)
+        s = torch.empty(lead + (R, C // 32), dtype=torch.uint8, device=x.device)
+    if mode != "row":
+        qt = torch.empty(lead + (C, R // 2), dtype=torch.uint8, device=x.device)
+        st = torch.empty(lead + (C, R // 32), dtype=torch.uint8, device=x.device)
+    _check(mx_quant4(QUANT_MODES[mode], _ptr(x), lead[0] if lead else 1, R, C, _ptr(q), _ptr(s),
+                     _ptr(qt), _ptr(st), _stream(x.device)))
+    if mode == "row":
+        return q, s
+    return (qt, st) if mode == "col" else (q, s, qt, st)
+
+
+def dequant(q, s, elem: str = "e4m3"):
+    """An MX tensor in row blocks back to BF16 [..., cols]: q u8 [..., cols]
+    ("e4m3", "e5m2") or [..., cols/2] ("e2m1"), s u8 [..., cols/32]."""
+    torch = _torch()
+    code = _elem(elem, OPERAND_ELEMS)
+    _need(q, torch.uint8, "q")
+    _need(s, torch.uint8, "s")
+    if q.dim() < 1:
+        raise ValueError("q must have at least one dim")
+    lead = tuple(q.shape[:-1])
+    C = q.shape[-1] * (2 if elem == "e2m1" else 1)
+    if C % 32 == 0:
+        _shape(s, lead + (C // 32,), "s")
+    y = torch.empty(lead + (C,), dtype=torch.bfloat16, device=q.device)
+    rows = 1
+    for d in lead:
+        rows *= d
+    _check(mx_dequant(code, _ptr(q), _ptr(s), rows, C, _ptr(y), _stream(q.device)))
+    return y
+
+
+def gemm4(a, sa, b, sb, a_elem: str = "e4m3", out=None):
+    """Product with a 4-bit weight, C = A * B^T (FP32 accumulation, BF16
+    result): a u8 [M, K] ("e4m3", "e5m2") or [M, K/2] ("e2m1") with sa [M,
+    K/32], b u8 [N, K/2] with sb [N, K/32], both as ``quant4`` lays them out.
+    For the forward pass b is the weight's row blocks, for the input's
+    gradient its column blocks.  out may share no memory with the operands."""
+    torch = _torch()
+    code = _elem(a_elem, OPERAND_ELEMS)
+    for t, n in ((a, "a"), (sa, "sa"), (b, "b"), (sb, "sb")):
+        _need(t, torch.uint8, n, 2)
+    M, N = a.shape[0], b.shape[0]
+    K = a.shape[1] * (2 if a_elem == "e2m1" else 1)
+    if K % 32 == 0:
+        _shape(sa, (M, K // 32), "sa")
+        _shape(b, (N, K // 2), "b")
+        _shape(sb, (N, K // 32), "sb")
+    out, given = _out(out, (M, N), a.device)
+    _check(mx_gemm4(code, M, N, K, _ptr(a), _ptr(sa), _ptr(b), _ptr(sb), _ptr(out),
+                    _stream(a.device)))
+    if given:
+        _written(out)
+    return out
+
+
+def grouped_gemm4(offsets, a, sa, b, sb, a_elem: str = "e4m3", out=None):
+    """``gemm4`` over per-expert token groups: rows offsets[g]:offsets[g+1] of
+    a times b[g]^T, b u8 [G, N, K/2] with sb [G, N, K/32]; offsets int64 [G+1]
+    on the device.  Returns BF16 [T, N]; rows from offsets[G] on are not
+    written."""
+    torch = _torch()
+    code = _elem(a_elem, OPERAND_ELEMS)
+    _need(offsets, torch.int64, "offsets", 1)
+    for t, n in ((a, "a"), (sa, "sa")):
+        _need(t, torch.uint8, n, 2)
+    for t, n in ((b, "b"), (sb, "sb")):
+        _need(t, torch.uint8, n, 3)
+    G, T, N = offsets.numel() - 1, a.shape[0], b.shape[1]
+    K = a.shape[1] * (2 if a_elem == "e2m1" else 1)
+    if G < 1:
+        raise ValueError("offsets must hold at least two entries (one group)")
+    if K % 32 == 0:
+        _shape(sa, (T, K // 32), "sa")
+        _shape(b, (G, N, K // 2), "b")
+        _shape(sb, (G, N, K // 32), "sb")
+    out, given = _out(out, (T, N), a.device)
+    _check(mx_grouped_gemm4(code, G, _ptr(offsets), T, N, K, _ptr(a), _ptr(sa), _ptr(b), _ptr(sb),
+                            _ptr(out), _stream(a.device)))
+    if given:
+        _written(out)
+    return out
+
+
+def swiglu_quant(gate_up, elem: str = "e4m3", checkpoint: bool = True, checkpoint_elem: str = "e4m3"):
+    """SwiGLU between an MLP's two products: gate_up BF16 [T, 2F] (gates
+    first) -> (q u8 [T, F], s u8 [T, F/32], ckpt), h = silu(gate) * up in row
+    blocks, the bytes of ``quant(h, "row", elem)`` for h rounded to BF16.
+    ckpt is gate_up itself in 8 bits, (u8 [T, 2F], u8 [T, 2F/32]), for
+    ``swiglu_backward``; None with checkpoint=False."""
+    torch = _torch()
+    code, ckpt_code = _elem(elem, ELEM_TYPES), _elem(checkpoint_elem, ELEM_TYPES)
+    _need(gate_up, torch.bfloat16, "gate_up", 2)
+    T, F2 = gate_up.shape
+    if F2 % 2:
+        raise ValueError(f"gate_up must have an even number of columns, got {F2}")
+    u8, dev = torch.uint8, gate_up.device
+    q = torch.empty((T, F2 // 2), dtype=u8, device=dev)
+    s = torch.empty((T, F2 // 64), dtype=u8, device=dev)
+    cq = torch.empty((T, F2), dtype=u8, device=dev) if checkpoint else None
+    cs = torch.empty((T, F2 // 32), dtype=u8, device=dev) if checkpoint else None
+    _check(mx_swiglu_quant(code, ckpt_code, _ptr(gate_up), T, F2 // 2, _ptr(q), _ptr(s),
+                           _ptr(cq) if checkpoint and T else None,
+                           _ptr(cs) if checkpoint and T else None, _stream(dev)))
+    return q, s, ((cq, cs) if checkpoint else None)
+
+
+def _swiglu_operands(dh, ckpt_q, ckpt_s):
+    torch = _torch()
+    _need(dh, torch.bfloat16, "dh", 2)
+    _need(ckpt_q, torch.uint8, "ckpt_q", 2)
+    _need(ckpt_s, torch.uint8, "ckpt_s", 2)
+    T, F = dh.shape
+    _shape(ckpt_q, (T, 2 * F), "ckpt_q")
+    if F % 32 == 0:
+        _shape(ckpt_s, (T, F // 16), "ckpt_s")
+    return T, F
+
+
+def swiglu_backward(dh, ckpt_q, ckpt_s, checkpoint_elem: str = "e4m3"):
+    """Gradient of the SwiGLU at the gate_up that the 8-bit checkpoint holds:
+    dh BF16 [T, F] -> d gate_up BF16 [T, 2F]."""
+    torch = _torch()
+    code = _elem(checkpoint_elem, ELEM_TYPES)
+    T, F = _swiglu_operands(dh, ckpt_q, ckpt_s)
+    dx = torch.empty((T, 2 * F), dtype=torch.bfloat16, device=dh.device)
+    _check(mx_swiglu_backward(code, _ptr(dh), _ptr(ckpt_q), _ptr(ckpt_s), T, F, _ptr(dx),
+                              _stream(dh.device)))
+    return dx
+
+
+def swiglu_backward_quant(dh, ckpt_q, ckpt_s, elem: str = "e4m3", checkpoint_elem: str = "e4m3"):
+    """``quant(swiglu_backward(...), "row", elem)`` in one pass: (q u8 [T, 2F],
+    s u8 [T, 2F/32]), the operand of the input's gradient, and of
+    ``requant_grouped_col`` for the weight's."""
+    torch = _torch()
+    code, ckpt_code = _elem(elem, ELEM_TYPES), _elem(checkpoint_elem, ELEM_TYPES)
+    T, F = _swiglu_operands(dh, ckpt_q, ckpt_s)
+    q = torch.empty((T, 2 * F), dtype=torch.uint8, device=dh.device)
+    s = torch.empty((T, F // 16), dtype=torch.uint8, device=dh.device)
+    _check(mx_swiglu_backward_quant(ckpt_code, code, _ptr(dh), _ptr(ckpt_q), _ptr(ckpt_s), T, F,
+                                    _ptr(q), _ptr(s), _stream(dh.device)))
+    return q, s
+
+
+def requant_col(q, s, elem: str = "e4m3", out_elem: str = "e4m3"):
+    """``quant(dequant(q, s, elem), "col", out_elem)`` in one pass over the
+    8-bit data: a forward product's operand (row blocks), kept as the
+    checkpoint, as the weight gradient's (q_t u8 [cols, rows], s_t u8 [cols,
+    rows/32])."""
+    torch = _torch()
+    code, out_code = _elem(elem, ELEM_TYPES), _elem(out_elem, ELEM_TYPES)
+    _need(q, torch.uint8, "q", 2)
+    _need(s, torch.uint8, "s", 2)
+    R, C = q.shape
+    if C % 32 == 0:
+        _shape(s, (R, C // 32), "s")
+    qt = torch.empty((C, R), dtype=torch.uint8, device=q.device)
+    st = torch.empty((C, R // 32), dtype=torch.uint8, device=q.device)
+    _check(mx_requant_col(code, out_code, _ptr(q), _ptr(s), R, C, _ptr(qt), _ptr(st),
+                          _stream(q.device)))
+    return qt, st
+
+
+def requant_grouped_col(q, s, offsets, elem: str = "e4m3", out_elem: str = "e4m3"):
+    """``quant_grouped_col(dequant(q, s, elem), offsets, out_elem)`` in one
+    pass over the 8-bit data: q u8 [T, C], s u8 [T, C/32], offsets int64 [G+1]
+    on the device -> (q_t u8 [C, cap], s_t u8 [C, cap/32])."""
+    torch = _torch()
+    code, out_code = _elem(elem, ELEM_TYPES), _elem(out_elem, ELEM_TYPES)
+    _need(q, torch.uint8, "q", 2)
+    _need(s, torch.uint8, "s", 2)
+    _need(offsets, torch.int64, "offsets", 1)
+    T, C = q.shape
+    if C % 32 == 0:
+        _shape(s, (T, C // 32), "s")
+    G = offsets.numel() - 1
+    cap = grouped_col_capacity(T, G)
+    qt = torch.empty((C, cap), dtype=torch.uint8, device=q.device)
+    st = torch.empty((C, cap // 32), dtype=torch.uint8, device=q.device)
+    _check(mx_requant_grouped_col(code, out_code, _ptr(q), _ptr(s), T, C, G, _ptr(offsets), _ptr(qt),
+                                  _ptr(st), _stream(q.device)))
+    return qt, st

@@ -158,6 +158,91 @@ mx_status check_score(mx_score score, mx_dtype dtype) {
   return MX_OK;
 }
 
+bool is_fp8(mx_elem_type e) { return e == MX_ELEM_E4M3 || e == MX_ELEM_E5M2; }
+bool is_elem(mx_elem_type e) { return is_fp8(e) || e == MX_ELEM_E2M1; }
+
+// The kernels for 4-bit weights and checkpoints move 16 bytes at a time.
+bool misaligned(const void* p) { return ((uintptr_t)p & 15) != 0; }
+
+constexpr int64_t GEMM4_N_LIMIT = int64_t(1) << 28;   // 32-column tiles of 512 threads in one grid
+constexpr int64_t SWIGLU_F_LIMIT = int64_t(1) << 33;  // eight-column chunks of a row in 32 bits
+
+// What the dense and the grouped product with a 4-bit weight share (M rows in
+// all, G weights of [N, K]).
+mx_status check_gemm4(mx_elem_type a_elem, int64_t M, int64_t G, int64_t N, int64_t K) {
+  if (!is_elem(a_elem)) return fail(MX_ERR_INVALID_ARG, "unknown element type %d", (int)a_elem);
+  if (M < 0 || N < 0 || K < 0) return fail(MX_ERR_INVALID_ARG, "negative GEMM shape");
+  if (mul_overflows(M, K) || mul_overflows(M, N) || mul_overflows(G, N) || mul_overflows(G * N, K) ||
+      M * N > INT64_MAX / 2)
+    return fail(MX_ERR_INVALID_ARG, "GEMM shape too large");
+  if (K % 32 != 0) return fail(MX_ERR_UNSUPPORTED_SHAPE, "K %lld is not a multiple of 32", (long long)K);
+  if (K >= K_LIMIT)
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "K %lld too large for 32-bit tile offsets", (long long)K);
+  if (N >= GEMM4_N_LIMIT)
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "N %lld exceeds one launch grid", (long long)N);
+  return MX_OK;
+}
+
+mx_status check_gemm4_pointers(mx_elem_type a_elem, int64_t M, int64_t G, int64_t N, int64_t K,
+                               const void* a, const void* sa, const void* b, const void* sb,
+                               const void* c) {
+  if (!c) return fail(MX_ERR_INVALID_ARG, "c is NULL");
+  if (misaligned(c)) return fail(MX_ERR_INVALID_ARG, "c is not 16-byte aligned");
+  if (K == 0) return MX_OK;
+  if (!a || !sa || !b || !sb) return fail(MX_ERR_INVALID_ARG, "an operand is NULL");
+  if (misaligned(a) || misaligned(b)) return fail(MX_ERR_INVALID_ARG, "a or b is not 16-byte aligned");
+  const int64_t bytes = 2 * M * N;
+  if (share_memory(c, bytes, a, a_elem == MX_ELEM_E2M1 ? M * K / 2 : M * K) ||
+      share_memory(c, bytes, sa, M * (K / 32)) || share_memory(c, bytes, b, G * N * (K / 2)) ||
+      share_memory(c, bytes, sb, G * N * (K / 32)))
+    return fail(MX_ERR_INVALID_ARG, "c shares memory with an operand");
+  return MX_OK;
+}
+
+mx_status check_swiglu(int64_t T, int64_t F) {
+  if (T < 0 || F < 0) return fail(MX_ERR_INVALID_ARG, "negative shape [%lld, 2 x %lld]", (long long)T,
+                                  (long long)F);
+  if (F % 32 != 0) return fail(MX_ERR_UNSUPPORTED_SHAPE, "F %lld is not a multiple of 32", (long long)F);
+  if (F >= SWIGLU_F_LIMIT) return fail(MX_ERR_UNSUPPORTED_SHAPE, "F %lld too large", (long long)F);
+  if (mul_overflows(T, 4 * F)) return fail(MX_ERR_INVALID_ARG, "shape too large");
+  return MX_OK;
+}
+
+// Shapes of a column quantisation's [R, C] source.
+mx_status check_columns(int64_t R, int64_t C, int64_t tile_rows, int64_t tile_cols) {
+  if (C % 32 != 0) return fail(MX_ERR_UNSUPPORTED_SHAPE, "cols %lld is not a multiple of 32", (long long)C);
+  if (R % 32 != 0) return fail(MX_ERR_UNSUPPORTED_SHAPE, "rows %lld is not a multiple of 32", (long long)R);
+  if ((C + tile_cols - 1) / tile_cols > 65535)
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "cols %lld exceeds the column-tile grid", (long long)C);
+  if ((R + tile_rows - 1) / tile_rows * 512 >= (int64_t(1) << 32))
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "rows %lld exceed the row-tile grid", (long long)R);
+  return MX_OK;
+}
+
+int compute_units(int dev) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  return g_num_cus[dev];
+}
+
+mx_status swiglu_backward_call(mx_elem_type ckpt_elem, int out_elem, const void* dh, const void* cq,
+                               const void* cs, int64_t T, int64_t F, void* dx, void* q, void* s,
+                               hipStream_t stream) {
+  if (!is_fp8(ckpt_elem)) return fail(MX_ERR_INVALID_ARG, "unknown element type %d", (int)ckpt_elem);
+  mx_status st = check_swiglu(T, F);
+  if (st != MX_OK || T == 0 || F == 0) return st;
+  if (!dh || !cq || !cs) return fail(MX_ERR_INVALID_ARG, "dh or the checkpoint is NULL");
+  if (out_elem < 0 ? !dx : (!q || !s)) return fail(MX_ERR_INVALID_ARG, "an output is NULL");
+  if (misaligned(dh) || misaligned(cq) || misaligned(dx) || misaligned(q))
+    return fail(MX_ERR_INVALID_ARG, "a pointer is not 16-byte aligned");
+  int dev;
+  st = current_device(&dev);
+  if (st != MX_OK) return st;
+  const hipError_t e = mx::launch_swiglu_backward((int)ckpt_elem, out_elem, dh, cq, cs, T, F, dx, q, s,
+                                                  stream);
+  if (e != hipSuccess) return hip_fail(e, "SwiGLU gradient kernel launch");
+  return MX_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -726,6 +811,187 @@ mx_status mx_grad_clip(int64_t n, void* const* tensors, const int64_t* numels,
   g_err[0] = '\0';
   if (!(max_norm >= 0.0f)) return fail(MX_ERR_INVALID_ARG, "max_norm %g is not a norm", (double)max_norm);
   return grad_call(n, tensors, numels, dtypes, true, max_norm, norm, workspace, workspace_bytes, stream);
+}
+
+mx_status mx_quant4(mx_quant_mode mode, const void* x, int64_t batch, int64_t rows, int64_t cols,
+                    void* q, void* s, void* q_t, void* s_t, hipStream_t stream) {
+  g_err[0] = '\0';
+  if (mode < MX_QUANT_ROW_1x32 || mode > MX_QUANT_DUAL_AXIS)
+    return fail(MX_ERR_INVALID_ARG, "quantisation mode %d is not offered in 4 bits", (int)mode);
+  if (batch < 0 || batch > 65535) return fail(MX_ERR_INVALID_ARG, "batch %lld not in [0, 65535]", (long long)batch);
+  if (rows < 0 || cols < 0) return fail(MX_ERR_INVALID_ARG, "negative shape [%lld, %lld]",
+                                        (long long)rows, (long long)cols);
+  if (mul_overflows(rows, cols) || mul_overflows(batch, rows * cols) ||
+      batch * rows * cols > (INT64_MAX / 4))
+    return fail(MX_ERR_INVALID_ARG, "shape too large");
+  if (cols % 32 != 0)
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "cols %lld is not a multiple of 32", (long long)cols);
+  if (mode != MX_QUANT_ROW_1x32) {
+    const mx_status sc = check_columns(rows, cols, 256, 64);
+    if (sc != MX_OK) return sc;
+  }
+  if (batch == 0 || rows == 0 || cols == 0) return MX_OK;
+  if (!x) return fail(MX_ERR_INVALID_ARG, "x is NULL");
+  if (mode != MX_QUANT_COL_1x32 && (!q || !s))
+    return fail(MX_ERR_INVALID_ARG, "q and s are required for this mode");
+  if (mode != MX_QUANT_ROW_1x32 && (!q_t || !s_t))
+    return fail(MX_ERR_INVALID_ARG, "q_t and s_t are required for this mode");
+  if (misaligned(x) || misaligned(q) || misaligned(q_t))
+    return fail(MX_ERR_INVALID_ARG, "x, q or q_t is not 16-byte aligned");
+  int dev;
+  const mx_status st = current_device(&dev);
+  if (st != MX_OK) return st;
+  const hipError_t e = mx::launch_quant4((int)mode, x, batch, rows, cols, q, s, q_t, s_t, stream);
+  if (e != hipSuccess) return hip_fail(e, "4-bit quantisation kernel launch");
+  return MX_OK;
+}
+
+mx_status mx_dequant(mx_elem_type elem, const void* q, const void* s, int64_t rows, int64_t cols,
+                     void* y, hipStream_t stream) {
+  g_err[0] = '\0';
+  if (!is_elem(elem)) return fail(MX_ERR_INVALID_ARG, "unknown element type %d", (int)elem);
+  if (rows < 0 || cols < 0) return fail(MX_ERR_INVALID_ARG, "negative shape [%lld, %lld]",
+                                        (long long)rows, (long long)cols);
+  if (mul_overflows(rows, cols) || rows * cols > INT64_MAX / 4)
+    return fail(MX_ERR_INVALID_ARG, "shape too large");
+  if (cols % 32 != 0)
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "cols %lld is not a multiple of 32", (long long)cols);
+  if (rows == 0 || cols == 0) return MX_OK;
+  if (!q || !s || !y) return fail(MX_ERR_INVALID_ARG, "q, s or y is NULL");
+  if (misaligned(q) || misaligned(y)) return fail(MX_ERR_INVALID_ARG, "q or y is not 16-byte aligned");
+  int dev;
+  const mx_status st = current_device(&dev);
+  if (st != MX_OK) return st;
+  const hipError_t e = mx::launch_dequant((int)elem, q, s, rows * cols, y, stream);
+  if (e != hipSuccess) return hip_fail(e, "dequantisation kernel launch");
+  return MX_OK;
+}
+
+mx_status mx_gemm4(mx_elem_type a_elem, int64_t M, int64_t N, int64_t K, const void* a,
+                   const void* sa, const void* b, const void* sb, void* c, hipStream_t stream) {
+  g_err[0] = '\0';
+  mx_status st = check_gemm4(a_elem, M, 1, N, K);
+  if (st != MX_OK) return st;
+  if (grid_too_large(gemm_tiles(M, N)))
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%lld x %lld output tiles exceed one launch grid",
+                (long long)M, (long long)N);
+  if (M == 0 || N == 0) return MX_OK;
+  st = check_gemm4_pointers(a_elem, M, 1, N, K, a, sa, b, sb, c);
+  if (st != MX_OK) return st;
+  int dev;
+  st = current_device(&dev);
+  if (st != MX_OK) return st;
+  const hipError_t e = K == 0 ? mx::launch_fill_zero(c, 2 * M * N, stream)
+                              : mx::launch_gemm4((int)a_elem, M, N, K, a, sa, b, sb, c,
+                                                 compute_units(dev), stream);
+  if (e != hipSuccess) return hip_fail(e, "4-bit weight GEMM kernel launch");
+  return MX_OK;
+}
+
+mx_status mx_grouped_gemm4(mx_elem_type a_elem, int64_t G, const int64_t* offsets, int64_t T,
+                           int64_t N, int64_t K, const void* a, const void* sa, const void* b,
+                           const void* sb, void* c, hipStream_t stream) {
+  g_err[0] = '\0';
+  if (G < 1 || G > 512) return fail(MX_ERR_INVALID_ARG, "group count %lld not in [1, 512]", (long long)G);
+  mx_status st = check_gemm4(a_elem, T, G, N, K);
+  if (st != MX_OK) return st;
+  if (((T + 255) / 256 + G) * ((N + 255) / 256) >= ((int64_t)1 << 31))
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "grouped GEMM of %lld x %lld needs 2^31 tiles or more",
+                (long long)T, (long long)N);
+  if (T == 0 || N == 0) return MX_OK;
+  if (!offsets) return fail(MX_ERR_INVALID_ARG, "offsets is NULL");
+  st = check_gemm4_pointers(a_elem, T, G, N, K, a, sa, b, sb, c);
+  if (st != MX_OK) return st;
+  int dev;
+  st = current_device(&dev);
+  if (st != MX_OK) return st;
+  const hipError_t e = mx::launch_grouped_gemm4((int)a_elem, G, offsets, T, N, K, a, sa, b, sb, c,
+                                                compute_units(dev), stream);
+  if (e != hipSuccess) return hip_fail(e, "grouped 4-bit weight GEMM kernel launch");
+  return MX_OK;
+}
+
+mx_status mx_swiglu_quant(mx_elem_type elem, mx_elem_type ckpt_elem, const void* x, int64_t T,
+                          int64_t F, void* q, void* s, void* ckpt_q, void* ckpt_s,
+                          hipStream_t stream) {
+  g_err[0] = '\0';
+  if (!is_fp8(elem) || !is_fp8(ckpt_elem))
+    return fail(MX_ERR_INVALID_ARG, "unknown element type (%d, checkpoint %d)", (int)elem, (int)ckpt_elem);
+  mx_status st = check_swiglu(T, F);
+  if (st != MX_OK || T == 0 || F == 0) return st;
+  if (!x || !q || !s) return fail(MX_ERR_INVALID_ARG, "x, q or s is NULL");
+  if ((ckpt_q == nullptr) != (ckpt_s == nullptr))
+    return fail(MX_ERR_INVALID_ARG, "one of ckpt_q and ckpt_s is NULL");
+  if (misaligned(x) || misaligned(q) || misaligned(ckpt_q))
+    return fail(MX_ERR_INVALID_ARG, "x, q or ckpt_q is not 16-byte aligned");
+  int dev;
+  st = current_device(&dev);
+  if (st != MX_OK) return st;
+  const hipError_t e = mx::launch_swiglu_quant((int)elem, (int)ckpt_elem, x, T, F, q, s, ckpt_q, ckpt_s,
+                                               stream);
+  if (e != hipSuccess) return hip_fail(e, "SwiGLU kernel launch");
+  return MX_OK;
+}
+
+mx_status mx_swiglu_backward(mx_elem_type ckpt_elem, const void* dh, const void* ckpt_q,
+                             const void* ckpt_s, int64_t T, int64_t F, void* dx, hipStream_t stream) {
+  g_err[0] = '\0';
+  return swiglu_backward_call(ckpt_elem, -1, dh, ckpt_q, ckpt_s, T, F, dx, nullptr, nullptr, stream);
+}
+
+mx_status mx_swiglu_backward_quant(mx_elem_type ckpt_elem, mx_elem_type elem, const void* dh,
+                                   const void* ckpt_q, const void* ckpt_s, int64_t T, int64_t F,
+                                   void* q, void* s, hipStream_t stream) {
+  g_err[0] = '\0';
+  if (!is_fp8(elem)) return fail(MX_ERR_INVALID_ARG, "unknown element type %d", (int)elem);
+  return swiglu_backward_call(ckpt_elem, (int)elem, dh, ckpt_q, ckpt_s, T, F, nullptr, q, s, stream);
+}
+
+mx_status mx_requant_col(mx_elem_type elem, mx_elem_type out_elem, const void* q, const void* s,
+                         int64_t rows, int64_t cols, void* q_t, void* s_t, hipStream_t stream) {
+  g_err[0] = '\0';
+  if (!is_fp8(elem) || !is_fp8(out_elem))
+    return fail(MX_ERR_INVALID_ARG, "unknown element type (%d to %d)", (int)elem, (int)out_elem);
+  if (rows < 0 || cols < 0) return fail(MX_ERR_INVALID_ARG, "negative shape [%lld, %lld]",
+                                        (long long)rows, (long long)cols);
+  if (mul_overflows(rows, cols)) return fail(MX_ERR_INVALID_ARG, "shape too large");
+  mx_status st = check_columns(rows, cols, 128, 128);
+  if (st != MX_OK || rows == 0 || cols == 0) return st;
+  if (!q || !s || !q_t || !s_t) return fail(MX_ERR_INVALID_ARG, "a pointer is NULL");
+  if (misaligned(q) || misaligned(q_t)) return fail(MX_ERR_INVALID_ARG, "q or q_t is not 16-byte aligned");
+  int dev;
+  st = current_device(&dev);
+  if (st != MX_OK) return st;
+  const hipError_t e = mx::launch_requant_col((int)elem, (int)out_elem, q, s, rows, cols, q_t, s_t, stream);
+  if (e != hipSuccess) return hip_fail(e, "column requantisation kernel launch");
+  return MX_OK;
+}
+
+mx_status mx_requant_grouped_col(mx_elem_type elem, mx_elem_type out_elem, const void* q,
+                                 const void* s, int64_t T, int64_t C, int64_t G,
+                                 const int64_t* offsets, void* q_t, void* s_t, hipStream_t stream) {
+  g_err[0] = '\0';
+  if (!is_fp8(elem) || !is_fp8(out_elem))
+    return fail(MX_ERR_INVALID_ARG, "unknown element type (%d to %d)", (int)elem, (int)out_elem);
+  if (G < 1 || G > 512) return fail(MX_ERR_INVALID_ARG, "group count %lld not in [1, 512]", (long long)G);
+  if (T < 0 || C < 0) return fail(MX_ERR_INVALID_ARG, "negative shape [%lld, %lld]", (long long)T,
+                                  (long long)C);
+  const int64_t cap = mx_grouped_col_capacity(T, G);
+  if (cap < 0 || cap >= K_LIMIT)
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "token capacity %lld too large", (long long)cap);
+  if (mul_overflows(T, C) || mul_overflows(cap, C)) return fail(MX_ERR_INVALID_ARG, "shape too large");
+  mx_status st = check_columns(cap, C, 128, 128);
+  if (st != MX_OK || C == 0) return st;
+  if (!offsets || !q_t || !s_t) return fail(MX_ERR_INVALID_ARG, "offsets, q_t or s_t is NULL");
+  if (T > 0 && (!q || !s)) return fail(MX_ERR_INVALID_ARG, "q or s is NULL");
+  if (misaligned(q) || misaligned(q_t)) return fail(MX_ERR_INVALID_ARG, "q or q_t is not 16-byte aligned");
+  int dev;
+  st = current_device(&dev);
+  if (st != MX_OK) return st;
+  const hipError_t e = mx::launch_requant_grouped_col((int)elem, (int)out_elem, q, s, T, C, G, offsets,
+                                                      cap, q_t, s_t, stream);
+  if (e != hipSuccess) return hip_fail(e, "grouped column requantisation kernel launch");
+  return MX_OK;
 }
 
 }  // extern "C"

@@ -51,18 +51,22 @@ __device__ __forceinline__ uint32_t xor_max(uint32_t v, int mask) {
   return umax(v, (uint32_t)__shfl_xor((int)v, mask, 64));
 }
 
-// Payload element types: OCP E4M3 (largest finite 448) and E5M2 (largest
-// finite 57344 = 1.75 * 2^15).
-enum Elem { ELEM_E4M3 = 0, ELEM_E5M2 = 1 };
+// Payload element types: OCP E4M3 (largest finite 448), E5M2 (largest finite
+// 57344 = 1.75 * 2^15) and the 4-bit E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+// their negatives; two to a byte, the first in the low half).  The numbers are
+// the MFMA's format codes.
+enum Elem { ELEM_E4M3 = 0, ELEM_E5M2 = 1, ELEM_E2M1 = 4 };
 
 // E8M0 scale byte for a block whose largest magnitude has BF16 bits `amax`:
-// e = E - 135 + [m > 96] for E4M3 (448 = 1.75 * 2^8) and E - 142 + [m > 96]
-// for E5M2 (57344 = 1.75 * 2^15), at least -127.
+// e = E - 135 + [m > 96] for E4M3 (448 = 1.75 * 2^8), E - 142 + [m > 96]
+// for E5M2 (57344 = 1.75 * 2^15) and E - 129 + [m > 64] for E2M1 (6 = 1.5 *
+// 2^2), at least -127.
 template <int EL>
 __device__ __forceinline__ uint32_t scale_byte_t(uint32_t amax) {
   if (amax >= 0x7F80u) return 0xFFu;  // Inf or NaN in the block
-  constexpr int off = EL == ELEM_E5M2 ? 142 : 135;
-  int e = (int)(amax >> 7) - off + ((amax & 0x7Fu) > 96u ? 1 : 0);
+  constexpr int off = EL == ELEM_E5M2 ? 142 : EL == ELEM_E2M1 ? 129 : 135;
+  constexpr uint32_t top = EL == ELEM_E2M1 ? 64u : 96u;
+  int e = (int)(amax >> 7) - off + ((amax & 0x7Fu) > top ? 1 : 0);
   e = e < -127 ? -127 : e;
   return (uint32_t)(e + 127);
 }
@@ -102,6 +106,59 @@ __device__ __forceinline__ uint2 cvt8_t(uint4 v, uint32_t sbyte) {
   return make_uint2(cvt4_t<EL>(v.x, v.y, sc), cvt4_t<EL>(v.z, v.w, sc));
 }
 __device__ __forceinline__ uint2 cvt8(uint4 v, uint32_t sbyte) { return cvt8_t<ELEM_E4M3>(v, sbyte); }
+
+// Eight BF16 of a chunk -> eight E2M1 codes in one dword.  A non-finite block
+// (scale byte 0xFF, which makes every product NaN) gets payload 0x77: the
+// format has no NaN of its own.
+__device__ __forceinline__ uint32_t cvt8_e2m1(uint4 v, uint32_t sbyte) {
+  if (sbyte == 0xFFu) return 0x77777777u;
+  const float sc = cvt_scale(sbyte);
+  uint32_t r = 0;
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(v2bf, v.x), sc, 0);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(v2bf, v.y), sc, 1);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(v2bf, v.z), sc, 2);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(v2bf, v.w), sc, 3);
+  return r;
+}
+
+// Payload of a block with scale byte sbyte back to BF16, rounded to nearest
+// even where the value has no BF16 (checked on the device over all codes at
+// the scales' ends); a block of scale 0xFF gives NaN throughout.
+constexpr uint32_t BF16_NAN_PAIR = 0x7FC07FC0u;
+
+// Eight FP8 codes (two dwords) -> eight BF16.
+template <int EL>
+__device__ __forceinline__ uint4 decode8_t(uint2 q, uint32_t sbyte) {
+  if (sbyte == 0xFFu)
+    return make_uint4(BF16_NAN_PAIR, BF16_NAN_PAIR, BF16_NAN_PAIR, BF16_NAN_PAIR);
+  const float sc = cvt_scale(sbyte);
+  uint4 r;
+  if (EL == ELEM_E5M2) {
+    r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(q.x, sc, false));
+    r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(q.x, sc, true));
+    r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(q.y, sc, false));
+    r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(q.y, sc, true));
+  } else {
+    r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q.x, sc, false));
+    r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q.x, sc, true));
+    r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q.y, sc, false));
+    r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q.y, sc, true));
+  }
+  return r;
+}
+
+// Eight E2M1 codes (one dword) -> eight BF16.
+__device__ __forceinline__ uint4 decode8_e2m1(uint32_t q, uint32_t sbyte) {
+  if (sbyte == 0xFFu)
+    return make_uint4(BF16_NAN_PAIR, BF16_NAN_PAIR, BF16_NAN_PAIR, BF16_NAN_PAIR);
+  const float sc = cvt_scale(sbyte);
+  uint4 r;
+  r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, sc, 0));
+  r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, sc, 1));
+  r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, sc, 2));
+  r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, sc, 3));
+  return r;
+}
 
 // BF16 pairs built from the same half of two packed words: (lo of a, lo of
 // b) and (hi of a, hi of b).  Used to pair two rows of one column.

@@ -94,4 +94,37 @@ size_t grad_workspace(int64_t n);
 hipError_t launch_grad(int64_t n, void* const* tensors, const int64_t* numels, const int* f32,
                        int clip, float max_norm, float* norm, void* workspace, hipStream_t stream);
 
+// E2M1 quantisation of `batch` [R, C] matrices: mode 0 = row (q, s), 1 =
+// column (q_t, s_t), 2 = both.
+hipError_t launch_quant4(int mode, const void* x, int64_t batch, int64_t R, int64_t C, void* q,
+                         void* s, void* qt, void* st, hipStream_t stream);
+// n elements (n % 32 == 0) of an MX tensor (elem 0 = E4M3, 1 = E5M2, 4 =
+// E2M1) back to BF16.
+hipError_t launch_dequant(int elem, const void* q, const void* s, int64_t n, void* y,
+                          hipStream_t stream);
+
+// Column blocks of an MX tensor in row blocks; shapes as launch_quant_tile's
+// column mode and launch_quant_grouped_col.
+hipError_t launch_requant_col(int elem, int out_elem, const void* q, const void* s, int64_t R,
+                              int64_t C, void* qt, void* st, hipStream_t stream);
+hipError_t launch_requant_grouped_col(int elem, int out_elem, const void* q, const void* s,
+                                      int64_t T, int64_t C, int64_t G, const int64_t* offsets,
+                                      int64_t cap, void* qt, void* st, hipStream_t stream);
+
+// Products with E2M1 weights b; a_elem 0 = E4M3, 1 = E5M2, 4 = E2M1.
+hipError_t launch_gemm4(int a_elem, int64_t M, int64_t N, int64_t K, const void* a, const void* sa,
+                        const void* b, const void* sb, void* c, int num_cus, hipStream_t stream);
+hipError_t launch_grouped_gemm4(int a_elem, int64_t G, const int64_t* offsets, int64_t T, int64_t N,
+                                int64_t K, const void* a, const void* sa, const void* b,
+                                const void* sb, void* c, int num_cus, hipStream_t stream);
+
+// SwiGLU of x [T, 2F] into row blocks q, s, with the checkpoint cq, cs of x
+// unless they are null, and the gradient from it (out_elem < 0: BF16 dx,
+// otherwise its row blocks q, s).
+hipError_t launch_swiglu_quant(int elem, int ckpt_elem, const void* x, int64_t T, int64_t F, void* q,
+                               void* s, void* cq, void* cs, hipStream_t stream);
+hipError_t launch_swiglu_backward(int ckpt_elem, int out_elem, const void* dh, const void* cq,
+                                  const void* cs, int64_t T, int64_t F, void* dx, void* q, void* s,
+                                  hipStream_t stream);
+
 }  // namespace mx

@@ -17,8 +17,13 @@
 // group g's columns from P_g = 128 (o_g / 128 + g) on and fills every column
 // that holds no token with zero blocks.
 //
-// All kernels are bound by HBM bandwidth: x is read once with 16-byte loads,
-// every output byte is written once.
+// The column modes also take an MX tensor in row blocks for x (a forward
+// product's operand, kept as an 8-bit checkpoint) and give its column blocks,
+// the operand of the weight gradient: payload and scales are turned back into
+// BF16 as they are read.
+//
+// All kernels are bound by HBM bandwidth: x is read once with 16-byte loads
+// (8-byte ones of an MX tensor), every output byte is written once.
 #include "mx_device.h"
 #include "mx_kernels.h"
 
@@ -188,9 +193,24 @@ __device__ __forceinline__ void gcol_block(const int64_t* __restrict__ offsets, 
   nreal = left <= 0 ? 0 : (left >= 32 ? 32 : (int)left);
 }
 
+// Eight elements c .. c + 7 of row r: SRC -1 reads BF16 x, otherwise x is the
+// payload of that element type and xs its row-block scales.
+template <int SRC>
+__device__ __forceinline__ uint4 load_chunk(const void* __restrict__ x, const uint8_t* __restrict__ xs,
+                                            int64_t r, int64_t c, int64_t C) {
+  const int64_t i = r * C + c;
+  if constexpr (SRC < 0) {
+    return load_stream16((const uint16_t*)x + i);
+  } else {
+    const u32x2 w = __builtin_nontemporal_load((const u32x2*)((const uint8_t*)x + i));
+    return decode8_t<SRC>(make_uint2(w.x, w.y), xs[i >> 5]);
+  }
+}
+
 // One 128 x 128 tile at rows R0.., columns C0.. (one tile per workgroup).
-template <int MODE, int EL>
-__device__ __forceinline__ void quant_tile(const uint16_t* __restrict__ x, int64_t R, int64_t C,
+template <int MODE, int EL, int SRC>
+__device__ __forceinline__ void quant_tile(const void* __restrict__ x, const uint8_t* __restrict__ xs,
+                                           int64_t R, int64_t C,
                                            uint8_t* __restrict__ q, uint8_t* __restrict__ s,
                                            uint8_t* __restrict__ qt, uint8_t* __restrict__ st,
                                            int64_t G, const int64_t* __restrict__ offsets,
@@ -211,12 +231,12 @@ __device__ __forceinline__ void quant_tile(const uint16_t* __restrict__ x, int64
     if (r0 < R) gcol_block(offsets, G, T, r0, lane, src, nreal);
 #pragma unroll
     for (int i = 0; i < 4; i++)
-      v[i] = (live && 4 * g + i < nreal) ? load_stream16(x + (src + 4 * g + i) * C + c)
+      v[i] = (live && 4 * g + i < nreal) ? load_chunk<SRC>(x, xs, src + 4 * g + i, c, C)
                                          : make_uint4(0, 0, 0, 0);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; i++)
-      v[i] = live ? load_stream16(x + (r0 + 4 * g + i) * C + c) : make_uint4(0, 0, 0, 0);
+      v[i] = live ? load_chunk<SRC>(x, xs, r0 + 4 * g + i, c, C) : make_uint4(0, 0, 0, 0);
   }
 
   const int rl = 32 * wr + 4 * g;        // local row of this lane's first row
@@ -322,9 +342,9 @@ __device__ __forceinline__ void quant_tile(const uint16_t* __restrict__ x, int64
 // grid.z indexes a batch of equally shaped matrices (contiguous inputs and
 // outputs); the grouped column mode uses G, offsets and T (x has T rows, R is
 // the padded capacity).  One tile per workgroup in every mode.
-template <int MODE, int EL>
+template <int MODE, int EL, int SRC>
 __global__ void __launch_bounds__(TILE_THREADS)
-quant_tile_kernel(const uint16_t* __restrict__ x, int64_t R, int64_t C, uint8_t* __restrict__ q,
+quant_tile_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ xs, int64_t R, int64_t C, uint8_t* __restrict__ q,
                   uint8_t* __restrict__ s, uint8_t* __restrict__ qt, uint8_t* __restrict__ st,
                   int64_t G, const int64_t* __restrict__ offsets, int64_t T) {
   if (blockIdx.z) {
@@ -349,7 +369,7 @@ quant_tile_kernel(const uint16_t* __restrict__ x, int64_t R, int64_t C, uint8_t*
     tr = lin / gridDim.y;
     tc = lin - tr * gridDim.y;
   }
-  quant_tile<MODE, EL>(x, R, C, q, s, qt, st, G, offsets, T, tr * TILE_ROWS, (lds8*)lq, (lds8*)lqt,
+  quant_tile<MODE, EL, SRC>(x, xs, R, C, q, s, qt, st, G, offsets, T, tr * TILE_ROWS, (lds8*)lq, (lds8*)lqt,
                        (lds8*)ls, (lds8*)lst, tc * TILE_COLS);
 }
 
@@ -375,8 +395,8 @@ hipError_t launch_quant_row(const void* x, int64_t n, void* q, void* s, int elem
 template <int MODE, int EL>
 static void launch_tile(dim3 grid, const void* x, int64_t R, int64_t C, void* q, void* s, void* qt,
                         void* st, int64_t G, const int64_t* offsets, int64_t T, hipStream_t stream) {
-  hipLaunchKernelGGL((quant_tile_kernel<MODE, EL>), grid, dim3(TILE_THREADS), 0, stream,
-                     (const uint16_t*)x, R, C, (uint8_t*)q, (uint8_t*)s, (uint8_t*)qt, (uint8_t*)st,
+  hipLaunchKernelGGL((quant_tile_kernel<MODE, EL, -1>), grid, dim3(TILE_THREADS), 0, stream,
+                     (const uint16_t*)x, (const uint8_t*)nullptr, R, C, (uint8_t*)q, (uint8_t*)s, (uint8_t*)qt, (uint8_t*)st,
                      G, offsets, T);
 }
 
@@ -426,6 +446,39 @@ hipError_t launch_quant_grouped_col(const void* x, int64_t T, int64_t C, int64_t
   dim3 grid((unsigned)((cap + TILE_ROWS - 1) / TILE_ROWS), (unsigned)((C + TILE_COLS - 1) / TILE_COLS));
   launch_tile_elem<TILE_GCOL>(elem, grid, x, cap, C, nullptr, nullptr, qt, st, G, offsets, T, stream);
   return hipGetLastError();
+}
+
+template <int MODE>
+static hipError_t launch_requant(int elem, int out_elem, dim3 grid, const void* x, const void* xs,
+                                 int64_t R, int64_t C, void* qt, void* st, int64_t G,
+                                 const int64_t* offsets, int64_t T, hipStream_t stream) {
+#define MX_REQUANT(SRC_, EL_)                                                                       \
+  hipLaunchKernelGGL((quant_tile_kernel<MODE, EL_, SRC_>), grid, dim3(TILE_THREADS), 0, stream,     \
+                     (const uint16_t*)x, (const uint8_t*)xs, R, C, (uint8_t*)nullptr,              \
+                     (uint8_t*)nullptr, (uint8_t*)qt, (uint8_t*)st, G, offsets, T)
+  if (elem == ELEM_E4M3 && out_elem == ELEM_E4M3) MX_REQUANT(ELEM_E4M3, ELEM_E4M3);
+  else if (elem == ELEM_E4M3 && out_elem == ELEM_E5M2) MX_REQUANT(ELEM_E4M3, ELEM_E5M2);
+  else if (elem == ELEM_E5M2 && out_elem == ELEM_E4M3) MX_REQUANT(ELEM_E5M2, ELEM_E4M3);
+  else if (elem == ELEM_E5M2 && out_elem == ELEM_E5M2) MX_REQUANT(ELEM_E5M2, ELEM_E5M2);
+  else return hipErrorInvalidValue;
+#undef MX_REQUANT
+  return hipGetLastError();
+}
+
+hipError_t launch_requant_col(int elem, int out_elem, const void* q, const void* s, int64_t R,
+                              int64_t C, void* qt, void* st, hipStream_t stream) {
+  const dim3 grid((unsigned)((R + TILE_ROWS - 1) / TILE_ROWS),
+                  (unsigned)((C + TILE_COLS - 1) / TILE_COLS));
+  return launch_requant<TILE_COL>(elem, out_elem, grid, q, s, R, C, qt, st, 0, nullptr, 0, stream);
+}
+
+hipError_t launch_requant_grouped_col(int elem, int out_elem, const void* q, const void* s,
+                                      int64_t T, int64_t C, int64_t G, const int64_t* offsets,
+                                      int64_t cap, void* qt, void* st, hipStream_t stream) {
+  if (G < 1 || G > GCOL_MAX_GROUPS) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)((cap + TILE_ROWS - 1) / TILE_ROWS),
+                  (unsigned)((C + TILE_COLS - 1) / TILE_COLS));
+  return launch_requant<TILE_GCOL>(elem, out_elem, grid, q, s, cap, C, qt, st, G, offsets, T, stream);
 }
 
 }  // namespace mx

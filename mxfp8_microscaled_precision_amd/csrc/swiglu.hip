@@ -1,0 +1,184 @@
+// SwiGLU between an MLP's two products, and its gradient from an 8-bit
+// checkpoint, for gfx950.
+//
+// x [T, 2F] BF16 holds the gates in columns 0 .. F - 1 and the up values in F
+// .. 2F - 1.  h = g sig(g) u with sig(g) = 1 / (1 + exp(-g)), computed in FP32
+// and rounded to BF16, leaves quantised in 1x32 blocks: the down product's
+// operand, without a BF16 copy in memory.  The checkpoint is x itself in 1x32
+// blocks, half the bytes of x, and all that the backward pass needs:
+//   dg = dh u sig(g) (1 + g (1 - sig(g))),  du = dh g sig(g).
+//
+// The kernels are bound by HBM.  A lane takes eight columns: 16 bytes of the
+// gates and 16 of the up values, four lanes to a block of 32.
+#include "mx_device.h"
+#include "mx_kernels.h"
+#include "mx_rows.h"
+
+namespace mx {
+
+constexpr int ACT_THREADS = 256;
+
+// sig(g) with no overflow: t = exp(-|g|) <= 1
+__device__ __forceinline__ float sigmoid(float g) {
+  const float t = __expf(-fabsf(g));
+  const float r = __builtin_amdgcn_rcpf(1.0f + t);
+  return g >= 0.0f ? r : t * r;
+}
+
+__device__ __forceinline__ uint4 as_uint4(u32x4 v) { return make_uint4(v.x, v.y, v.z, v.w); }
+__device__ __forceinline__ u32x4 as_vec(uint4 v) { return (u32x4){v.x, v.y, v.z, v.w}; }
+
+// Rows t0 .. of the caller's slice; n8 = F / 8 chunks to a row, nchunks = rows * n8.
+template <int EL, int CE, bool CKPT>
+__global__ void __launch_bounds__(ACT_THREADS)
+swiglu_quant_kernel(const uint16_t* __restrict__ x, uint32_t n8, uint32_t nchunks,
+                    uint8_t* __restrict__ q, uint8_t* __restrict__ s, uint8_t* __restrict__ cq,
+                    uint8_t* __restrict__ cs) {
+  const uint32_t c = blockIdx.x * ACT_THREADS + threadIdx.x;
+  if (c >= nchunks) return;
+  const uint32_t row = c / n8, k = c - row * n8;
+  const int64_t F = 8 * (int64_t)n8;
+  const uint16_t* src = x + (int64_t)row * 2 * F + 8 * k;
+  const uint4 vg = load_stream16(src), vu = load_stream16(src + F);
+  float g[8], u[8], h[8];
+  unpack8(as_vec(vg), g);
+  unpack8(as_vec(vu), u);
+#pragma unroll
+  for (int i = 0; i < 8; i++) h[i] = g[i] * sigmoid(g[i]) * u[i];
+  const uint4 vh = as_uint4(pack8(h));
+  // a row's quads are whole: n8 is a multiple of 4, and so is nchunks
+  const uint32_t sb = scale_byte_t<EL>(quad_max(chunk_absmax(vh)));
+  *(uint2*)(q + 8 * (int64_t)c) = cvt8_t<EL>(vh, sb);
+  if ((k & 3) == 0) s[c >> 2] = (uint8_t)sb;
+  if (CKPT) {
+    const uint32_t sg = scale_byte_t<CE>(quad_max(chunk_absmax(vg)));
+    const uint32_t su = scale_byte_t<CE>(quad_max(chunk_absmax(vu)));
+    const int64_t at = (int64_t)row * 2 * F + 8 * k;
+    *(uint2*)(cq + at) = cvt8_t<CE>(vg, sg);
+    *(uint2*)(cq + at + F) = cvt8_t<CE>(vu, su);
+    if ((k & 3) == 0) {
+      cs[at >> 5] = (uint8_t)sg;
+      cs[(at + F) >> 5] = (uint8_t)su;
+    }
+  }
+}
+
+// OUT: -1 writes dx in BF16, otherwise it is the element type that dx's rows
+// are quantised to.
+template <int CE, int OUT>
+__global__ void __launch_bounds__(ACT_THREADS)
+swiglu_backward_kernel(const uint16_t* __restrict__ dh, const uint8_t* __restrict__ cq,
+                       const uint8_t* __restrict__ cs, uint32_t n8, uint32_t nchunks,
+                       uint16_t* __restrict__ dx, uint8_t* __restrict__ q, uint8_t* __restrict__ s) {
+  const uint32_t c = blockIdx.x * ACT_THREADS + threadIdx.x;
+  if (c >= nchunks) return;
+  const uint32_t row = c / n8, k = c - row * n8;
+  const int64_t F = 8 * (int64_t)n8;
+  const int64_t at = (int64_t)row * 2 * F + 8 * k;
+  const u32x2 wg = __builtin_nontemporal_load((const u32x2*)(cq + at));
+  const u32x2 wu = __builtin_nontemporal_load((const u32x2*)(cq + at + F));
+  const uint4 vd = load_stream16(dh + 8 * (int64_t)c);
+  const uint32_t sg = cs[at >> 5], su = cs[(at + F) >> 5];
+  float g[8], u[8], d[8], dg[8], du[8];
+  unpack8(as_vec(decode8_t<CE>(make_uint2(wg.x, wg.y), sg)), g);
+  unpack8(as_vec(decode8_t<CE>(make_uint2(wu.x, wu.y), su)), u);
+  unpack8(as_vec(vd), d);
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const float p = sigmoid(g[i]);
+    // the bounded factors first: no product overflows that the result does not
+    dg[i] = d[i] * (u[i] * (p * (1.0f + g[i] * (1.0f - p))));
+    du[i] = d[i] * (g[i] * p);
+  }
+  const u32x4 og = pack8(dg), ou = pack8(du);
+  if (OUT < 0) {
+    __builtin_nontemporal_store(og, (u32x4*)(dx + at));
+    __builtin_nontemporal_store(ou, (u32x4*)(dx + at + F));
+  } else {
+    constexpr int EL = OUT < 0 ? 0 : OUT;
+    const uint32_t bg = scale_byte_t<EL>(quad_max(chunk_absmax(as_uint4(og))));
+    const uint32_t bu = scale_byte_t<EL>(quad_max(chunk_absmax(as_uint4(ou))));
+    *(uint2*)(q + at) = cvt8_t<EL>(as_uint4(og), bg);
+    *(uint2*)(q + at + F) = cvt8_t<EL>(as_uint4(ou), bu);
+    if ((k & 3) == 0) {
+      s[at >> 5] = (uint8_t)bg;
+      s[(at + F) >> 5] = (uint8_t)bu;
+    }
+  }
+}
+
+// Rows of one launch: chunk numbers, rounded up to a workgroup, stay below 2^31.
+static int64_t slice_rows(int64_t F) {
+  const int64_t rows = (((int64_t)1 << 31) - ACT_THREADS) / (F / 8);
+  return rows;
+}
+
+template <int EL, int CE>
+static hipError_t swiglu_quant_t(const uint16_t* x, int64_t T, int64_t F, uint8_t* q, uint8_t* s,
+                                 uint8_t* cq, uint8_t* cs, hipStream_t stream) {
+  const int64_t step = slice_rows(F);
+  for (int64_t t = 0; t < T; t += step) {
+    const int64_t rows = T - t < step ? T - t : step;
+    const uint32_t nchunks = (uint32_t)(rows * (F / 8));
+    const dim3 grid((nchunks + ACT_THREADS - 1) / ACT_THREADS), block(ACT_THREADS);
+    if (cq)
+      hipLaunchKernelGGL((swiglu_quant_kernel<EL, CE, true>), grid, block, 0, stream, x + t * 2 * F,
+                         (uint32_t)(F / 8), nchunks, q + t * F, s + t * (F / 32), cq + t * 2 * F,
+                         cs + t * (F / 16));
+    else
+      hipLaunchKernelGGL((swiglu_quant_kernel<EL, CE, false>), grid, block, 0, stream, x + t * 2 * F,
+                         (uint32_t)(F / 8), nchunks, q + t * F, s + t * (F / 32), nullptr, nullptr);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+hipError_t launch_swiglu_quant(int elem, int ckpt_elem, const void* x, int64_t T, int64_t F, void* q,
+                               void* s, void* cq, void* cs, hipStream_t stream) {
+#define MX_SWIGLU(EL_, CE_)                                                                       \
+  return swiglu_quant_t<EL_, CE_>((const uint16_t*)x, T, F, (uint8_t*)q, (uint8_t*)s, (uint8_t*)cq, \
+                                  (uint8_t*)cs, stream)
+  if (elem == ELEM_E4M3 && ckpt_elem == ELEM_E4M3) MX_SWIGLU(ELEM_E4M3, ELEM_E4M3);
+  if (elem == ELEM_E5M2 && ckpt_elem == ELEM_E4M3) MX_SWIGLU(ELEM_E5M2, ELEM_E4M3);
+  if (elem == ELEM_E4M3 && ckpt_elem == ELEM_E5M2) MX_SWIGLU(ELEM_E4M3, ELEM_E5M2);
+  if (elem == ELEM_E5M2 && ckpt_elem == ELEM_E5M2) MX_SWIGLU(ELEM_E5M2, ELEM_E5M2);
+#undef MX_SWIGLU
+  return hipErrorInvalidValue;
+}
+
+template <int CE, int OUT>
+static hipError_t swiglu_backward_t(const uint16_t* dh, const uint8_t* cq, const uint8_t* cs, int64_t T,
+                                    int64_t F, uint16_t* dx, uint8_t* q, uint8_t* s,
+                                    hipStream_t stream) {
+  const int64_t step = slice_rows(F);
+  for (int64_t t = 0; t < T; t += step) {
+    const int64_t rows = T - t < step ? T - t : step;
+    const uint32_t nchunks = (uint32_t)(rows * (F / 8));
+    hipLaunchKernelGGL((swiglu_backward_kernel<CE, OUT>), dim3((nchunks + ACT_THREADS - 1) / ACT_THREADS),
+                       dim3(ACT_THREADS), 0, stream, dh + t * F, cq + t * 2 * F, cs + t * (F / 16),
+                       (uint32_t)(F / 8), nchunks, OUT < 0 ? dx + t * 2 * F : nullptr,
+                       OUT < 0 ? nullptr : q + t * 2 * F, OUT < 0 ? nullptr : s + t * (F / 16));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+hipError_t launch_swiglu_backward(int ckpt_elem, int out_elem, const void* dh, const void* cq,
+                                  const void* cs, int64_t T, int64_t F, void* dx, void* q, void* s,
+                                  hipStream_t stream) {
+#define MX_SWIGLU_B(CE_, OUT_)                                                                    \
+  return swiglu_backward_t<CE_, OUT_>((const uint16_t*)dh, (const uint8_t*)cq, (const uint8_t*)cs, T, \
+                                      F, (uint16_t*)dx, (uint8_t*)q, (uint8_t*)s, stream)
+  if (ckpt_elem == ELEM_E4M3 && out_elem < 0) MX_SWIGLU_B(ELEM_E4M3, -1);
+  if (ckpt_elem == ELEM_E4M3 && out_elem == ELEM_E4M3) MX_SWIGLU_B(ELEM_E4M3, ELEM_E4M3);
+  if (ckpt_elem == ELEM_E4M3 && out_elem == ELEM_E5M2) MX_SWIGLU_B(ELEM_E4M3, ELEM_E5M2);
+  if (ckpt_elem == ELEM_E5M2 && out_elem < 0) MX_SWIGLU_B(ELEM_E5M2, -1);
+  if (ckpt_elem == ELEM_E5M2 && out_elem == ELEM_E4M3) MX_SWIGLU_B(ELEM_E5M2, ELEM_E4M3);
+  if (ckpt_elem == ELEM_E5M2 && out_elem == ELEM_E5M2) MX_SWIGLU_B(ELEM_E5M2, ELEM_E5M2);
+#undef MX_SWIGLU_B
+  return hipErrorInvalidValue;
+}
+
+}  // namespace mx
