@@ -4,7 +4,8 @@
 // result; dense, and grouped by device-side expert offsets.  The pages name
 // 4-bit weights with 8-bit activations for serving and 4-bit training of the
 // routed experts (practice page, w4a8-mx; torchtitan-npu MXFP8/HiF8 tutorial,
-// step-2 environment table, ENABLE_MXFP4_QAT).
+// step-2 environment table, ENABLE_MXFP4_QAT).  This file has the kernels for
+// many rows; gemm4_few.hip those for few.
 //
 // Lane layouts of the scaled MFMAs, found by one-hot operands on the device.
 // 16x16x128: lane l = 16 g + i holds row i; in 4 bits its 16 bytes are K 32 g
@@ -14,217 +15,625 @@
 // halves at K 16 g and 32 + 16 g.  The order of K is free, so long as A and B
 // agree: which block of the data stands in which hardware block is chosen for
 // the loads.
-#include "gemm_common.h"
+#include "gemm4.h"
 
 namespace mx {
 
-typedef float v4f __attribute__((ext_vector_type(4)));
-typedef uint16_t u16_at1 __attribute__((aligned(1)));
+// One workgroup tile of 64 F x 64 F results: four waves of 32 F x 32 F, F x F
+// accumulators of 32x32 each.  A K step is 128 bytes of an A row: 128 elements
+// in 8 bits, 256 in 4.  Both operands are staged through a double-buffered
+// LDS tile; 16-byte chunks are swizzled by row so that the 16 lanes served
+// together read 16 bank groups: rows of 128 bytes as in gemm_common.h, B's
+// rows of 64 bytes (8-bit A) with chunk c of row r at c ^ (r / 4 & 3).
+//
+// Which blocks meet.  4-bit A: a 16-byte chunk of either operand is one block;
+// half S of a step reads chunks 2 S + g and 4 + 2 S + g (g: lane half), two
+// MFMAs of blocks (2 S, 2 S + 1) and (4 + 2 S, 4 + 2 S + 1).  8-bit A: half S
+// multiplies blocks S and 2 + S, of which A's lanes hold 16 bytes each (chunks
+// 2 S + g and 4 + 2 S + g) and B's lane half g the block 2 g + S (chunk 2 g +
+// S).
+template <int FA, int F>
+struct Tile4 {
+  static constexpr bool A4 = FA == ELEM_E2M1;
+  static constexpr int ROWS = 64 * F;
+  static constexpr int KS = A4 ? 256 : 128;    // elements of a K step
+  static constexpr int SB = KS / 32;           // scale bytes of a row and step
+  static constexpr int GS = 16 / SB;           // steps that 16 scale bytes last
+  static constexpr int BROW = A4 ? 128 : 64;   // bytes of a B row and step
+  static constexpr int A_BYTES = ROWS * 128, B_BYTES = ROWS * BROW;
+  static constexpr int A_OPS = 2 * F, B_OPS = A4 ? 2 * F : F;  // 1 KB loads of a wave and step
+  static constexpr int DS_READS = A4 ? 4 * F : 3 * F;          // 16-byte LDS reads of half a step
 
-// ---------------------------------------------------------------------------
-// Few rows: the weight streams from memory straight into MFMA operands.
-// ---------------------------------------------------------------------------
-// A workgroup of 8 waves computes 16 MF rows x 16 NF columns; its waves take
-// the 256-element chunks of K in turn and their sums are added in LDS in the
-// order of the waves.  A lane's share of a chunk of a 4-bit row is 32
-// consecutive bytes, blocks 2 g and 2 g + 1: MFMA j takes block 2 g + j as
-// hardware block g, and a row's four lanes read one whole line.
-constexpr int SK_WAVES = 8;
-constexpr int SK_THREADS = 64 * SK_WAVES;
+  const uint8_t* __restrict__ a;
+  const uint8_t* __restrict__ sa;
+  const uint8_t* __restrict__ b;
+  const uint8_t* __restrict__ sb;
+  int64_t m0, m_end, n0, N, K;
+  int64_t nks, nkb;
+  lds_u8 *st0, *st1;  // stages: A tile, then B tile
+  lds_u8 *ss0, *ss1;  // scale tiles of 16 bytes a row: A's rows, then B's
+  u32x4 ra, rb, rsa, rsb;
+  uint32_t voff_a, voff_b, a_step, b_step, svoff;
+  lds_u8* pf_scratch;  // L2 prefetch as in the 8-bit GEMM (gemm.hip)
+  uint32_t pf_row_a, pf_row_b, pf_a, pf_b;
 
-// One lane's operands of a chunk for one fragment of 16 rows.
-template <int F>
-struct SkFrag {
-  v4i lo[2], hi[2];  // hi: 8-bit operands only
-  uint32_t sc;       // scale bytes of MFMA 0 and 1
-
-  // p, s: the lane's row; c: chunk; full: the whole chunk lies in K
-  __device__ __forceinline__ void load(const uint8_t* __restrict__ p, const uint8_t* __restrict__ s,
-                                       int64_t c, int64_t K, int g, bool full) {
-    const int64_t nkb = K >> 5;
-    if (full) {
-      sc = *(const u16_at1*)(s + 8 * c + 2 * g);
+  __device__ __forceinline__ void setup(int wave, int lane) {
+    const int64_t mrows = m_end - m0, nrows = (N - n0) < ROWS ? (N - n0) : ROWS;
+    const int64_t pa = A4 ? K >> 1 : K, pb = K >> 1;
+    nks = (K + KS - 1) / KS;
+    nkb = K >> 5;
+    ra = make_rsrc(a + m0 * pa, mrows * pa);
+    rb = make_rsrc(b + n0 * pb, nrows * pb);
+    rsa = make_rsrc(sa + m0 * nkb, mrows * nkb);
+    rsb = make_rsrc(sb + n0 * nkb, nrows * nkb);
+    // A: load t = wave + 4 u covers LDS rows 8 t .. 8 t + 7; lane i lands in
+    // row r = 8 t + i / 8 at physical chunk i % 8, logical (i % 8) ^ swz(r)
+    const int sw = (4 * wave + (lane >> 4)) & 7;
+    voff_a = (uint32_t)((8 * wave + (lane >> 3)) * pa + 16 * ((lane & 7) ^ sw));
+    a_step = (uint32_t)(32 * pa);
+    if (A4) {
+      voff_b = (uint32_t)((8 * wave + (lane >> 3)) * pb + 16 * ((lane & 7) ^ sw));
+      b_step = (uint32_t)(32 * pb);
     } else {
-      sc = 0x7F7Fu;
-      for (int j = 0; j < 2; j++)
-        if (8 * c + 2 * g + j < nkb)
-          sc = (sc & ~(0xFFu << (8 * j))) | ((uint32_t)s[8 * c + 2 * g + j] << (8 * j));
+      // rows of 64 bytes: load t covers LDS rows 16 t .. 16 t + 15; lane i
+      // lands in row 16 t + i / 4 at chunk i % 4, logical (i % 4) ^ (i / 16)
+      voff_b = (uint32_t)((16 * wave + (lane >> 2)) * pb + 16 * ((lane & 3) ^ (lane >> 4)));
+      b_step = (uint32_t)(64 * pb);
     }
+    svoff = (uint32_t)((64 * wave + lane) * nkb);
+    pf_row_a = (uint32_t)((64 * wave + lane) * pa);
+    pf_row_b = (uint32_t)((64 * wave + lane) * pb);
+  }
+
+  // Loads of step kt into stage st; TAIL: the step may end past K, whose
+  // chunks read as zero.  A step past the last touches no memory.
+  template <bool TAIL>
+  __device__ __forceinline__ void load_a(lds_u8* st, int64_t kt, int u, int wave, int lane) {
+    const uint32_t base = kt < nks ? (uint32_t)(128 * kt) : OOB;
+    uint32_t off = voff_a + base + u * a_step;
+    if (TAIL) {
+      const int lc = (lane & 7) ^ ((4 * wave + (lane >> 4)) & 7);
+      off = 128 * kt + 16 * lc < (A4 ? K >> 1 : K) ? off : OOB;
+    }
+    dma16(st + (wave + 4 * u) * 1024, off, ra);
+  }
+  template <bool TAIL>
+  __device__ __forceinline__ void load_b(lds_u8* st, int64_t kt, int u, int wave, int lane) {
+    const uint32_t base = kt < nks ? (uint32_t)(BROW * kt) : OOB;
+    uint32_t off = voff_b + base + u * b_step;
+    if (TAIL) {
+      const int lc = A4 ? (lane & 7) ^ ((4 * wave + (lane >> 4)) & 7) : (lane & 3) ^ (lane >> 4);
+      off = BROW * kt + 16 * lc < (K >> 1) ? off : OOB;
+    }
+    dma16(st + A_BYTES + (wave + 4 * u) * 1024, off, rb);
+  }
+  template <bool TAIL>
+  __device__ __forceinline__ void issue_stage(lds_u8* st, int64_t kt, int wave, int lane) {
 #pragma unroll
-    for (int j = 0; j < 2; j++) {
-      if (F == ELEM_E2M1) {
-        const int b = 2 * g + j;
-        lo[j] = full || 8 * c + b < nkb ? *(const v4i*)(p + 128 * c + 16 * b) : (v4i){0, 0, 0, 0};
+    for (int u = 0; u < A_OPS; u++) load_a<TAIL>(st, kt, u, wave, lane);
+#pragma unroll
+    for (int u = 0; u < B_OPS; u++) load_b<TAIL>(st, kt, u, wave, lane);
+  }
+
+  // Scale bytes of GS steps, 16 bytes a row (K a multiple of 512)
+  __device__ __forceinline__ void issue_scales(lds_u8* buf, int64_t group, int wave) {
+    const uint32_t off = 16 * group < nkb ? svoff + (uint32_t)(16 * group) : OOB;
+    dma16(buf + wave * 1024, off, rsa);
+    dma16(buf + 4096 + wave * 1024, off, rsb);
+  }
+
+  // A row's scale bytes of one step (8 of them: `hi` the last four) as the
+  // word whose byte S + 2 h (4-bit A: MFMA h of half S) or S (8-bit A) is this
+  // lane half's.
+  __device__ __forceinline__ static uint32_t shape_scale(uint32_t lo, uint32_t hi, int g) {
+    if (A4) return __builtin_amdgcn_perm(hi, lo, g ? 0x07050301u : 0x06040200u);
+    return lo >> (16 * g);
+  }
+  __device__ __forceinline__ void read_scales(const lds_u8* buf, int q, int wm, int wn, int lane,
+                                              uint32_t* sar, uint32_t* sbr) {
+    const int g = lane >> 5, i = lane & 31;
+#pragma unroll
+    for (int f = 0; f < F; f++) {
+      const lds_u8* pa = buf + (32 * F * wm + 32 * f + i) * 16 + SB * q;
+      const lds_u8* pb = buf + 4096 + (32 * F * wn + 32 * f + i) * 16 + SB * q;
+      if (A4) {
+        const v2i x = *(const lds_v2i*)pa, y = *(const lds_v2i*)pb;
+        sar[f] = shape_scale((uint32_t)x.x, (uint32_t)x.y, g);
+        sbr[f] = shape_scale((uint32_t)y.x, (uint32_t)y.y, g);
       } else {
-        const int b = 2 * (g >> 1) + j;
-        const uint8_t* at = p + 256 * c + 32 * b + 16 * (g & 1);
-        lo[j] = full || 8 * c + b < nkb ? *(const v4i*)at : (v4i){0, 0, 0, 0};
-        hi[j] = full || 8 * c + b + 4 < nkb ? *(const v4i*)(at + 128) : (v4i){0, 0, 0, 0};
+        sar[f] = *(const lds_u16*)(pa + 2 * g);
+        sbr[f] = *(const lds_u16*)(pb + 2 * g);
       }
     }
   }
-  __device__ __forceinline__ v8i operand(int j) const {
-    if (F == ELEM_E2M1) return (v8i){lo[j].x, lo[j].y, lo[j].z, lo[j].w, 0, 0, 0, 0};
-    return (v8i){lo[j].x, lo[j].y, lo[j].z, lo[j].w, hi[j].x, hi[j].y, hi[j].z, hi[j].w};
-  }
-};
 
-template <int FA, int MF, int NF>
-struct SkChunk {
-  SkFrag<FA> a[MF];
-  SkFrag<ELEM_E2M1> b[NF];
-};
+  // Fragment f of an operand for half S of the step in stage st
+  template <int S>
+  __device__ __forceinline__ static v8i frag_a(const lds_u8* st, int wm, int f, int lane) {
+    return read_frag(st, 32 * F * wm + 32 * f + (lane & 31), S, lane >> 5);
+  }
+  template <int S>
+  __device__ __forceinline__ static v8i frag_b(const lds_u8* st, int wn, int f, int lane) {
+    const int row = 32 * F * wn + 32 * f + (lane & 31), g = lane >> 5;
+    if (A4) return read_frag(st + A_BYTES, row, S, g);
+    const v4i x = *(const lds_v4i*)(st + A_BYTES + row * 64 + (((2 * g + S) ^ ((row >> 2) & 3)) << 4));
+    return (v8i){x.x, x.y, x.z, x.w, 0, 0, 0, 0};
+  }
+  template <int S>
+  __device__ __forceinline__ static void read_frags(const lds_u8* st, int wm, int wn, int lane, v8i* af,
+                                                    v8i* bf) {
+#pragma unroll
+    for (int f = 0; f < F; f++) af[f] = frag_a<S>(st, wm, f, lane);
+#pragma unroll
+    for (int f = 0; f < F; f++) bf[f] = frag_b<S>(st, wn, f, lane);
+  }
 
-// Rows m0 .. m_end - 1 (at most 16 MF of them) x columns n0 .. of C.
-template <int FA, int MF, int NF>
-__device__ __forceinline__ void skinny_tile(const uint8_t* __restrict__ a, const uint8_t* __restrict__ sa,
-                                            const uint8_t* __restrict__ b, const uint8_t* __restrict__ sb,
-                                            uint16_t* __restrict__ c, int64_t m0, int64_t m_end,
-                                            int64_t n0, int64_t N, int64_t K, v4f* red) {
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int g = lane >> 4, i = lane & 15;
-  const int64_t pitch_a = FA == ELEM_E2M1 ? K >> 1 : K, pitch_b = K >> 1, nkb = K >> 5;
-  const uint8_t *pa[MF], *psa[MF], *pb[NF], *psb[NF];
-  // rows past the end repeat the last one; their results are not stored
-#pragma unroll
-  for (int f = 0; f < MF; f++) {
-    int64_t m = m0 + 16 * f + i;
-    m = m < m_end ? m : m_end - 1;
-    pa[f] = a + m * pitch_a;
-    psa[f] = sa + m * nkb;
+  __device__ __forceinline__ static v8i half_of(v8i v, int h) {
+    return h ? (v8i){v[4], v[5], v[6], v[7], 0, 0, 0, 0} : (v8i){v[0], v[1], v[2], v[3], 0, 0, 0, 0};
   }
+  template <int S>
+  __device__ __forceinline__ static void mma(const v8i* af, const v8i* bf, const uint32_t* sar,
+                                             const uint32_t* sbr, v16f (&acc)[F][F]) {
+    if constexpr (A4) {
 #pragma unroll
-  for (int f = 0; f < NF; f++) {
-    int64_t n = n0 + 16 * f + i;
-    n = n < N ? n : N - 1;
-    pb[f] = b + n * pitch_b;
-    psb[f] = sb + n * nkb;
-  }
-  v4f acc[NF][MF];
+      for (int fn = 0; fn < F; fn++)
 #pragma unroll
-  for (int x = 0; x < NF; x++)
+        for (int fm = 0; fm < F; fm++)
+          acc[fn][fm] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              half_of(bf[fn], 0), half_of(af[fm], 0), acc[fn][fm], ELEM_E2M1, ELEM_E2M1, S, (int)sbr[fn],
+              S, (int)sar[fm]);
 #pragma unroll
-    for (int y = 0; y < MF; y++) acc[x][y] = (v4f){0, 0, 0, 0};
-  auto load = [&](SkChunk<FA, MF, NF>& t, int64_t ch, bool full) {
+      for (int fn = 0; fn < F; fn++)
 #pragma unroll
-    for (int f = 0; f < NF; f++) t.b[f].load(pb[f], psb[f], ch, K, g, full);
-#pragma unroll
-    for (int f = 0; f < MF; f++) t.a[f].load(pa[f], psa[f], ch, K, g, full);
-  };
-  auto mma = [&](const SkChunk<FA, MF, NF>& t) {
-#pragma unroll
-    for (int j = 0; j < 2; j++)
-#pragma unroll
-      for (int x = 0; x < NF; x++)
-#pragma unroll
-        for (int y = 0; y < MF; y++) {
-          if (j == 0)
-            acc[x][y] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                t.b[x].operand(0), t.a[y].operand(0), acc[x][y], ELEM_E2M1, FA, 0, (int)t.b[x].sc, 0,
-                (int)t.a[y].sc);
-          else
-            acc[x][y] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                t.b[x].operand(1), t.a[y].operand(1), acc[x][y], ELEM_E2M1, FA, 1, (int)t.b[x].sc, 1,
-                (int)t.a[y].sc);
-        }
-  };
-  const int64_t whole = K >> 8;  // whole chunks
-  SkChunk<FA, MF, NF> t0, t1;
-  int64_t ch = wave;
-  if (ch < whole) load(t0, ch, true);
-  for (; ch < whole; ch += 2 * SK_WAVES) {
-    const bool two = ch + SK_WAVES < whole;
-    if (two) load(t1, ch + SK_WAVES, true);
-    mma(t0);
-    if (!two) break;
-    if (ch + 2 * SK_WAVES < whole) load(t0, ch + 2 * SK_WAVES, true);
-    mma(t1);
-  }
-  if ((K & 255) != 0 && wave == (int)(whole % SK_WAVES)) {
-    load(t0, whole, false);
-    mma(t0);
-  }
-  // lane l, element e of a fragment: column 4 (l / 16) + e, row l % 16
-#pragma unroll
-  for (int x = 0; x < NF; x++)
-#pragma unroll
-    for (int y = 0; y < MF; y++) red[((wave * NF + x) * MF + y) * 64 + lane] = acc[x][y];
-  __syncthreads();
-  for (int t = threadIdx.x; t < NF * MF * 64; t += SK_THREADS) {
-    v4f v = red[t];
-#pragma unroll
-    for (int w = 1; w < SK_WAVES; w++) v += red[w * NF * MF * 64 + t];
-    const int l = t & 63, f = t >> 6;
-    const int64_t m = m0 + 16 * (f % MF) + (l & 15);
-    const int64_t n = n0 + 16 * (f / MF) + 4 * (l >> 4);
-    if (m >= m_end) continue;
-    uint16_t* dst = c + m * N + n;
-    const uint32_t w[2] = {cvt_pk_bf16(v.x, v.y), cvt_pk_bf16(v.z, v.w)};
-    if ((N & 3) == 0 && n < N) {
-      *(u32x2*)dst = (u32x2){w[0], w[1]};
+        for (int fm = 0; fm < F; fm++)
+          acc[fn][fm] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              half_of(bf[fn], 1), half_of(af[fm], 1), acc[fn][fm], ELEM_E2M1, ELEM_E2M1, S + 2,
+              (int)sbr[fn], S + 2, (int)sar[fm]);
     } else {
 #pragma unroll
-      for (int e = 0; e < 4; e++)
-        if (n + e < N) dst[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+      for (int fn = 0; fn < F; fn++)
+#pragma unroll
+        for (int fm = 0; fm < F; fm++)
+          acc[fn][fm] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              bf[fn], af[fm], acc[fn][fm], ELEM_E2M1, FA, S, (int)sbr[fn], S, (int)sar[fm]);
     }
   }
-  __syncthreads();  // `red` may be written again
+  __device__ __forceinline__ static void clear(v16f (&acc)[F][F]) {
+#pragma unroll
+    for (int x = 0; x < F; x++)
+#pragma unroll
+      for (int y = 0; y < F; y++) acc[x][y] = (v16f){};
+  }
+
+  // ---- K a multiple of 512: scales through LDS, loads two steps ahead ----
+  // Phase A of step kt: MFMAs of half 0 on registers F0, reads of half 1 into
+  // F1; barrier: every wave has read stage kt, stage kt + 1 has landed; phase
+  // B: loads of stage kt + 2 into the buffer just released, MFMAs of half 1,
+  // reads of half 0 of stage kt + 1 and of its scales.  The waits leave the
+  // two latest vector-memory operations in flight: a step's L2 prefetches.
+  __device__ __forceinline__ void prefetch(int64_t kt, int wave) {
+    const uint32_t live = kt < nks ? 0u : OOB;
+    prefetch_lines(pf_scratch + wave * 512, (pf_row_a + (uint32_t)(128 * kt)) | pf_a | live, ra);
+    prefetch_lines(pf_scratch + wave * 512 + 256, (pf_row_b + (uint32_t)(BROW * kt)) | pf_b | live, rb);
+  }
+  template <int U>
+  __device__ __forceinline__ void step(lds_u8* cur, lds_u8* nxt, const lds_u8* sread, lds_u8* sdma,
+                                       int64_t kt, int wave, int wm, int wn, int lane, uint32_t* sc_a,
+                                       uint32_t* sc_b, v8i* f0a, v8i* f0b, v8i* f1a, v8i* f1b,
+                                       v16f (&acc)[F][F]) {
+    uint32_t nx_a[F], nx_b[F];
+    read_frags<1>(cur, wm, wn, lane, f1a, f1b);
+    mma<0>(f0a, f0b, sc_a, sc_b, acc);
+    interleave<DS_READS>();
+    wait_vm_but_prefetch();
+    __syncthreads();
+    if (U == 0) issue_scales(sdma, kt / GS + 1, wave);
+    read_scales(sread, (U + 1) % GS, wm, wn, lane, nx_a, nx_b);
+#pragma unroll
+    for (int f = 0; f < F; f++) {
+      f0a[f] = frag_a<0>(nxt, wm, f, lane);
+#pragma unroll
+      for (int u = f * A_OPS / F; u < (f + 1) * A_OPS / F; u++) load_a<false>(cur, kt + 2, u, wave, lane);
+    }
+#pragma unroll
+    for (int f = 0; f < F; f++) {
+      f0b[f] = frag_b<0>(nxt, wn, f, lane);
+#pragma unroll
+      for (int u = f * B_OPS / F; u < (f + 1) * B_OPS / F; u++) load_b<false>(cur, kt + 2, u, wave, lane);
+    }
+    prefetch(kt + PF_DIST, wave);
+    mma<1>(f1a, f1b, sc_a, sc_b, acc);
+    interleave<DS_READS + 2 * F>();
+#pragma unroll
+    for (int f = 0; f < F; f++) {
+      sc_a[f] = nx_a[f];
+      sc_b[f] = nx_b[f];
+    }
+  }
+  // MFMA, LDS read, MFMA, ... for half a step's instructions
+  template <int NDS>
+  __device__ __forceinline__ static void interleave() {
+    constexpr int n = F * F * (A4 ? 2 : 1), per = (NDS + n - 1) / n;
+#pragma unroll
+    for (int i = 0; i < n; i++) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, per, 0);
+    }
+  }
+
+  // The prologue in parts, for a caller that starts a tile's loads while it
+  // stores the last one's result: first() loads stage 0 and its scales,
+  // second() stage 1; run() waits for stage 0 (with `stored`, NST stores
+  // were issued between the two) and runs the K loop.
+  __device__ __forceinline__ void first(int wave, int lane) {
+    issue_stage<false>(st0, 0, wave, lane);
+    issue_scales(ss0, 0, wave);
+  }
+  __device__ __forceinline__ void second(int wave, int lane) { issue_stage<false>(st1, 1, wave, lane); }
+  template <int NST>
+  __device__ __forceinline__ void run(v16f (&acc)[F][F], int wave, int lane, bool stored) {
+    const int wm = wave & 1, wn = wave >> 1;
+    clear(acc);
+    if (stored)
+      wait_vm<NST + A_OPS + B_OPS>();
+    else
+      wait_vm<A_OPS + B_OPS>();
+    __syncthreads();
+    uint32_t sc_a[F], sc_b[F];
+    v8i f0a[F], f0b[F], f1a[F], f1b[F];
+    read_scales(ss0, 0, wm, wn, lane, sc_a, sc_b);
+    prefetch(2, wave);
+    read_frags<0>(st0, wm, wn, lane, f0a, f0b);
+    for (int64_t j = 0; j * GS < nks; j++) {
+      const int64_t kt = j * GS;
+      lds_u8 *scur = (j & 1) ? ss1 : ss0, *snxt = (j & 1) ? ss0 : ss1;
+      if constexpr (GS == 2) {
+        step<0>(st0, st1, scur, snxt, kt, wave, wm, wn, lane, sc_a, sc_b, f0a, f0b, f1a, f1b, acc);
+        step<1>(st1, st0, snxt, snxt, kt + 1, wave, wm, wn, lane, sc_a, sc_b, f0a, f0b, f1a, f1b, acc);
+      } else {
+        step<0>(st0, st1, scur, snxt, kt, wave, wm, wn, lane, sc_a, sc_b, f0a, f0b, f1a, f1b, acc);
+        step<1>(st1, st0, scur, snxt, kt + 1, wave, wm, wn, lane, sc_a, sc_b, f0a, f0b, f1a, f1b, acc);
+        step<2>(st0, st1, scur, snxt, kt + 2, wave, wm, wn, lane, sc_a, sc_b, f0a, f0b, f1a, f1b, acc);
+        step<3>(st1, st0, snxt, snxt, kt + 3, wave, wm, wn, lane, sc_a, sc_b, f0a, f0b, f1a, f1b, acc);
+      }
+    }
+  }
+
+  // ---- any K: scales from memory, loads one step ahead ----
+  // A row's scale bytes of step kt; blocks past K get 1.0 (their payload is 0)
+  __device__ __forceinline__ uint32_t load_scale(const uint8_t* __restrict__ row, int64_t kt, int g) const {
+    const int64_t kb = SB * kt;
+    uint32_t lo, hi = 0;
+    if (kb + SB <= nkb) {
+      lo = *(const u32_at1*)(row + kb);
+      if (A4) hi = *(const u32_at1*)(row + kb + 4);
+    } else {
+      lo = hi = 0x7F7F7F7Fu;
+      for (int e = 0; e < SB; e++)
+        if (kb + e < nkb) {
+          uint32_t& w = e < 4 ? lo : hi;
+          w = (w & ~(0xFFu << (8 * (e & 3)))) | ((uint32_t)row[kb + e] << (8 * (e & 3)));
+        }
+    }
+    return shape_scale(lo, hi, g);
+  }
+  __device__ __forceinline__ void run_any(v16f (&acc)[F][F], int wave, int lane) {
+    const int wm = wave & 1, wn = wave >> 1, g = lane >> 5, i = lane & 31;
+    clear(acc);
+    const uint8_t *rowa[F], *rowb[F];  // rows past the end repeat the last one; not stored
+#pragma unroll
+    for (int f = 0; f < F; f++) {
+      int64_t m = m0 + 32 * F * wm + 32 * f + i, n = n0 + 32 * F * wn + 32 * f + i;
+      rowa[f] = sa + (m < m_end ? m : m_end - 1) * nkb;
+      rowb[f] = sb + (n < N ? n : N - 1) * nkb;
+    }
+    uint32_t sc_a[F], sc_b[F], nx_a[F], nx_b[F];
+    issue_stage<true>(st0, 0, wave, lane);
+#pragma unroll
+    for (int f = 0; f < F; f++) {
+      nx_a[f] = load_scale(rowa[f], 0, g);
+      nx_b[f] = load_scale(rowb[f], 0, g);
+    }
+    for (int64_t kt = 0; kt < nks; kt++) {
+      lds_u8 *cur = (kt & 1) ? st1 : st0, *nxt = (kt & 1) ? st0 : st1;
+      // this wave's loads of stage kt have landed, then every wave's; and
+      // every wave is done reading the other stage
+      wait_vm_all();
+      __syncthreads();
+#pragma unroll
+      for (int f = 0; f < F; f++) {
+        sc_a[f] = nx_a[f];
+        sc_b[f] = nx_b[f];
+      }
+      if (kt + 1 < nks) {
+        issue_stage<true>(nxt, kt + 1, wave, lane);
+#pragma unroll
+        for (int f = 0; f < F; f++) {
+          nx_a[f] = load_scale(rowa[f], kt + 1, g);
+          nx_b[f] = load_scale(rowb[f], kt + 1, g);
+        }
+      }
+      v8i af[F], bf[F], ag[F], bg[F];
+      read_frags<0>(cur, wm, wn, lane, af, bf);
+      read_frags<1>(cur, wm, wn, lane, ag, bg);
+      mma<0>(af, bf, sc_a, sc_b, acc);
+      mma<1>(ag, bg, sc_a, sc_b, acc);
+    }
+  }
+
+  // The result from registers, any N: lanes l and l + 32 trade groups so that
+  // a lane holds eight consecutive columns, as in gemm_common.h.
+  __device__ __forceinline__ void store(const v16f (&acc)[F][F], uint16_t* __restrict__ c, int wave,
+                                        int lane) const {
+    const int wm = wave & 1, wn = wave >> 1, g = lane >> 5, i = lane & 31;
+    const bool vec = (N & 7) == 0;
+#pragma unroll
+    for (int fn = 0; fn < F; fn++)
+#pragma unroll
+      for (int fm = 0; fm < F; fm++) {
+        const v16f& v = acc[fn][fm];
+        uint32_t p[4][2];
+#pragma unroll
+        for (int r4 = 0; r4 < 4; r4++) {
+          p[r4][0] = cvt_pk_bf16(v[4 * r4 + 0], v[4 * r4 + 1]);
+          p[r4][1] = cvt_pk_bf16(v[4 * r4 + 2], v[4 * r4 + 3]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+          for (int d = 0; d < 2; d++) {
+            const auto s = __builtin_amdgcn_permlane32_swap(p[2 * h][d], p[2 * h + 1][d], false, false);
+            p[2 * h][d] = s[0];
+            p[2 * h + 1][d] = s[1];
+          }
+        const int64_t m = m0 + 32 * F * wm + 32 * fm + i;
+        if (m >= m_end) continue;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          const int64_t n = n0 + 32 * F * wn + 32 * fn + 16 * h + 8 * g;
+          const uint32_t w[4] = {p[2 * h][0], p[2 * h][1], p[2 * h + 1][0], p[2 * h + 1][1]};
+          uint16_t* dst = c + m * N + n;
+          if (vec && n + 8 <= N) {
+            *(uint4*)dst = make_uint4(w[0], w[1], w[2], w[3]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+              if (n + e < N) dst[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+          }
+        }
+      }
+  }
+};
+
+// Any K and N, one tile per workgroup.
+template <int FA, int F>
+__global__ void __launch_bounds__(NT)
+gemm4_any_kernel(const uint8_t* __restrict__ a, const uint8_t* __restrict__ sa,
+                 const uint8_t* __restrict__ b, const uint8_t* __restrict__ sb, uint16_t* __restrict__ c,
+                 int64_t M, int64_t N, int64_t K) {
+  typedef Tile4<FA, F> T;
+  __shared__ __attribute__((aligned(16))) uint8_t s0[T::A_BYTES + T::B_BYTES];
+  __shared__ __attribute__((aligned(16))) uint8_t s1[T::A_BYTES + T::B_BYTES];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int64_t mt, nt;
+  tile_of(blockIdx.x, (M + T::ROWS - 1) / T::ROWS, (N + T::ROWS - 1) / T::ROWS, mt, nt);
+  T t;
+  t.a = a, t.sa = sa, t.b = b, t.sb = sb;
+  t.m0 = mt * T::ROWS;
+  t.m_end = t.m0 + T::ROWS < M ? t.m0 + T::ROWS : M;
+  t.n0 = nt * T::ROWS;
+  t.N = N, t.K = K;
+  t.st0 = (lds_u8*)s0, t.st1 = (lds_u8*)s1;
+  t.setup(wave, lane);
+  v16f acc[F][F];
+  t.run_any(acc, wave, lane);
+  t.store(acc, c, wave, lane);
 }
 
-template <int FA, int MF, int NF>
-__global__ void __launch_bounds__(SK_THREADS)
-gemm4_skinny_kernel(const uint8_t* __restrict__ a, const uint8_t* __restrict__ sa,
-                    const uint8_t* __restrict__ b, const uint8_t* __restrict__ sb,
-                    uint16_t* __restrict__ c, int64_t M, int64_t N, int64_t K) {
-  __shared__ v4f red[SK_WAVES * NF * MF * 64];
-  for (int64_t m0 = (int64_t)blockIdx.y * 16 * MF; m0 < M; m0 += (int64_t)gridDim.y * 16 * MF)
-    skinny_tile<FA, MF, NF>(a, sa, b, sb, c, m0, m0 + 16 * MF < M ? m0 + 16 * MF : M,
-                            (int64_t)blockIdx.x * 16 * NF, N, K, red);
+// Persistent, K a multiple of 512 and N of 8: one workgroup per compute unit
+// walks tiles bid, bid + grid, ...; a tile's first loads run while the last
+// one's result is stored.
+template <int FA>
+__global__ void __launch_bounds__(NT)
+gemm4_persistent_kernel(const uint8_t* __restrict__ a, const uint8_t* __restrict__ sa,
+                        const uint8_t* __restrict__ b, const uint8_t* __restrict__ sb,
+                        uint16_t* __restrict__ c, int64_t M, int64_t N, int64_t K) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem0[STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t smem1[STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t sscale[2 * SCALE_TILE];
+  __shared__ __attribute__((aligned(16))) uint8_t spf[2048];
+  const int64_t nm = (M + BM - 1) / BM, nn = (N + BN - 1) / BN, tiles = nm * nn;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  typedef Tile4<FA, 4> T;
+  auto make = [&](int64_t t, T& tl) {
+    int64_t mt, nt;
+    tile_of(t, nm, nn, mt, nt);
+    tl.a = a, tl.sa = sa, tl.b = b, tl.sb = sb;
+    tl.m0 = mt * BM;
+    tl.m_end = (mt + 1) * BM < M ? (mt + 1) * BM : M;
+    tl.n0 = nt * BN;
+    tl.N = N, tl.K = K;
+    tl.st0 = (lds_u8*)smem0, tl.st1 = (lds_u8*)smem1;
+    tl.ss0 = (lds_u8*)sscale, tl.ss1 = (lds_u8*)sscale + SCALE_TILE;
+    tl.pf_scratch = (lds_u8*)spf;
+    tl.pf_a = (nt % (32 / GM_TILES) == 0) ? 0u : OOB;
+    tl.pf_b = (mt % GM_TILES == 0 && !tile_runs_rr((uint32_t)nm, (uint32_t)nn)) ? 0u : OOB;
+  };
+  int64_t t = blockIdx.x;
+  if (t >= tiles) return;
+  T tl;
+  make(t, tl);
+  tl.setup(wave, lane);
+  tl.first(wave, lane);
+  bool stored = false;
+  for (;;) {
+    tl.second(wave, lane);
+    v16f acc[4][4];
+    tl.template run<32>(acc, wave, lane, stored);
+    const int64_t m0 = tl.m0, m_end = tl.m_end, n0 = tl.n0;
+    // every load has landed (none may still be writing LDS) and every wave
+    // is past its last read of the stage and scale buffers
+    wait_vm_all();
+    __syncthreads();
+    t += gridDim.x;
+    const bool more = __builtin_amdgcn_readfirstlane((int)(t < tiles)) != 0;
+    if (more) {
+      make(t, tl);
+      tl.setup(wave, lane);
+      tl.first(wave, lane);
+    }
+    store_tile_bf16_lds_halves(acc, (lds_u8*)smem1, c, N, m0, m_end, n0, N, wave & 1, wave >> 1, wave,
+                               lane);
+    stored = true;
+    if (!more) break;
+  }
 }
 
-template <int FA, int MF, int NF>
-__global__ void __launch_bounds__(SK_THREADS)
-grouped4_skinny_kernel(const int64_t* __restrict__ offsets, int64_t T,
-                       const uint8_t* __restrict__ a, const uint8_t* __restrict__ sa,
-                       const uint8_t* __restrict__ b, const uint8_t* __restrict__ sb,
-                       uint16_t* __restrict__ c, int64_t N, int64_t K) {
-  __shared__ v4f red[SK_WAVES * NF * MF * 64];
-  const int64_t g = blockIdx.y;
-  // clamped, so that bad offsets read and write rows of [0, T) only
-  int64_t lo = offsets[g], hi = offsets[g + 1];
-  lo = lo < 0 ? 0 : (lo > T ? T : lo);
-  hi = hi < lo ? lo : (hi > T ? T : hi);
-  for (int64_t m0 = lo; m0 < hi; m0 += 16 * MF)
-    skinny_tile<FA, MF, NF>(a, sa, b + g * N * (K >> 1), sb + g * N * (K >> 5), c, m0,
-                            m0 + 16 * MF < hi ? m0 + 16 * MF : hi, (int64_t)blockIdx.x * 16 * NF, N, K,
-                            red);
+// Grouped: every workgroup derives the tile list from the device-side offsets
+// (clamped into [0, T] and made non-decreasing, so bad offsets never address
+// outside the operands) and walks it with a static stride, the tiles of a
+// group in the dense kernel's order.  FAST: K a multiple of 512, N of 8.
+template <int FA, bool FAST>
+__global__ void __launch_bounds__(NT)
+grouped_gemm4_kernel(int64_t G, const int64_t* __restrict__ offsets, int64_t T_, int64_t N, int64_t K,
+                     const uint8_t* __restrict__ a, const uint8_t* __restrict__ sa,
+                     const uint8_t* __restrict__ b, const uint8_t* __restrict__ sb,
+                     uint16_t* __restrict__ c) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem0[STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t smem1[STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t sscale[2 * SCALE_TILE];
+  __shared__ __attribute__((aligned(16))) uint8_t spf[2048];
+  __shared__ int64_t s_off[MAX_GROUPS + 1];
+  __shared__ int64_t s_pre[MAX_GROUPS + 1];
+  const int64_t nn = (N + BN - 1) / BN;
+  for (int64_t g = threadIdx.x; g <= G; g += NT) {
+    const int64_t o = offsets[g];
+    s_off[g] = o < 0 ? 0 : (o > T_ ? T_ : o);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int64_t prev = 0, acc = 0;
+    for (int64_t g = 0; g < G; g++) {
+      const int64_t lo = s_off[g] > prev ? s_off[g] : prev;
+      const int64_t hi = s_off[g + 1] > lo ? s_off[g + 1] : lo;
+      s_off[g] = lo;
+      prev = lo;
+      s_pre[g] = acc;
+      acc += ((hi - lo + BM - 1) / BM) * nn;
+    }
+    s_off[G] = s_off[G] > prev ? s_off[G] : prev;
+    s_pre[G] = acc;
+  }
+  __syncthreads();
+  const int64_t total = s_pre[G];
+  const int64_t nwg = gridDim.x, bid = blockIdx.x;
+  const int64_t wg = (bid & 7) * (nwg >> 3) + (bid >> 3);  // contiguous tile runs per XCD
+  // tile indices fit in 32 bits (the host checks the tile count)
+  const uint32_t span = GM_TILES * (uint32_t)nn;
+  int64_t g = 0;  // largest g with s_pre[g] <= t: searched once, then advanced
+  {
+    int64_t hi = G;
+    while (hi - g > 1) {
+      const int64_t mid = (g + hi) >> 1;
+      if (s_pre[mid] <= wg) g = mid; else hi = mid;
+    }
+  }
+  typedef Tile4<FA, 4> T;
+  auto make = [&](int64_t t, T& tl) {
+    while (s_pre[g + 1] <= t) g++;  // s_pre[G] = total > t stops it
+    const uint32_t local = (uint32_t)(t - s_pre[g]);
+    const uint32_t nmg = (uint32_t)((s_off[g + 1] - s_off[g] + BM - 1) / BM);
+    const uint32_t run = local / span;
+    const uint32_t top = run * GM_TILES;
+    const uint32_t gsz = (nmg - top) < (uint32_t)GM_TILES ? (nmg - top) : (uint32_t)GM_TILES;
+    const uint32_t in = local - run * span;
+    const uint32_t nt = in / gsz;
+    const int64_t mt = top + (in - nt * gsz);
+    tl.a = a, tl.sa = sa;
+    tl.b = b + g * N * (K >> 1);
+    tl.sb = sb + g * N * (K >> 5);
+    tl.m0 = s_off[g] + mt * BM;
+    tl.m_end = (tl.m0 + BM) < s_off[g + 1] ? tl.m0 + BM : s_off[g + 1];
+    tl.n0 = (int64_t)nt * BN;
+    tl.N = N, tl.K = K;
+    tl.st0 = (lds_u8*)smem0, tl.st1 = (lds_u8*)smem1;
+    tl.ss0 = (lds_u8*)sscale, tl.ss1 = (lds_u8*)sscale + SCALE_TILE;
+    tl.pf_scratch = (lds_u8*)spf;
+    tl.pf_a = (nt % (32 / GM_TILES) == 0) ? 0u : OOB;
+    tl.pf_b = (mt == top && nn > 32) ? 0u : OOB;
+  };
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int64_t t = wg;
+  if (t >= total) return;
+  T tl;
+  if constexpr (FAST) {
+    make(t, tl);
+    tl.setup(wave, lane);
+    tl.first(wave, lane);
+    bool stored = false;
+    for (;;) {
+      tl.second(wave, lane);
+      v16f acc[4][4];
+      tl.template run<32>(acc, wave, lane, stored);
+      const int64_t m0 = tl.m0, m_end = tl.m_end, n0 = tl.n0;
+      wait_vm_all();
+      __syncthreads();
+      t += nwg;
+      const bool more = __builtin_amdgcn_readfirstlane((int)(t < total)) != 0;
+      if (more) {
+        make(t, tl);
+        tl.setup(wave, lane);
+        tl.first(wave, lane);
+      }
+      store_tile_bf16_lds_halves(acc, (lds_u8*)smem1, c, N, m0, m_end, n0, N, wave & 1, wave >> 1, wave,
+                                 lane);
+      stored = true;
+      if (!more) break;
+    }
+  } else {
+    for (; t < total; t += nwg) {
+      make(t, tl);
+      tl.setup(wave, lane);
+      v16f acc[4][4];
+      tl.run_any(acc, wave, lane);
+      tl.store(acc, c, wave, lane);
+      __syncthreads();  // the stages are free again
+    }
+  }
+}
+
+// K and N that the pipelined kernels take: whole groups of 16 scale bytes,
+// whole 16-byte chunks of a result row, 32-bit offsets within a tile's rows.
+static bool pipelined(int64_t N, int64_t K) {
+  return K % 512 == 0 && N % 8 == 0 && (int64_t)BM * N * 2 < ((int64_t)1 << 31);
 }
 
 template <int FA>
-static void launch_skinny(int64_t M, int64_t N, int64_t K, const uint8_t* a, const uint8_t* sa,
-                          const uint8_t* b, const uint8_t* sb, uint16_t* c, hipStream_t stream) {
-  const unsigned gx = (unsigned)((N + 31) / 32);
-#define MX_SKINNY(MF_)                                                                            \
-  do {                                                                                            \
-    const int64_t gy = (M + 16 * MF_ - 1) / (16 * MF_);                                           \
-    hipLaunchKernelGGL((gemm4_skinny_kernel<FA, MF_, 2>), dim3(gx, (unsigned)(gy < 65535 ? gy : 65535)), \
-                       dim3(SK_THREADS), 0, stream, a, sa, b, sb, c, M, N, K);                    \
-  } while (0)
-  if (M <= 16) MX_SKINNY(1);
-  else if (M <= 32) MX_SKINNY(2);
-  else MX_SKINNY(4);
-#undef MX_SKINNY
+static void launch_many(int64_t M, int64_t N, int64_t K, const uint8_t* a, const uint8_t* sa,
+                        const uint8_t* b, const uint8_t* sb, uint16_t* c, int num_cus,
+                        hipStream_t stream) {
+  const int64_t tiles = ((M + BM - 1) / BM) * ((N + BN - 1) / BN);
+  const int64_t cus = (num_cus > 8 ? num_cus : 256) / 8 * 8;
+  if (pipelined(N, K))
+    hipLaunchKernelGGL((gemm4_persistent_kernel<FA>), dim3((unsigned)(tiles < cus ? tiles : cus)), dim3(NT), 0,
+                       stream, a, sa, b, sb, c, M, N, K);
+  else
+    hipLaunchKernelGGL((gemm4_any_kernel<FA, 4>), dim3((unsigned)tiles), dim3(NT), 0, stream, a, sa, b, sb, c,
+                       M, N, K);
 }
 
 hipError_t launch_gemm4(int a_elem, int64_t M, int64_t N, int64_t K, const void* a, const void* sa,
                         const void* b, const void* sb, void* c, int num_cus, hipStream_t stream) {
+  if (M <= 64) return launch_gemm4_few(a_elem, M, N, K, a, sa, b, sb, c, stream);
   const uint8_t *A = (const uint8_t*)a, *SA = (const uint8_t*)sa, *B = (const uint8_t*)b,
                 *SB = (const uint8_t*)sb;
   uint16_t* C = (uint16_t*)c;
-  if (a_elem == ELEM_E4M3) launch_skinny<ELEM_E4M3>(M, N, K, A, SA, B, SB, C, stream);
-  else if (a_elem == ELEM_E5M2) launch_skinny<ELEM_E5M2>(M, N, K, A, SA, B, SB, C, stream);
-  else if (a_elem == ELEM_E2M1) launch_skinny<ELEM_E2M1>(M, N, K, A, SA, B, SB, C, stream);
+  if (a_elem == ELEM_E4M3) launch_many<ELEM_E4M3>(M, N, K, A, SA, B, SB, C, num_cus, stream);
+  else if (a_elem == ELEM_E5M2) launch_many<ELEM_E5M2>(M, N, K, A, SA, B, SB, C, num_cus, stream);
+  else if (a_elem == ELEM_E2M1) launch_many<ELEM_E2M1>(M, N, K, A, SA, B, SB, C, num_cus, stream);
   else return hipErrorInvalidValue;
   return hipGetLastError();
 }
@@ -233,22 +642,27 @@ hipError_t launch_grouped_gemm4(int a_elem, int64_t G, const int64_t* offsets, i
                                 int64_t K, const void* a, const void* sa, const void* b,
                                 const void* sb, void* c, int num_cus, hipStream_t stream) {
   if (G < 1 || G > MAX_GROUPS) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)((N + 31) / 32), (unsigned)G);
-#define MX_GSKINNY(FA_, MF_)                                                                      \
-  hipLaunchKernelGGL((grouped4_skinny_kernel<FA_, MF_, 2>), grid, dim3(SK_THREADS), 0, stream, offsets, \
-                     T, (const uint8_t*)a, (const uint8_t*)sa, (const uint8_t*)b, (const uint8_t*)sb, \
-                     (uint16_t*)c, N, K)
-#define MX_GSKINNY_M(FA_)               \
-  do {                                  \
-    if (T <= 16 * G) MX_GSKINNY(FA_, 1); \
-    else MX_GSKINNY(FA_, 4);            \
+  if (T <= 64 * G) return launch_grouped_gemm4_few(a_elem, G, offsets, T, N, K, a, sa, b, sb, c, stream);
+  const int64_t upper = ((T + BM - 1) / BM + G) * ((N + BN - 1) / BN);
+  int64_t wgs = ((num_cus > 0 ? num_cus : 256) + 7) / 8 * 8;
+  if (upper < wgs) wgs = (upper + 7) / 8 * 8;
+  const bool fast = pipelined(N, K);
+#define MX_GROUPED4(FA_)                                                                          \
+  do {                                                                                            \
+    if (fast)                                                                                     \
+      hipLaunchKernelGGL((grouped_gemm4_kernel<FA_, true>), dim3((unsigned)wgs), dim3(NT), 0, stream, G, \
+                         offsets, T, N, K, (const uint8_t*)a, (const uint8_t*)sa, (const uint8_t*)b, \
+                         (const uint8_t*)sb, (uint16_t*)c);                                       \
+    else                                                                                          \
+      hipLaunchKernelGGL((grouped_gemm4_kernel<FA_, false>), dim3((unsigned)wgs), dim3(NT), 0, stream, G, \
+                         offsets, T, N, K, (const uint8_t*)a, (const uint8_t*)sa, (const uint8_t*)b, \
+                         (const uint8_t*)sb, (uint16_t*)c);                                       \
   } while (0)
-  if (a_elem == ELEM_E4M3) MX_GSKINNY_M(ELEM_E4M3);
-  else if (a_elem == ELEM_E5M2) MX_GSKINNY_M(ELEM_E5M2);
-  else if (a_elem == ELEM_E2M1) MX_GSKINNY_M(ELEM_E2M1);
+  if (a_elem == ELEM_E4M3) MX_GROUPED4(ELEM_E4M3);
+  else if (a_elem == ELEM_E5M2) MX_GROUPED4(ELEM_E5M2);
+  else if (a_elem == ELEM_E2M1) MX_GROUPED4(ELEM_E2M1);
   else return hipErrorInvalidValue;
-#undef MX_GSKINNY_M
-#undef MX_GSKINNY
+#undef MX_GROUPED4
   return hipGetLastError();
 }
 
