@@ -474,9 +474,18 @@ mx_status mx_dequant(mx_elem_type elem, const void* q, const void* s, int64_t ro
  *   the operands (MX_ERR_INVALID_ARG).
  * The forward product takes mx_quant4's row blocks of the weight, the
  * backward one its column blocks.  Requires K % 32 == 0, K < 2^23, N < 2^28.
- * K == 0 writes zeros; M == 0 or N == 0 is a no-op. */
+ * K == 0 writes zeros; M == 0 or N == 0 is a no-op.
+ *   workspace: DEVICE scratch of at least mx_gemm4_workspace_size bytes, 16-byte
+ *   aligned, for sums of a split contraction (NULL where that size is 0);
+ *   written and read by the call's own kernels only, so calls on one stream
+ *   may share it, calls that may run at the same time not. */
 mx_status mx_gemm4(mx_elem_type a_elem, int64_t M, int64_t N, int64_t K, const void* a,
-                   const void* sa, const void* b, const void* sb, void* c, hipStream_t stream);
+                   const void* sa, const void* b, const void* sb, void* c, void* workspace,
+                   size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of device workspace mx_gemm4 needs.  Pure host function, no HIP call;
+ * 0 for sizes that mx_gemm4 rejects. */
+size_t mx_gemm4_workspace_size(mx_elem_type a_elem, int64_t M, int64_t N, int64_t K);
 
 /* mx_gemm4 over per-expert token groups: rows offsets[g] .. offsets[g+1] - 1
  * of c are those of a times b[g]^T, b [G, N, K/2], sb [G, N, K/32].  offsets:

@@ -37,7 +37,8 @@ __all__ = [
     "mx_grad_norm_workspace_size", "Routing", "route", "route_backward", "dispatch",
     "dispatch_quant", "combine", "combine_backward", "grad_norm", "grad_clip", "SCORES",
     "GROUP_VALUES",
-    "mx_quant4", "mx_dequant", "mx_gemm4", "mx_grouped_gemm4", "mx_swiglu_quant",
+    "mx_quant4", "mx_dequant", "mx_gemm4", "mx_gemm4_workspace_size", "mx_grouped_gemm4",
+    "mx_swiglu_quant",
     "mx_swiglu_backward", "mx_swiglu_backward_quant", "mx_requant_col", "mx_requant_grouped_col",
     "quant4", "dequant", "gemm4", "grouped_gemm4", "swiglu_quant", "swiglu_backward",
     "swiglu_backward_quant", "requant_col", "requant_grouped_col", "OPERAND_ELEMS",
@@ -141,7 +142,9 @@ def lib() -> ctypes.CDLL:
         L.mx_dequant.restype = c_int
         L.mx_dequant.argtypes = [c_int, vp, vp, i64, i64, vp, vp]
         L.mx_gemm4.restype = c_int
-        L.mx_gemm4.argtypes = [c_int, i64, i64, i64, vp, vp, vp, vp, vp, vp]
+        L.mx_gemm4.argtypes = [c_int, i64, i64, i64, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.mx_gemm4_workspace_size.restype = sz
+        L.mx_gemm4_workspace_size.argtypes = [c_int, i64, i64, i64]
         L.mx_grouped_gemm4.restype = c_int
         L.mx_grouped_gemm4.argtypes = [c_int, i64, vp, i64, i64, i64, vp, vp, vp, vp, vp, vp]
         L.mx_swiglu_quant.restype = c_int
@@ -299,8 +302,12 @@ def mx_dequant(elem, q, s, rows, cols, y, stream) -> int:
     return lib().mx_dequant(elem, q, s, rows, cols, y, stream)
 
 
-def mx_gemm4(a_elem, M, N, K, a, sa, b, sb, c, stream) -> int:
-    return lib().mx_gemm4(a_elem, M, N, K, a, sa, b, sb, c, stream)
+def mx_gemm4(a_elem, M, N, K, a, sa, b, sb, c, workspace, workspace_bytes, stream) -> int:
+    return lib().mx_gemm4(a_elem, M, N, K, a, sa, b, sb, c, workspace, workspace_bytes, stream)
+
+
+def mx_gemm4_workspace_size(a_elem, M, N, K) -> int:
+    return lib().mx_gemm4_workspace_size(a_elem, M, N, K)
 
 
 def mx_grouped_gemm4(a_elem, G, offsets, T, N, K, a, sa, b, sb, c, stream) -> int:
@@ -989,7 +996,9 @@ def gemm4(a, sa, b, sb, a_elem: str = "e4m3", out=None):
         _shape(b, (N, K // 2), "b")
         _shape(sb, (N, K // 32), "sb")
     out, given = _out(out, (M, N), a.device)
-    _check(mx_gemm4(code, M, N, K, _ptr(a), _ptr(sa), _ptr(b), _ptr(sb), _ptr(out),
+    nws = mx_gemm4_workspace_size(code, M, N, K)
+    ws = torch.empty(nws, dtype=torch.uint8, device=a.device) if nws else None
+    _check(mx_gemm4(code, M, N, K, _ptr(a), _ptr(sa), _ptr(b), _ptr(sb), _ptr(out), _ptr(ws), nws,
                     _stream(a.device)))
     if given:
         _written(out)

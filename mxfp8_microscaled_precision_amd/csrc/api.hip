@@ -867,22 +867,35 @@ mx_status mx_dequant(mx_elem_type elem, const void* q, const void* s, int64_t ro
   return MX_OK;
 }
 
+size_t mx_gemm4_workspace_size(mx_elem_type a_elem, int64_t M, int64_t N, int64_t K) {
+  if (!is_elem(a_elem) || M < 1 || N < 1 || K < 1 || K % 32 != 0 || K >= K_LIMIT ||
+      N >= GEMM4_N_LIMIT || mul_overflows(M, N) || grid_too_large(4 * gemm_tiles(M, N)))
+    return 0;
+  return mx::gemm4_workspace(M, N, K);
+}
+
 mx_status mx_gemm4(mx_elem_type a_elem, int64_t M, int64_t N, int64_t K, const void* a,
-                   const void* sa, const void* b, const void* sb, void* c, hipStream_t stream) {
+                   const void* sa, const void* b, const void* sb, void* c, void* workspace,
+                   size_t workspace_bytes, hipStream_t stream) {
   g_err[0] = '\0';
   mx_status st = check_gemm4(a_elem, M, 1, N, K);
   if (st != MX_OK) return st;
-  if (grid_too_large(gemm_tiles(M, N)))
+  // a tile of 256 x 256 is up to four workgroups
+  if (M > (INT64_MAX >> 8) || grid_too_large(4 * gemm_tiles(M, N)))
     return fail(MX_ERR_UNSUPPORTED_SHAPE, "%lld x %lld output tiles exceed one launch grid",
                 (long long)M, (long long)N);
   if (M == 0 || N == 0) return MX_OK;
   st = check_gemm4_pointers(a_elem, M, 1, N, K, a, sa, b, sb, c);
   if (st != MX_OK) return st;
+  const size_t need = mx_gemm4_workspace_size(a_elem, M, N, K);
+  if (workspace_bytes < need || (need > 0 && !workspace))
+    return fail(MX_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  if (misaligned(workspace)) return fail(MX_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
   int dev;
   st = current_device(&dev);
   if (st != MX_OK) return st;
   const hipError_t e = K == 0 ? mx::launch_fill_zero(c, 2 * M * N, stream)
-                              : mx::launch_gemm4((int)a_elem, M, N, K, a, sa, b, sb, c,
+                              : mx::launch_gemm4((int)a_elem, M, N, K, a, sa, b, sb, c, workspace,
                                                  compute_units(dev), stream);
   if (e != hipSuccess) return hip_fail(e, "4-bit weight GEMM kernel launch");
   return MX_OK;

@@ -4,22 +4,20 @@
 // result; dense, and grouped by device-side expert offsets.  The pages name
 // 4-bit weights with 8-bit activations for serving and 4-bit training of the
 // routed experts (practice page, w4a8-mx; torchtitan-npu MXFP8/HiF8 tutorial,
-// step-2 environment table, ENABLE_MXFP4_QAT).  This file has the kernels for
-// many rows; gemm4_few.hip those for few.
+// step-2 environment table, ENABLE_MXFP4_QAT).  This file has the large tiles
+// for many rows; gemm4_deep.hip the small ones, for everything else.
 //
-// Lane layouts of the scaled MFMAs, found by one-hot operands on the device.
-// 16x16x128: lane l = 16 g + i holds row i; in 4 bits its 16 bytes are K 32 g
-// .. 32 g + 31; in 8 bits its first 16 bytes are K 16 g .. 16 g + 15 and its
-// last 16 are K 64 + 16 g .. ; its scale byte is that of the hardware block g
-// (K 32 g ..) in both.  32x32x64: the same with two lane halves, the 8-bit
-// halves at K 16 g and 32 + 16 g.  The order of K is free, so long as A and B
-// agree: which block of the data stands in which hardware block is chosen for
-// the loads.
+// Lane layout of v_mfma_scale_f32_32x32x64, found by one-hot operands on the
+// device: lane l = 32 g + i holds row i; in 4 bits its 16 bytes are K 32 g ..
+// 32 g + 31; in 8 bits its first 16 bytes are K 16 g .. 16 g + 15 and its last
+// 16 are K 32 + 16 g ..; its scale byte is that of K 32 g .. 32 g + 31 in both.
+// The order of K is free, so long as A and B agree: which block of the data
+// stands in which hardware block is chosen for the loads.
 #include "gemm4.h"
 
 namespace mx {
 
-// One workgroup tile of 64 F x 64 F results: four waves of 32 F x 32 F, F x F
+// One workgroup tile of 256 x 256 results: four waves of 128 x 128, 4 x 4
 // accumulators of 32x32 each.  A K step is 128 bytes of an A row: 128 elements
 // in 8 bits, 256 in 4.  Both operands are staged through a double-buffered
 // LDS tile; 16-byte chunks are swizzled by row so that the 16 lanes served
@@ -32,8 +30,9 @@ namespace mx {
 // multiplies blocks S and 2 + S, of which A's lanes hold 16 bytes each (chunks
 // 2 S + g and 4 + 2 S + g) and B's lane half g the block 2 g + S (chunk 2 g +
 // S).
-template <int FA, int F>
+template <int FA>
 struct Tile4 {
+  static constexpr int F = 4;
   static constexpr bool A4 = FA == ELEM_E2M1;
   static constexpr int ROWS = 64 * F;
   static constexpr int KS = A4 ? 256 : 128;    // elements of a K step
@@ -60,7 +59,7 @@ struct Tile4 {
   __device__ __forceinline__ void setup(int wave, int lane) {
     const int64_t mrows = m_end - m0, nrows = (N - n0) < ROWS ? (N - n0) : ROWS;
     const int64_t pa = A4 ? K >> 1 : K, pb = K >> 1;
-    nks = (K + KS - 1) / KS;
+    nks = K / KS;
     nkb = K >> 5;
     ra = make_rsrc(a + m0 * pa, mrows * pa);
     rb = make_rsrc(b + n0 * pb, nrows * pb);
@@ -85,34 +84,20 @@ struct Tile4 {
     pf_row_b = (uint32_t)((64 * wave + lane) * pb);
   }
 
-  // Loads of step kt into stage st; TAIL: the step may end past K, whose
-  // chunks read as zero.  A step past the last touches no memory.
-  template <bool TAIL>
-  __device__ __forceinline__ void load_a(lds_u8* st, int64_t kt, int u, int wave, int lane) {
+  // Loads of step kt into stage st; a step past the last touches no memory.
+  __device__ __forceinline__ void load_a(lds_u8* st, int64_t kt, int u, int wave) {
     const uint32_t base = kt < nks ? (uint32_t)(128 * kt) : OOB;
-    uint32_t off = voff_a + base + u * a_step;
-    if (TAIL) {
-      const int lc = (lane & 7) ^ ((4 * wave + (lane >> 4)) & 7);
-      off = 128 * kt + 16 * lc < (A4 ? K >> 1 : K) ? off : OOB;
-    }
-    dma16(st + (wave + 4 * u) * 1024, off, ra);
+    dma16(st + (wave + 4 * u) * 1024, voff_a + base + u * a_step, ra);
   }
-  template <bool TAIL>
-  __device__ __forceinline__ void load_b(lds_u8* st, int64_t kt, int u, int wave, int lane) {
+  __device__ __forceinline__ void load_b(lds_u8* st, int64_t kt, int u, int wave) {
     const uint32_t base = kt < nks ? (uint32_t)(BROW * kt) : OOB;
-    uint32_t off = voff_b + base + u * b_step;
-    if (TAIL) {
-      const int lc = A4 ? (lane & 7) ^ ((4 * wave + (lane >> 4)) & 7) : (lane & 3) ^ (lane >> 4);
-      off = BROW * kt + 16 * lc < (K >> 1) ? off : OOB;
-    }
-    dma16(st + A_BYTES + (wave + 4 * u) * 1024, off, rb);
+    dma16(st + A_BYTES + (wave + 4 * u) * 1024, voff_b + base + u * b_step, rb);
   }
-  template <bool TAIL>
-  __device__ __forceinline__ void issue_stage(lds_u8* st, int64_t kt, int wave, int lane) {
+  __device__ __forceinline__ void issue_stage(lds_u8* st, int64_t kt, int wave) {
 #pragma unroll
-    for (int u = 0; u < A_OPS; u++) load_a<TAIL>(st, kt, u, wave, lane);
+    for (int u = 0; u < A_OPS; u++) load_a(st, kt, u, wave);
 #pragma unroll
-    for (int u = 0; u < B_OPS; u++) load_b<TAIL>(st, kt, u, wave, lane);
+    for (int u = 0; u < B_OPS; u++) load_b(st, kt, u, wave);
   }
 
   // Scale bytes of GS steps, 16 bytes a row (K a multiple of 512)
@@ -205,7 +190,6 @@ struct Tile4 {
       for (int y = 0; y < F; y++) acc[x][y] = (v16f){};
   }
 
-  // ---- K a multiple of 512: scales through LDS, loads two steps ahead ----
   // Phase A of step kt: MFMAs of half 0 on registers F0, reads of half 1 into
   // F1; barrier: every wave has read stage kt, stage kt + 1 has landed; phase
   // B: loads of stage kt + 2 into the buffer just released, MFMAs of half 1,
@@ -233,13 +217,13 @@ struct Tile4 {
     for (int f = 0; f < F; f++) {
       f0a[f] = frag_a<0>(nxt, wm, f, lane);
 #pragma unroll
-      for (int u = f * A_OPS / F; u < (f + 1) * A_OPS / F; u++) load_a<false>(cur, kt + 2, u, wave, lane);
+      for (int u = f * A_OPS / F; u < (f + 1) * A_OPS / F; u++) load_a(cur, kt + 2, u, wave);
     }
 #pragma unroll
     for (int f = 0; f < F; f++) {
       f0b[f] = frag_b<0>(nxt, wn, f, lane);
 #pragma unroll
-      for (int u = f * B_OPS / F; u < (f + 1) * B_OPS / F; u++) load_b<false>(cur, kt + 2, u, wave, lane);
+      for (int u = f * B_OPS / F; u < (f + 1) * B_OPS / F; u++) load_b(cur, kt + 2, u, wave);
     }
     prefetch(kt + PF_DIST, wave);
     mma<1>(f1a, f1b, sc_a, sc_b, acc);
@@ -265,11 +249,11 @@ struct Tile4 {
   // stores the last one's result: first() loads stage 0 and its scales,
   // second() stage 1; run() waits for stage 0 (with `stored`, NST stores
   // were issued between the two) and runs the K loop.
-  __device__ __forceinline__ void first(int wave, int lane) {
-    issue_stage<false>(st0, 0, wave, lane);
+  __device__ __forceinline__ void first(int wave) {
+    issue_stage(st0, 0, wave);
     issue_scales(ss0, 0, wave);
   }
-  __device__ __forceinline__ void second(int wave, int lane) { issue_stage<false>(st1, 1, wave, lane); }
+  __device__ __forceinline__ void second(int wave) { issue_stage(st1, 1, wave); }
   template <int NST>
   __device__ __forceinline__ void run(v16f (&acc)[F][F], int wave, int lane, bool stored) {
     const int wm = wave & 1, wn = wave >> 1;
@@ -298,138 +282,7 @@ struct Tile4 {
       }
     }
   }
-
-  // ---- any K: scales from memory, loads one step ahead ----
-  // A row's scale bytes of step kt; blocks past K get 1.0 (their payload is 0)
-  __device__ __forceinline__ uint32_t load_scale(const uint8_t* __restrict__ row, int64_t kt, int g) const {
-    const int64_t kb = SB * kt;
-    uint32_t lo, hi = 0;
-    if (kb + SB <= nkb) {
-      lo = *(const u32_at1*)(row + kb);
-      if (A4) hi = *(const u32_at1*)(row + kb + 4);
-    } else {
-      lo = hi = 0x7F7F7F7Fu;
-      for (int e = 0; e < SB; e++)
-        if (kb + e < nkb) {
-          uint32_t& w = e < 4 ? lo : hi;
-          w = (w & ~(0xFFu << (8 * (e & 3)))) | ((uint32_t)row[kb + e] << (8 * (e & 3)));
-        }
-    }
-    return shape_scale(lo, hi, g);
-  }
-  __device__ __forceinline__ void run_any(v16f (&acc)[F][F], int wave, int lane) {
-    const int wm = wave & 1, wn = wave >> 1, g = lane >> 5, i = lane & 31;
-    clear(acc);
-    const uint8_t *rowa[F], *rowb[F];  // rows past the end repeat the last one; not stored
-#pragma unroll
-    for (int f = 0; f < F; f++) {
-      int64_t m = m0 + 32 * F * wm + 32 * f + i, n = n0 + 32 * F * wn + 32 * f + i;
-      rowa[f] = sa + (m < m_end ? m : m_end - 1) * nkb;
-      rowb[f] = sb + (n < N ? n : N - 1) * nkb;
-    }
-    uint32_t sc_a[F], sc_b[F], nx_a[F], nx_b[F];
-    issue_stage<true>(st0, 0, wave, lane);
-#pragma unroll
-    for (int f = 0; f < F; f++) {
-      nx_a[f] = load_scale(rowa[f], 0, g);
-      nx_b[f] = load_scale(rowb[f], 0, g);
-    }
-    for (int64_t kt = 0; kt < nks; kt++) {
-      lds_u8 *cur = (kt & 1) ? st1 : st0, *nxt = (kt & 1) ? st0 : st1;
-      // this wave's loads of stage kt have landed, then every wave's; and
-      // every wave is done reading the other stage
-      wait_vm_all();
-      __syncthreads();
-#pragma unroll
-      for (int f = 0; f < F; f++) {
-        sc_a[f] = nx_a[f];
-        sc_b[f] = nx_b[f];
-      }
-      if (kt + 1 < nks) {
-        issue_stage<true>(nxt, kt + 1, wave, lane);
-#pragma unroll
-        for (int f = 0; f < F; f++) {
-          nx_a[f] = load_scale(rowa[f], kt + 1, g);
-          nx_b[f] = load_scale(rowb[f], kt + 1, g);
-        }
-      }
-      v8i af[F], bf[F], ag[F], bg[F];
-      read_frags<0>(cur, wm, wn, lane, af, bf);
-      read_frags<1>(cur, wm, wn, lane, ag, bg);
-      mma<0>(af, bf, sc_a, sc_b, acc);
-      mma<1>(ag, bg, sc_a, sc_b, acc);
-    }
-  }
-
-  // The result from registers, any N: lanes l and l + 32 trade groups so that
-  // a lane holds eight consecutive columns, as in gemm_common.h.
-  __device__ __forceinline__ void store(const v16f (&acc)[F][F], uint16_t* __restrict__ c, int wave,
-                                        int lane) const {
-    const int wm = wave & 1, wn = wave >> 1, g = lane >> 5, i = lane & 31;
-    const bool vec = (N & 7) == 0;
-#pragma unroll
-    for (int fn = 0; fn < F; fn++)
-#pragma unroll
-      for (int fm = 0; fm < F; fm++) {
-        const v16f& v = acc[fn][fm];
-        uint32_t p[4][2];
-#pragma unroll
-        for (int r4 = 0; r4 < 4; r4++) {
-          p[r4][0] = cvt_pk_bf16(v[4 * r4 + 0], v[4 * r4 + 1]);
-          p[r4][1] = cvt_pk_bf16(v[4 * r4 + 2], v[4 * r4 + 3]);
-        }
-#pragma unroll
-        for (int h = 0; h < 2; h++)
-#pragma unroll
-          for (int d = 0; d < 2; d++) {
-            const auto s = __builtin_amdgcn_permlane32_swap(p[2 * h][d], p[2 * h + 1][d], false, false);
-            p[2 * h][d] = s[0];
-            p[2 * h + 1][d] = s[1];
-          }
-        const int64_t m = m0 + 32 * F * wm + 32 * fm + i;
-        if (m >= m_end) continue;
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-          const int64_t n = n0 + 32 * F * wn + 32 * fn + 16 * h + 8 * g;
-          const uint32_t w[4] = {p[2 * h][0], p[2 * h][1], p[2 * h + 1][0], p[2 * h + 1][1]};
-          uint16_t* dst = c + m * N + n;
-          if (vec && n + 8 <= N) {
-            *(uint4*)dst = make_uint4(w[0], w[1], w[2], w[3]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-              if (n + e < N) dst[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-          }
-        }
-      }
-  }
 };
-
-// Any K and N, one tile per workgroup.
-template <int FA, int F>
-__global__ void __launch_bounds__(NT)
-gemm4_any_kernel(const uint8_t* __restrict__ a, const uint8_t* __restrict__ sa,
-                 const uint8_t* __restrict__ b, const uint8_t* __restrict__ sb, uint16_t* __restrict__ c,
-                 int64_t M, int64_t N, int64_t K) {
-  typedef Tile4<FA, F> T;
-  __shared__ __attribute__((aligned(16))) uint8_t s0[T::A_BYTES + T::B_BYTES];
-  __shared__ __attribute__((aligned(16))) uint8_t s1[T::A_BYTES + T::B_BYTES];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int64_t mt, nt;
-  tile_of(blockIdx.x, (M + T::ROWS - 1) / T::ROWS, (N + T::ROWS - 1) / T::ROWS, mt, nt);
-  T t;
-  t.a = a, t.sa = sa, t.b = b, t.sb = sb;
-  t.m0 = mt * T::ROWS;
-  t.m_end = t.m0 + T::ROWS < M ? t.m0 + T::ROWS : M;
-  t.n0 = nt * T::ROWS;
-  t.N = N, t.K = K;
-  t.st0 = (lds_u8*)s0, t.st1 = (lds_u8*)s1;
-  t.setup(wave, lane);
-  v16f acc[F][F];
-  t.run_any(acc, wave, lane);
-  t.store(acc, c, wave, lane);
-}
 
 // Persistent, K a multiple of 512 and N of 8: one workgroup per compute unit
 // walks tiles bid, bid + grid, ...; a tile's first loads run while the last
@@ -446,7 +299,7 @@ gemm4_persistent_kernel(const uint8_t* __restrict__ a, const uint8_t* __restrict
   const int64_t nm = (M + BM - 1) / BM, nn = (N + BN - 1) / BN, tiles = nm * nn;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  typedef Tile4<FA, 4> T;
+  typedef Tile4<FA> T;
   auto make = [&](int64_t t, T& tl) {
     int64_t mt, nt;
     tile_of(t, nm, nn, mt, nt);
@@ -466,10 +319,10 @@ gemm4_persistent_kernel(const uint8_t* __restrict__ a, const uint8_t* __restrict
   T tl;
   make(t, tl);
   tl.setup(wave, lane);
-  tl.first(wave, lane);
+  tl.first(wave);
   bool stored = false;
   for (;;) {
-    tl.second(wave, lane);
+    tl.second(wave);
     v16f acc[4][4];
     tl.template run<32>(acc, wave, lane, stored);
     const int64_t m0 = tl.m0, m_end = tl.m_end, n0 = tl.n0;
@@ -482,7 +335,7 @@ gemm4_persistent_kernel(const uint8_t* __restrict__ a, const uint8_t* __restrict
     if (more) {
       make(t, tl);
       tl.setup(wave, lane);
-      tl.first(wave, lane);
+      tl.first(wave);
     }
     store_tile_bf16_lds_halves(acc, (lds_u8*)smem1, c, N, m0, m_end, n0, N, wave & 1, wave >> 1, wave,
                                lane);
@@ -494,8 +347,8 @@ gemm4_persistent_kernel(const uint8_t* __restrict__ a, const uint8_t* __restrict
 // Grouped: every workgroup derives the tile list from the device-side offsets
 // (clamped into [0, T] and made non-decreasing, so bad offsets never address
 // outside the operands) and walks it with a static stride, the tiles of a
-// group in the dense kernel's order.  FAST: K a multiple of 512, N of 8.
-template <int FA, bool FAST>
+// group in the dense kernel's order.  K a multiple of 512, N of 8.
+template <int FA>
 __global__ void __launch_bounds__(NT)
 grouped_gemm4_kernel(int64_t G, const int64_t* __restrict__ offsets, int64_t T_, int64_t N, int64_t K,
                      const uint8_t* __restrict__ a, const uint8_t* __restrict__ sa,
@@ -540,7 +393,7 @@ grouped_gemm4_kernel(int64_t G, const int64_t* __restrict__ offsets, int64_t T_,
       if (s_pre[mid] <= wg) g = mid; else hi = mid;
     }
   }
-  typedef Tile4<FA, 4> T;
+  typedef Tile4<FA> T;
   auto make = [&](int64_t t, T& tl) {
     while (s_pre[g + 1] <= t) g++;  // s_pre[G] = total > t stops it
     const uint32_t local = (uint32_t)(t - s_pre[g]);
@@ -569,46 +422,43 @@ grouped_gemm4_kernel(int64_t G, const int64_t* __restrict__ offsets, int64_t T_,
   int64_t t = wg;
   if (t >= total) return;
   T tl;
-  if constexpr (FAST) {
-    make(t, tl);
-    tl.setup(wave, lane);
-    tl.first(wave, lane);
-    bool stored = false;
-    for (;;) {
-      tl.second(wave, lane);
-      v16f acc[4][4];
-      tl.template run<32>(acc, wave, lane, stored);
-      const int64_t m0 = tl.m0, m_end = tl.m_end, n0 = tl.n0;
-      wait_vm_all();
-      __syncthreads();
-      t += nwg;
-      const bool more = __builtin_amdgcn_readfirstlane((int)(t < total)) != 0;
-      if (more) {
-        make(t, tl);
-        tl.setup(wave, lane);
-        tl.first(wave, lane);
-      }
-      store_tile_bf16_lds_halves(acc, (lds_u8*)smem1, c, N, m0, m_end, n0, N, wave & 1, wave >> 1, wave,
-                                 lane);
-      stored = true;
-      if (!more) break;
-    }
-  } else {
-    for (; t < total; t += nwg) {
+  make(t, tl);
+  tl.setup(wave, lane);
+  tl.first(wave);
+  bool stored = false;
+  for (;;) {
+    tl.second(wave);
+    v16f acc[4][4];
+    tl.template run<32>(acc, wave, lane, stored);
+    const int64_t m0 = tl.m0, m_end = tl.m_end, n0 = tl.n0;
+    wait_vm_all();
+    __syncthreads();
+    t += nwg;
+    const bool more = __builtin_amdgcn_readfirstlane((int)(t < total)) != 0;
+    if (more) {
       make(t, tl);
       tl.setup(wave, lane);
-      v16f acc[4][4];
-      tl.run_any(acc, wave, lane);
-      tl.store(acc, c, wave, lane);
-      __syncthreads();  // the stages are free again
+      tl.first(wave);
     }
+    store_tile_bf16_lds_halves(acc, (lds_u8*)smem1, c, N, m0, m_end, n0, N, wave & 1, wave >> 1, wave,
+                               lane);
+    stored = true;
+    if (!more) break;
   }
 }
 
-// K and N that the pipelined kernels take: whole groups of 16 scale bytes,
-// whole 16-byte chunks of a result row, 32-bit offsets within a tile's rows.
+// Which kernel: K and N that the pipelined tiles take are whole groups of 16
+// scale bytes, whole 16-byte chunks of a result row and 32-bit offsets within
+// a tile's rows.
 static bool pipelined(int64_t N, int64_t K) {
   return K % 512 == 0 && N % 8 == 0 && (int64_t)BM * N * 2 < ((int64_t)1 << 31);
+}
+
+// Large tiles from 160 of them on (K = 18432, N = 7168, 8-bit A: 2048 rows, 224
+// tiles, 237 us against 318 in small ones; 1024 rows, 112 tiles, 203 against
+// 163).
+static bool many(int64_t M, int64_t N, int64_t K) {
+  return pipelined(N, K) && ((M + BM - 1) / BM) * ((N + BN - 1) / BN) >= 160;
 }
 
 template <int FA>
@@ -617,17 +467,18 @@ static void launch_many(int64_t M, int64_t N, int64_t K, const uint8_t* a, const
                         hipStream_t stream) {
   const int64_t tiles = ((M + BM - 1) / BM) * ((N + BN - 1) / BN);
   const int64_t cus = (num_cus > 8 ? num_cus : 256) / 8 * 8;
-  if (pipelined(N, K))
-    hipLaunchKernelGGL((gemm4_persistent_kernel<FA>), dim3((unsigned)(tiles < cus ? tiles : cus)), dim3(NT), 0,
-                       stream, a, sa, b, sb, c, M, N, K);
-  else
-    hipLaunchKernelGGL((gemm4_any_kernel<FA, 4>), dim3((unsigned)tiles), dim3(NT), 0, stream, a, sa, b, sb, c,
-                       M, N, K);
+  hipLaunchKernelGGL((gemm4_persistent_kernel<FA>), dim3((unsigned)(tiles < cus ? tiles : cus)), dim3(NT), 0,
+                     stream, a, sa, b, sb, c, M, N, K);
+}
+
+size_t gemm4_workspace(int64_t M, int64_t N, int64_t K) {
+  return many(M, N, K) ? 0 : gemm4_deep_workspace(M, N, K);
 }
 
 hipError_t launch_gemm4(int a_elem, int64_t M, int64_t N, int64_t K, const void* a, const void* sa,
-                        const void* b, const void* sb, void* c, int num_cus, hipStream_t stream) {
-  if (M <= 64) return launch_gemm4_few(a_elem, M, N, K, a, sa, b, sb, c, stream);
+                        const void* b, const void* sb, void* c, void* workspace, int num_cus,
+                        hipStream_t stream) {
+  if (!many(M, N, K)) return launch_gemm4_deep(a_elem, M, N, K, a, sa, b, sb, c, workspace, stream);
   const uint8_t *A = (const uint8_t*)a, *SA = (const uint8_t*)sa, *B = (const uint8_t*)b,
                 *SB = (const uint8_t*)sb;
   uint16_t* C = (uint16_t*)c;
@@ -642,22 +493,17 @@ hipError_t launch_grouped_gemm4(int a_elem, int64_t G, const int64_t* offsets, i
                                 int64_t K, const void* a, const void* sa, const void* b,
                                 const void* sb, void* c, int num_cus, hipStream_t stream) {
   if (G < 1 || G > MAX_GROUPS) return hipErrorInvalidValue;
-  if (T <= 64 * G) return launch_grouped_gemm4_few(a_elem, G, offsets, T, N, K, a, sa, b, sb, c, stream);
+  // large tiles from 96 rows a group on (64 groups of 4096 x 4096: 128 rows each
+  // 265 us against 304 in small ones, 78 rows each 255 against 218)
+  if (!pipelined(N, K) || T < 96 * G)
+    return launch_grouped_gemm4_deep(a_elem, G, offsets, T, N, K, a, sa, b, sb, c, stream);
   const int64_t upper = ((T + BM - 1) / BM + G) * ((N + BN - 1) / BN);
   int64_t wgs = ((num_cus > 0 ? num_cus : 256) + 7) / 8 * 8;
   if (upper < wgs) wgs = (upper + 7) / 8 * 8;
-  const bool fast = pipelined(N, K);
 #define MX_GROUPED4(FA_)                                                                          \
-  do {                                                                                            \
-    if (fast)                                                                                     \
-      hipLaunchKernelGGL((grouped_gemm4_kernel<FA_, true>), dim3((unsigned)wgs), dim3(NT), 0, stream, G, \
-                         offsets, T, N, K, (const uint8_t*)a, (const uint8_t*)sa, (const uint8_t*)b, \
-                         (const uint8_t*)sb, (uint16_t*)c);                                       \
-    else                                                                                          \
-      hipLaunchKernelGGL((grouped_gemm4_kernel<FA_, false>), dim3((unsigned)wgs), dim3(NT), 0, stream, G, \
-                         offsets, T, N, K, (const uint8_t*)a, (const uint8_t*)sa, (const uint8_t*)b, \
-                         (const uint8_t*)sb, (uint16_t*)c);                                       \
-  } while (0)
+  hipLaunchKernelGGL((grouped_gemm4_kernel<FA_>), dim3((unsigned)wgs), dim3(NT), 0, stream, G, offsets, \
+                     T, N, K, (const uint8_t*)a, (const uint8_t*)sa, (const uint8_t*)b,           \
+                     (const uint8_t*)sb, (uint16_t*)c)
   if (a_elem == ELEM_E4M3) MX_GROUPED4(ELEM_E4M3);
   else if (a_elem == ELEM_E5M2) MX_GROUPED4(ELEM_E5M2);
   else if (a_elem == ELEM_E2M1) MX_GROUPED4(ELEM_E2M1);

@@ -1,0 +1,571 @@
+// Products with 4-bit MX weights for gfx950 where the weight's bytes count:
+// tens to hundreds of rows, or sizes that the large tiles do not take.  C = A *
+// B^T as in gemm4.hip, which has the lane layouts; any N and any K that is a
+// multiple of 32.
+//
+// Small tiles and many stages: the loads of NS - 1 K steps are in flight, so
+// that a compute unit keeps some 60 KB of the weight on its way.  Where the
+// result has fewer tiles than the chip has places, K is split over workgroups
+// whose FP32 sums a second kernel adds in the order of the splits.
+#include "gemm4.h"
+#include "mx_rows.h"
+
+namespace mx {
+
+// A tile of 32 WM FM rows x 32 WN FN columns, WM WN waves, FM x FN accumulators
+// of 32x32 each.  A K step is 128 KH elements (256 with 4-bit A).  A stage holds
+// the A tile in panels of 128 bytes a row, the B tile in rows of 64 KH bytes
+// (128 with 4-bit A) and the step's scale words, a dword of four scale bytes a
+// row and 128 elements: A's rows, padded to whole waves, then B's.  Chunk
+// swizzles and the meeting of blocks are those of gemm4.hip, panel by panel.
+// TWO: stages for two workgroups on a compute unit.
+template <int FA, int WM, int WN, int FM, int FN, int KH_, bool TWO>
+struct Deep4 {
+  static constexpr bool A4 = FA == ELEM_E2M1;
+  static constexpr int WAVES = WM * WN;
+  static constexpr int BMR = 32 * WM * FM, BNR = 32 * WN * FN;
+  static constexpr int KH = A4 ? 2 : KH_;               // scale dwords of a row and step
+  static constexpr int KS = 128 * KH;
+  static constexpr int PANELS = A4 ? 1 : KH;            // of A
+  static constexpr int BROW = 64 * KH;
+  static constexpr int A_PANEL = BMR * 128;
+  static constexpr int A_BYTES = PANELS * A_PANEL, B_BYTES = BNR * BROW;
+  static constexpr int A_OPS = A_BYTES / 1024 / WAVES;  // 1 KB loads of a wave and step
+  static constexpr int B_OPS = B_BYTES / 1024 / WAVES;
+  static constexpr int OPS = A_OPS + B_OPS + KH;
+  static constexpr int A_ROWS = (BMR + 63) / 64 * 64;   // A's places among the scale rows
+  static_assert(A_ROWS + BNR <= 64 * WAVES, "a wave loads the scales of 64 rows");
+  static_assert(A_OPS * 1024 * WAVES == A_BYTES && B_OPS * 1024 * WAVES == B_BYTES, "whole loads");
+  static constexpr int S_BYTES = 256 * WAVES;           // one array of scale words
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + KH * S_BYTES;
+  static constexpr int FIT = (TWO ? 81920 : 163840) / STAGE_BYTES;
+  static constexpr int NS = FIT > 8 ? 8 : FIT;
+  static_assert(NS >= 2 && (NS - 1) * OPS < 64, "vmcnt holds 6 bits");
+
+  const uint8_t* __restrict__ a;
+  const uint8_t* __restrict__ sa;
+  const uint8_t* __restrict__ b;
+  const uint8_t* __restrict__ sb;
+  int64_t m0, m_end, n0, N, K;
+  int kt0, kt1;         // K steps of this workgroup
+  int full;             // steps that lie in K wholly; at most one more follows
+  lds_u8* st;
+  u32x4 ra, rb, rs;
+  uint32_t off_a[A_OPS], off_b[B_OPS], off_s;  // this lane's offsets at step 0
+  uint32_t pos_a[A_OPS], pos_b;                // and its chunks' bytes within a step's row
+  uint32_t row_a, row_b, nkb;                  // bytes of a row
+
+  __device__ __forceinline__ void setup(int wave, int lane) {
+    const int64_t mrows = m_end - m0, nrows = (N - n0) < BNR ? (N - n0) : BNR;
+    row_a = (uint32_t)(A4 ? K >> 1 : K);
+    row_b = (uint32_t)(K >> 1);
+    nkb = (uint32_t)(K >> 5);
+    full = (int)(K / KS);
+    ra = make_rsrc(a + m0 * row_a, mrows * row_a);
+    rb = make_rsrc(b + n0 * row_b, nrows * row_b);
+    // A: load t covers rows 8 (t % (BMR / 8)) .. + 7 of panel t / (BMR / 8);
+    // lane i lands in row i / 8 of them at chunk i % 8, logical (i % 8) ^ swz(row)
+#pragma unroll
+    for (int u = 0; u < A_OPS; u++) {
+      const int t = wave + WAVES * u, row = 8 * (t % (BMR / 8)) + (lane >> 3);
+      pos_a[u] = 128 * (t / (BMR / 8)) + 16 * ((lane & 7) ^ swz(row));
+      off_a[u] = (uint32_t)row * row_a + pos_a[u];
+    }
+    constexpr int CH = BROW / 16;
+#pragma unroll
+    for (int u = 0; u < B_OPS; u++) {
+      const int row = (wave + WAVES * u) * (64 / CH) + lane / CH;
+      pos_b = 16 * ((lane % CH) ^ (CH == 8 ? swz(row) : (row >> 2) & 3));  // the same for every u
+      off_b[u] = (uint32_t)row * row_b + pos_b;
+    }
+    // scale rows 64 wave .. 64 wave + 63
+    const bool isb = 64 * wave >= A_ROWS;
+    const int row = 64 * wave + lane - (isb ? A_ROWS : 0);
+    const int64_t rows = isb ? nrows : mrows;
+    rs = make_rsrc(isb ? sb + n0 * nkb : sa + m0 * nkb, rows * nkb);
+    off_s = row < rows && 64 * wave < A_ROWS + BNR ? (uint32_t)row * nkb : OOB;
+    if (nkb < 4) off_s = OOB;  // rows shorter than a dword: short_scales() loads them
+  }
+
+  // Loads of step kt into the stage at `to`.  WHOLE: the step lies in K and
+  // in this workgroup's part, its offset is scalar.  Otherwise chunks past K
+  // read as zero, and a step past the last touches no memory.
+  template <bool WHOLE>
+  __device__ __forceinline__ void issue(lds_u8* to, int kt, int wave) {
+    const uint32_t ka = (uint32_t)kt * (128 * PANELS), kb = (uint32_t)kt * BROW, ks = (uint32_t)kt * (KS / 32);
+    lds_u8* const tb = to + A_BYTES;
+    lds_u8* const ts = tb + B_BYTES + 256 * wave;
+    if constexpr (WHOLE) {
+#pragma unroll
+      for (int u = 0; u < A_OPS; u++) dma16_at(to + (wave + WAVES * u) * 1024, off_a[u], ra, ka);
+#pragma unroll
+      for (int u = 0; u < B_OPS; u++) dma16_at(tb + (wave + WAVES * u) * 1024, off_b[u], rb, kb);
+#pragma unroll
+      for (int h = 0; h < KH; h++) dma4_at(ts + S_BYTES * h, off_s, rs, ks + 4 * h);
+    } else {
+      const bool live = kt < kt1;
+#pragma unroll
+      for (int u = 0; u < A_OPS; u++)
+        dma16(to + (wave + WAVES * u) * 1024, live && ka + pos_a[u] < row_a ? off_a[u] + ka : OOB, ra);
+#pragma unroll
+      for (int u = 0; u < B_OPS; u++)
+        dma16(tb + (wave + WAVES * u) * 1024, live && kb + pos_b < row_b ? off_b[u] + kb : OOB, rb);
+      // a dword that would pass the row's last scale byte ends there instead
+      // and is shifted when it is read
+#pragma unroll
+      for (int h = 0; h < KH; h++) {
+        const uint32_t at = ks + 4 * h;
+        dma4(ts + S_BYTES * h, live && at < nkb ? off_s + (at + 4 <= nkb ? at : nkb - 4) : OOB, rs);
+      }
+    }
+  }
+
+  // A row's scale words of a step: with 8-bit A word h holds byte S for half S
+  // of panel h, with 4-bit A word 0 byte S + 2 h for MFMA h of half S.
+  __device__ __forceinline__ static void scale(const lds_u8* stage, int row, uint32_t* w) {
+    typedef const __attribute__((address_space(3))) uint32_t lds_u32;
+#pragma unroll
+    for (int h = 0; h < KH; h++) w[h] = *(lds_u32*)(stage + A_BYTES + B_BYTES + S_BYTES * h + 4 * row);
+  }
+  template <bool WHOLE>
+  __device__ __forceinline__ void shape(uint32_t* w, int kt, int g) const {
+    if constexpr (!WHOLE) {  // past K the payload is 0, and so may be its scales
+#pragma unroll
+      for (int h = 0; h < KH; h++) {
+        const uint32_t at = (uint32_t)kt * (KS / 32) + 4 * h;
+        if (at + 4 > nkb) w[h] = at < nkb ? w[h] >> (8 * (at + 4 - nkb)) : 0u;
+      }
+    }
+    if (A4) {
+      w[0] = __builtin_amdgcn_perm(w[KH - 1], w[0], g ? 0x07050301u : 0x06040200u);
+    } else {
+#pragma unroll
+      for (int h = 0; h < KH; h++) w[h] >>= 16 * g;
+    }
+  }
+
+  // A step's MFMAs come in UNITS of half a panel (half a step with 4-bit A),
+  // whose fragments are read while the unit before is multiplied: unit 0 of a
+  // stage while the last unit of the stage before is.
+  static constexpr int UNITS = 2 * PANELS;
+  struct Frags {
+    v8i a[FM], b[FN];
+  };
+  template <int U>
+  __device__ __forceinline__ static void read_unit(const lds_u8* cur, Frags& f, int wm, int wn, int lane) {
+    constexpr int h = U / 2, S = U % 2;
+    const int g = lane >> 5, i = lane & 31;
+#pragma unroll
+    for (int x = 0; x < FM; x++) f.a[x] = read_frag(cur + h * A_PANEL, 32 * FM * wm + 32 * x + i, S, g);
+#pragma unroll
+    for (int x = 0; x < FN; x++) {
+      const int row = 32 * FN * wn + 32 * x + i;
+      if (A4) {
+        f.b[x] = read_frag(cur + A_BYTES, row, S, g);
+      } else {
+        const int c = 4 * h + 2 * g + S;
+        const v4i v = *(const lds_v4i*)(cur + A_BYTES + row * BROW +
+                                        ((c ^ (BROW == 128 ? swz(row) : (row >> 2) & 3)) << 4));
+        f.b[x] = (v8i){v.x, v.y, v.z, v.w, 0, 0, 0, 0};
+      }
+    }
+  }
+  template <int U>
+  __device__ __forceinline__ static void mma_unit(const Frags& f, v16f (&acc)[FN][FM],
+                                                  const uint32_t (&sar)[FM][KH],
+                                                  const uint32_t (&sbr)[FN][KH]) {
+    constexpr int h = U / 2, S = U % 2;
+    if constexpr (A4) {
+#pragma unroll
+      for (int x = 0; x < FN; x++)
+#pragma unroll
+        for (int y = 0; y < FM; y++)
+          acc[x][y] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              low(f.b[x]), low(f.a[y]), acc[x][y], ELEM_E2M1, ELEM_E2M1, S, (int)sbr[x][0], S, (int)sar[y][0]);
+#pragma unroll
+      for (int x = 0; x < FN; x++)
+#pragma unroll
+        for (int y = 0; y < FM; y++)
+          acc[x][y] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              high(f.b[x]), high(f.a[y]), acc[x][y], ELEM_E2M1, ELEM_E2M1, S + 2, (int)sbr[x][0], S + 2,
+              (int)sar[y][0]);
+    } else {
+#pragma unroll
+      for (int x = 0; x < FN; x++)
+#pragma unroll
+        for (int y = 0; y < FM; y++)
+          acc[x][y] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              f.b[x], f.a[y], acc[x][y], ELEM_E2M1, FA, S, (int)sbr[x][h], S, (int)sar[y][h]);
+    }
+  }
+
+  __device__ __forceinline__ static void read_scales(const lds_u8* cur, int wm, int wn, int lane,
+                                                     uint32_t (&sar)[FM][KH], uint32_t (&sbr)[FN][KH]) {
+    const int i = lane & 31;
+#pragma unroll
+    for (int f = 0; f < FM; f++) scale(cur, 32 * FM * wm + 32 * f + i, sar[f]);
+#pragma unroll
+    for (int f = 0; f < FN; f++) scale(cur, A_ROWS + 32 * FN * wn + 32 * f + i, sbr[f]);
+  }
+  template <bool WHOLE>
+  __device__ __forceinline__ void shape_scales(int kt, int lane, uint32_t (&sar)[FM][KH],
+                                               uint32_t (&sbr)[FN][KH]) const {
+#pragma unroll
+    for (int f = 0; f < FM; f++) shape<WHOLE>(sar[f], kt, lane >> 5);
+#pragma unroll
+    for (int f = 0; f < FN; f++) shape<WHOLE>(sbr[f], kt, lane >> 5);
+  }
+
+  // One unit's MFMAs with the LDS reads of the next among them
+  template <int NDS>
+  __device__ __forceinline__ static void interleave() {
+    constexpr int n = FM * FN * (A4 ? 2 : 1), per = (NDS + n - 1) / n;
+#pragma unroll
+    for (int i = 0; i < n; i++) {
+      __builtin_amdgcn_sched_group_barrier(0x100, per, 0);  // LDS reads
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);    // MFMA
+    }
+  }
+  static constexpr int UNIT_READS = 2 * FM + (A4 ? 2 : 1) * FN;
+
+  // K below 128, one step: the scale bytes of each row one by one, placed as
+  // shape() expects them of the last dword of a row.
+  __device__ __forceinline__ void short_scales(int wave, int lane) {
+    typedef __attribute__((address_space(3))) uint32_t lds_u32;
+    const bool isb = 64 * wave >= A_ROWS;
+    const int row = 64 * wave + lane - (isb ? A_ROWS : 0);
+    const int64_t rows = isb ? N - n0 : m_end - m0;
+    if (row < rows && row < (isb ? BNR : BMR)) {
+      const uint8_t* p = isb ? sb + (n0 + row) * nkb : sa + (m0 + row) * nkb;
+      uint32_t w = 0;
+      for (uint32_t e = 0; e < nkb; e++) w |= (uint32_t)p[e] << (8 * (4 - nkb + e));
+      *(lds_u32*)(st + A_BYTES + B_BYTES + 256 * wave + 4 * lane) = w;
+    }
+    __syncthreads();
+  }
+
+  // Step kt on stage `cur`, unit 0 of it in f0 and its scales shaped; leaves
+  // the same of step kt + 1.  WHOLE: steps up to kt + NS are whole ones.
+  template <bool WHOLE>
+  __device__ __forceinline__ void step(lds_u8* cur, const lds_u8* nxt, int kt, int wave, int wm, int wn,
+                                       int lane, Frags& f0, uint32_t (&sar)[FM][KH],
+                                       uint32_t (&sbr)[FN][KH], v16f (&acc)[FN][FM]) {
+    Frags f1;
+    uint32_t nar[FM][KH], nbr[FN][KH];
+    read_unit<1>(cur, f1, wm, wn, lane);
+    mma_unit<0>(f0, acc, sar, sbr);
+    interleave<UNIT_READS>();
+    if constexpr (UNITS == 4) {
+      read_unit<2>(cur, f0, wm, wn, lane);
+      mma_unit<1>(f1, acc, sar, sbr);
+      interleave<UNIT_READS>();
+      read_unit<3>(cur, f1, wm, wn, lane);
+      mma_unit<2>(f0, acc, sar, sbr);
+      interleave<UNIT_READS>();
+    }
+    // every wave has read this stage, which takes step kt + NS; the next one
+    // has landed for every wave
+    wait_vm<(NS - 2) * OPS>();
+    __syncthreads();
+    read_scales(nxt, wm, wn, lane, nar, nbr);
+    read_unit<0>(nxt, f0, wm, wn, lane);
+    issue<WHOLE>(cur, kt + NS, wave);
+    mma_unit<UNITS - 1>(f1, acc, sar, sbr);
+    interleave<UNIT_READS + (FM + FN) * KH>();
+    __builtin_amdgcn_sched_barrier(0);  // the scales' shifts would wait on their reads among the MFMAs
+    shape_scales<WHOLE>(kt + 1, lane, nar, nbr);
+#pragma unroll
+    for (int h = 0; h < KH; h++) {
+#pragma unroll
+      for (int f = 0; f < FM; f++) sar[f][h] = nar[f][h];
+#pragma unroll
+      for (int f = 0; f < FN; f++) sbr[f][h] = nbr[f][h];
+    }
+  }
+
+  __device__ __forceinline__ void run(v16f (&acc)[FN][FM], int wave, int lane) {
+    const int wm = wave % WM, wn = wave / WM;
+#pragma unroll
+    for (int x = 0; x < FN; x++)
+#pragma unroll
+      for (int y = 0; y < FM; y++) acc[x][y] = (v16f){};
+#pragma unroll
+    for (int p = 0; p < NS; p++) issue<false>(st + p * STAGE_BYTES, kt0 + p, wave);
+    wait_vm<(NS - 1) * OPS>();
+    __syncthreads();
+    if (nkb < 4) short_scales(wave, lane);
+    Frags f0;
+    uint32_t sar[FM][KH], sbr[FN][KH];
+    read_scales(st, wm, wn, lane, sar, sbr);
+    read_unit<0>(st, f0, wm, wn, lane);
+    shape_scales<false>(kt0, lane, sar, sbr);
+    lds_u8* cur = st;
+    lds_u8* const end = st + NS * STAGE_BYTES;
+    const int whole = (kt1 < full ? kt1 : full) - NS;  // steps before it start whole ones
+    int kt = kt0;
+    for (; kt < whole; kt++) {
+      lds_u8* nxt = cur + STAGE_BYTES == end ? st : cur + STAGE_BYTES;
+      step<true>(cur, nxt, kt, wave, wm, wn, lane, f0, sar, sbr, acc);
+      cur = nxt;
+    }
+    for (; kt < kt1; kt++) {
+      lds_u8* nxt = cur + STAGE_BYTES == end ? st : cur + STAGE_BYTES;
+      step<false>(cur, nxt, kt, wave, wm, wn, lane, f0, sar, sbr, acc);
+      cur = nxt;
+    }
+    wait_vm_all();  // no load may still be writing LDS when the workgroup ends
+  }
+
+  __device__ __forceinline__ static v8i low(v8i v) { return (v8i){v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
+  __device__ __forceinline__ static v8i high(v8i v) { return (v8i){v[4], v[5], v[6], v[7], 0, 0, 0, 0}; }
+
+  // The result in BF16, any N: lanes l and l + 32 trade groups so that a lane
+  // holds eight consecutive columns (gemm_common.h).
+  __device__ __forceinline__ void store(const v16f (&acc)[FN][FM], uint16_t* __restrict__ c, int wave,
+                                        int lane) const {
+    const int wm = wave % WM, wn = wave / WM, g = lane >> 5, i = lane & 31;
+#pragma unroll
+    for (int fn = 0; fn < FN; fn++)
+#pragma unroll
+      for (int fm = 0; fm < FM; fm++) {
+        const v16f& v = acc[fn][fm];
+        uint32_t p[4][2];
+#pragma unroll
+        for (int r4 = 0; r4 < 4; r4++) {
+          p[r4][0] = cvt_pk_bf16(v[4 * r4 + 0], v[4 * r4 + 1]);
+          p[r4][1] = cvt_pk_bf16(v[4 * r4 + 2], v[4 * r4 + 3]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+          for (int d = 0; d < 2; d++) {
+            const auto s = __builtin_amdgcn_permlane32_swap(p[2 * h][d], p[2 * h + 1][d], false, false);
+            p[2 * h][d] = s[0];
+            p[2 * h + 1][d] = s[1];
+          }
+        const int64_t m = m0 + 32 * FM * wm + 32 * fm + i;
+        if (m >= m_end) continue;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          const int64_t n = n0 + 32 * FN * wn + 32 * fn + 16 * h + 8 * g;
+          const uint32_t w[4] = {p[2 * h][0], p[2 * h][1], p[2 * h + 1][0], p[2 * h + 1][1]};
+          uint16_t* dst = c + m * N + n;
+          if (n + 8 <= N) {
+            *(u32x4_at2*)dst = (u32x4_at2){w[0], w[1], w[2], w[3]};
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+              if (n + e < N) dst[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+          }
+        }
+      }
+  }
+
+  // The FP32 sums of one split into its share of the workspace, whole tiles in
+  // rows of ldw columns: a lane writes groups of four consecutive columns.
+  __device__ __forceinline__ void store_partial(const v16f (&acc)[FN][FM], float* __restrict__ ws, int64_t ldw,
+                                                int wave, int lane) const {
+    const int wm = wave % WM, wn = wave / WM, g = lane >> 5, i = lane & 31;
+#pragma unroll
+    for (int fn = 0; fn < FN; fn++)
+#pragma unroll
+      for (int fm = 0; fm < FM; fm++) {
+        const v16f& v = acc[fn][fm];
+        const int64_t m = m0 + 32 * FM * wm + 32 * fm + i;
+        if (m >= m_end) continue;
+#pragma unroll
+        for (int r4 = 0; r4 < 4; r4++) {
+          const int64_t n = n0 + 32 * FN * wn + 32 * fn + 8 * r4 + 4 * g;
+          *(v4f*)(ws + m * ldw + n) = (v4f){v[4 * r4], v[4 * r4 + 1], v[4 * r4 + 2], v[4 * r4 + 3]};
+        }
+      }
+  }
+};
+
+// Dense: blockIdx.y is the split of K, blockIdx.x the tile, the rows of one
+// part of the weight side by side.
+template <int FA, int WM, int WN, int FM, int FN, int KH, bool TWO>
+__global__ void __launch_bounds__(64 * WM * WN)
+gemm4_deep_kernel(const uint8_t* __restrict__ a, const uint8_t* __restrict__ sa,
+                  const uint8_t* __restrict__ b, const uint8_t* __restrict__ sb, uint16_t* __restrict__ c,
+                  int64_t M, int64_t N, int64_t K, float* __restrict__ ws, int64_t ldw) {
+  typedef Deep4<FA, WM, WN, FM, FN, KH, TWO> T;
+  __shared__ __attribute__((aligned(16))) uint8_t stages[T::NS * T::STAGE_BYTES];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t nm = (uint32_t)((M + T::BMR - 1) / T::BMR);
+  // workgroups are dealt to the 8 XCDs in turn: each takes a contiguous part of
+  // the tiles, so that those of one part of the weight share its L2
+  const uint32_t per = gridDim.x >> 3, rem = gridDim.x & 7, x = blockIdx.x & 7;
+  const uint32_t tile = x * per + (x < rem ? x : rem) + (blockIdx.x >> 3);
+  const uint32_t nt = tile / nm, mt = tile - nt * nm;
+  T t;
+  t.a = a, t.sa = sa, t.b = b, t.sb = sb;
+  t.m0 = (int64_t)mt * T::BMR;
+  t.m_end = t.m0 + T::BMR < M ? t.m0 + T::BMR : M;
+  t.n0 = (int64_t)nt * T::BNR;
+  t.N = N, t.K = K;
+  const int64_t nks = (K + T::KS - 1) / T::KS;
+  t.kt0 = (int)(nks * blockIdx.y / gridDim.y);
+  t.kt1 = (int)(nks * (blockIdx.y + 1) / gridDim.y);
+  t.st = (lds_u8*)stages;
+  t.setup(wave, lane);
+  v16f acc[FN][FM];
+  t.run(acc, wave, lane);
+  if (gridDim.y == 1) t.store(acc, c, wave, lane);
+  else t.store_partial(acc, ws + (int64_t)blockIdx.y * M * ldw, ldw, wave, lane);
+}
+
+// The splits' sums, added in their order and rounded to BF16; a thread takes
+// four columns.
+__global__ void __launch_bounds__(256)
+gemm4_join_kernel(const float* __restrict__ ws, int64_t M, int64_t N, int64_t ldw, int splits,
+                  uint16_t* __restrict__ c) {
+  const uint32_t n = 4 * (blockIdx.x * 256 + threadIdx.x);
+  const int64_t m = blockIdx.y;
+  if (n >= N) return;
+  const float* p = ws + m * ldw + n;
+  v4f v = *(const v4f*)p;
+  for (int s = 1; s < splits; s++) v += *(const v4f*)(p + s * M * ldw);
+  const uint32_t w[2] = {cvt_pk_bf16(v.x, v.y), cvt_pk_bf16(v.z, v.w)};
+  uint16_t* dst = c + m * N + n;
+  if (n + 4 <= N) {
+    *(u32x2_at2*)dst = (u32x2_at2){w[0], w[1]};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+      if (n + e < N) dst[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+  }
+}
+
+// Grouped: blockIdx.y is the group, blockIdx.x the column tile; a workgroup
+// takes its group's rows tile by tile.
+template <int FA, int WM, int WN, int FM, int FN, int KH, bool TWO>
+__global__ void __launch_bounds__(64 * WM * WN)
+grouped4_deep_kernel(const int64_t* __restrict__ offsets, int64_t rows, const uint8_t* __restrict__ a,
+                     const uint8_t* __restrict__ sa, const uint8_t* __restrict__ b,
+                     const uint8_t* __restrict__ sb, uint16_t* __restrict__ c, int64_t N, int64_t K) {
+  typedef Deep4<FA, WM, WN, FM, FN, KH, TWO> T;
+  __shared__ __attribute__((aligned(16))) uint8_t stages[T::NS * T::STAGE_BYTES];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t g = blockIdx.y;
+  // clamped, so that bad offsets read and write rows of [0, rows) only
+  int64_t lo = offsets[g], hi = offsets[g + 1];
+  lo = lo < 0 ? 0 : (lo > rows ? rows : lo);
+  hi = hi < lo ? lo : (hi > rows ? rows : hi);
+  T t;
+  t.a = a, t.sa = sa;
+  t.b = b + g * N * (K >> 1), t.sb = sb + g * N * (K >> 5);
+  t.n0 = (int64_t)blockIdx.x * T::BNR;
+  t.N = N, t.K = K;
+  t.kt0 = 0, t.kt1 = (int)((K + T::KS - 1) / T::KS);
+  t.st = (lds_u8*)stages;
+  for (int64_t m0 = lo; m0 < hi; m0 += T::BMR) {
+    t.m0 = m0;
+    t.m_end = m0 + T::BMR < hi ? m0 + T::BMR : hi;
+    t.setup(wave, lane);
+    v16f acc[FN][FM];
+    t.run(acc, wave, lane);
+    t.store(acc, c, wave, lane);
+    __syncthreads();  // every wave is done with the stages
+  }
+}
+
+// Which tile, measured at K = 7168 and 18432 with N = 18432 and 7168 (us, 8-bit
+// A).  Up to 32 rows 32 x 128, two workgroups to a compute unit (1 x 18432 x
+// 7168: 15.5, one to a unit 17.0); up to 64 rows 64 x 128 (64 x 18432: 24.2, two
+// to a unit 26.3); above, 128 x 128 while its tiles find a unit each (512 x 7168
+// x 18432: 75, against 117 with 128 x 256), 128 x 256 beyond (2048 rows: 318
+// against 361).  K is split so far as workgroups still find a unit each, eight
+// steps to a split at least (1 x 7168 x 18432: 15.6 in four, 31 whole).
+enum Shape4 { TILE_32, TILE_64, TILE_128, TILE_WIDE };
+
+struct Plan4 {
+  Shape4 shape;
+  int64_t tiles, ldw;
+  int splits;
+};
+
+static Plan4 plan_of(int64_t M, int64_t N, int64_t K) {
+  const int64_t n128 = (N + 127) / 128, t128 = (M + 127) / 128 * n128;
+  Plan4 p;
+  p.ldw = n128 * 128;
+  if (M <= 32) p.shape = TILE_32, p.tiles = n128;
+  else if (M <= 64) p.shape = TILE_64, p.tiles = n128;
+  else if (t128 <= 256) p.shape = TILE_128, p.tiles = t128;
+  else p.shape = TILE_WIDE, p.tiles = (M + 127) / 128 * ((N + 255) / 256);
+  int64_t s = 256 / p.tiles;
+  if (s > K / 2048) s = K / 2048;
+  // the wide tile's partial sums would need rows of its own width
+  p.splits = s < 1 || p.shape == TILE_WIDE ? 1 : s > 16 ? 16 : (int)s;
+  return p;
+}
+
+size_t gemm4_deep_workspace(int64_t M, int64_t N, int64_t K) {
+  const Plan4 p = plan_of(M, N, K);
+  return p.splits == 1 ? 0 : (size_t)(p.splits * M * p.ldw * 4);
+}
+
+template <int FA>
+static void launch_deep(int64_t M, int64_t N, int64_t K, const uint8_t* a, const uint8_t* sa,
+                        const uint8_t* b, const uint8_t* sb, uint16_t* c, float* ws, hipStream_t stream) {
+  const Plan4 p = plan_of(M, N, K);
+  const dim3 grid((unsigned)p.tiles, (unsigned)p.splits);
+#define MX_DEEP(WM_, WN_, FM_, FN_, KH_, TWO_)                                                    \
+  hipLaunchKernelGGL((gemm4_deep_kernel<FA, WM_, WN_, FM_, FN_, KH_, TWO_>), grid, dim3(64 * WM_ * WN_), 0, \
+                     stream, a, sa, b, sb, c, M, N, K, ws, p.ldw)
+  switch (p.shape) {
+    case TILE_32: MX_DEEP(1, 4, 1, 1, 2, true); break;
+    case TILE_64: MX_DEEP(2, 2, 1, 2, 2, false); break;
+    case TILE_128: MX_DEEP(2, 2, 2, 2, 2, false); break;
+    case TILE_WIDE: MX_DEEP(2, 4, 2, 2, 1, false); break;
+  }
+#undef MX_DEEP
+  if (p.splits > 1)
+    hipLaunchKernelGGL(gemm4_join_kernel, dim3((unsigned)((N + 1023) / 1024), (unsigned)M), dim3(256), 0, stream,
+                       ws, M, N, p.ldw, p.splits, c);
+}
+
+hipError_t launch_gemm4_deep(int a_elem, int64_t M, int64_t N, int64_t K, const void* a,
+                             const void* sa, const void* b, const void* sb, void* c, void* ws,
+                             hipStream_t stream) {
+  const uint8_t *A = (const uint8_t*)a, *SA = (const uint8_t*)sa, *B = (const uint8_t*)b,
+                *SB = (const uint8_t*)sb;
+  uint16_t* C = (uint16_t*)c;
+  if (a_elem == ELEM_E4M3) launch_deep<ELEM_E4M3>(M, N, K, A, SA, B, SB, C, (float*)ws, stream);
+  else if (a_elem == ELEM_E5M2) launch_deep<ELEM_E5M2>(M, N, K, A, SA, B, SB, C, (float*)ws, stream);
+  else if (a_elem == ELEM_E2M1) launch_deep<ELEM_E2M1>(M, N, K, A, SA, B, SB, C, (float*)ws, stream);
+  else return hipErrorInvalidValue;
+  return hipGetLastError();
+}
+
+template <int FA>
+static void launch_grouped_deep(int64_t G, const int64_t* offsets, int64_t T, int64_t N, int64_t K,
+                                const uint8_t* a, const uint8_t* sa, const uint8_t* b, const uint8_t* sb,
+                                uint16_t* c, hipStream_t stream) {
+  const dim3 grid((unsigned)((N + 127) / 128), (unsigned)G);
+  // 64 groups of 4096 x 4096: 16 rows each 129 us in tiles of 32 rows, 157 in
+  // 128; 62 rows each 262 and 199
+  if (T <= 24 * G)
+    hipLaunchKernelGGL((grouped4_deep_kernel<FA, 1, 4, 1, 1, 2, true>), grid, dim3(256), 0, stream, offsets, T, a,
+                       sa, b, sb, c, N, K);
+  else
+    hipLaunchKernelGGL((grouped4_deep_kernel<FA, 2, 2, 2, 2, 1, FA != ELEM_E2M1>), grid, dim3(256), 0, stream,
+                       offsets, T, a, sa, b, sb, c, N, K);
+}
+
+hipError_t launch_grouped_gemm4_deep(int a_elem, int64_t G, const int64_t* offsets, int64_t T,
+                                     int64_t N, int64_t K, const void* a, const void* sa,
+                                     const void* b, const void* sb, void* c, hipStream_t stream) {
+  const uint8_t *A = (const uint8_t*)a, *SA = (const uint8_t*)sa, *B = (const uint8_t*)b,
+                *SB = (const uint8_t*)sb;
+  uint16_t* C = (uint16_t*)c;
+  if (a_elem == ELEM_E4M3) launch_grouped_deep<ELEM_E4M3>(G, offsets, T, N, K, A, SA, B, SB, C, stream);
+  else if (a_elem == ELEM_E5M2) launch_grouped_deep<ELEM_E5M2>(G, offsets, T, N, K, A, SA, B, SB, C, stream);
+  else if (a_elem == ELEM_E2M1) launch_grouped_deep<ELEM_E2M1>(G, offsets, T, N, K, A, SA, B, SB, C, stream);
+  else return hipErrorInvalidValue;
+  return hipGetLastError();
+}
+
+}  // namespace mx

@@ -112,8 +112,11 @@ hipError_t launch_requant_grouped_col(int elem, int out_elem, const void* q, con
                                       int64_t cap, void* qt, void* st, hipStream_t stream);
 
 // Products with E2M1 weights b; a_elem 0 = E4M3, 1 = E5M2, 4 = E2M1.
+// workspace: gemm4_workspace bytes.
+size_t gemm4_workspace(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm4(int a_elem, int64_t M, int64_t N, int64_t K, const void* a, const void* sa,
-                        const void* b, const void* sb, void* c, int num_cus, hipStream_t stream);
+                        const void* b, const void* sb, void* c, void* workspace, int num_cus,
+                        hipStream_t stream);
 hipError_t launch_grouped_gemm4(int a_elem, int64_t G, const int64_t* offsets, int64_t T, int64_t N,
                                 int64_t K, const void* a, const void* sa, const void* b,
                                 const void* sb, void* c, int num_cus, hipStream_t stream);

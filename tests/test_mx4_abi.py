@@ -52,18 +52,18 @@ FAR = [P + (i << 30) for i in range(6)]   # operands well apart
 ])
 def test_gemm4_sizes(sizes, want):
     a, sa, b, sb, c, _ = FAR
-    assert mx.mx_gemm4(*sizes, a, sa, b, sb, c, 0) == want
+    assert mx.mx_gemm4(*sizes, a, sa, b, sb, c, 0, 0, 0) == want
 
 
 @pytest.mark.parametrize("missing", range(5))
 def test_gemm4_pointers(missing):
     ptrs = FAR[:5]
     ptrs[missing] = 0
-    assert mx.mx_gemm4(0, 4, 4, 32, *ptrs, 0) == INVALID
+    assert mx.mx_gemm4(0, 4, 4, 32, *ptrs, 0, 0, 0) == INVALID
     assert mx.mx_grouped_gemm4(0, 2, P, 4, 4, 32, *ptrs, 0) == INVALID
     if missing in (0, 2, 4):
         ptrs[missing] = FAR[missing] + 8
-        assert mx.mx_gemm4(0, 4, 4, 32, *ptrs, 0) == INVALID
+        assert mx.mx_gemm4(0, 4, 4, 32, *ptrs, 0, 0, 0) == INVALID
         assert "aligned" in mx.mx_last_error()
 
 
@@ -71,9 +71,21 @@ def test_gemm4_pointers(missing):
 def test_gemm4_result_shares_no_memory(other):
     ptrs = FAR[:5]
     ptrs[4] = ptrs[other]
-    assert mx.mx_gemm4(4, 4, 4, 32, *ptrs, 0) == INVALID
+    assert mx.mx_gemm4(4, 4, 4, 32, *ptrs, 0, 0, 0) == INVALID
     assert "shares memory" in mx.mx_last_error()
     assert mx.mx_grouped_gemm4(4, 2, P, 4, 4, 32, *ptrs, 0) == INVALID
+
+
+def test_gemm4_workspace():
+    size = mx.mx_gemm4_workspace_size(0, 64, 512, 8192)
+    assert size > 0 and mx.mx_gemm4_workspace_size(0, 1 << 15, 1 << 14, 8192) == 0
+    ptrs = FAR[:5]
+    assert mx.mx_gemm4(0, 64, 512, 8192, *ptrs, FAR[5], size - 1, 0) == INVALID
+    assert mx.mx_gemm4(0, 64, 512, 8192, *ptrs, 0, size, 0) == INVALID
+    assert mx.mx_gemm4(0, 64, 512, 8192, *ptrs, FAR[5] + 8, size, 0) == INVALID
+    assert "aligned" in mx.mx_last_error()
+    for bad in ((2, 64, 512, 8192), (0, -1, 512, 8192), (0, 64, 0, 8192), (0, 64, 512, 8200), (0, 64, 1 << 28, 32)):
+        assert mx.mx_gemm4_workspace_size(*bad) == 0
 
 
 @pytest.mark.parametrize("sizes,want", [
