@@ -17,24 +17,13 @@
 // group g's columns from P_g = 128 (o_g / 128 + g) on and fills every column
 // that holds no token with zero blocks.
 //
-// The column modes also take an MX tensor in row blocks for x (a forward
-// product's operand, kept as an 8-bit checkpoint) and give its column blocks,
-// the operand of the weight gradient: payload and scales are turned back into
-// BF16 as they are read.
-//
-// All kernels are bound by HBM bandwidth: x is read once with 16-byte loads
-// (8-byte ones of an MX tensor), every output byte is written once.
+// All kernels are bound by HBM bandwidth: x is read once with 16-byte loads,
+// every output byte is written once.
+#include "mx_columns.h"
 #include "mx_device.h"
 #include "mx_kernels.h"
 
 namespace mx {
-
-typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-
-__device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
-  u16x2 r = __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b));
-  return __builtin_bit_cast(uint32_t, r);
-}
 
 // ---------------------------------------------------------------------------
 // 1x32 along rows.  Row-major [R, C] with C % 32 == 0 is the same as the flat
@@ -139,78 +128,9 @@ typedef __attribute__((address_space(3))) uint8_t lds8;
 __device__ __forceinline__ int row_chunk(int r, int k) { return k ^ ((r >> 2) & 7); }
 __device__ __forceinline__ int col_chunk(int c, int k) { return k ^ ((c >> 3) & 7); }
 
-// Grouped column mode: the wave's 32 output rows r0 .. r0+31 (a block of
-// the padded token axis) -> first source row and number of real rows.  The
-// group is the last g with P_g <= r0, found by counting (one ballot per 64
-// groups, all offsets loaded at once, lane l of word k holding offsets[64k+l]);
-// offsets are clamped into [0, T], so
-// bad offsets give wrong blocks but only rows inside [0, T) are read.
-constexpr int GCOL_MAX_GROUPS = 512;
-
-// A wave-uniform lane's copy of a 64-bit register.
-__device__ __forceinline__ int64_t readlane64(int64_t v, int l) {
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, l);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)((uint64_t)v >> 32), l);
-  return (int64_t)(((uint64_t)hi << 32) | lo);
-}
-
-__device__ __forceinline__ void gcol_block(const int64_t* __restrict__ offsets, int64_t G,
-                                           int64_t T, int64_t r0, int lane, int64_t& src,
-                                           int& nreal) {
-  int64_t o[GCOL_MAX_GROUPS / 64];
-#pragma unroll
-  for (int k = 0; k < GCOL_MAX_GROUPS / 64; k++) {
-    const int64_t gg = 64 * k + lane;
-    o[k] = gg <= G ? offsets[gg] : T;
-  }
-  int cnt = 0;
-#pragma unroll
-  for (int k = 0; k < GCOL_MAX_GROUPS / 64; k++) {
-    const int64_t gg = 64 * k + lane;
-    const int64_t oc = o[k] < 0 ? 0 : (o[k] > T ? T : o[k]);
-    cnt += __popcll(__ballot(gg < G && 128 * (oc / 128 + gg) <= r0));
-  }
-  src = 0;
-  nreal = 0;
-  if (cnt == 0) return;
-  const int64_t g = cnt - 1;
-  // offsets[g] and offsets[g + 1] from the lanes that loaded them (g is
-  // uniform); only offsets[512] lies past the loaded words
-  int64_t lo = 0, hi = 0;
-#pragma unroll
-  for (int k = 0; k < GCOL_MAX_GROUPS / 64; k++) {
-    if ((g >> 6) == k) lo = readlane64(o[k], (int)(g & 63));
-    if (((g + 1) >> 6) == k) hi = readlane64(o[k], (int)((g + 1) & 63));
-  }
-  if (g + 1 == GCOL_MAX_GROUPS) hi = offsets[g + 1];
-  lo = lo < 0 ? 0 : (lo > T ? T : lo);
-  hi = hi < lo ? lo : (hi > T ? T : hi);
-  const int64_t first = 128 * (lo / 128 + g);
-  if (r0 < first) return;                       // only with decreasing offsets
-  const int64_t j = (r0 - first) >> 5;          // block of the group's range
-  const int64_t left = (hi - lo) - 32 * j;
-  src = lo + 32 * j;
-  nreal = left <= 0 ? 0 : (left >= 32 ? 32 : (int)left);
-}
-
-// Eight elements c .. c + 7 of row r: SRC -1 reads BF16 x, otherwise x is the
-// payload of that element type and xs its row-block scales.
-template <int SRC>
-__device__ __forceinline__ uint4 load_chunk(const void* __restrict__ x, const uint8_t* __restrict__ xs,
-                                            int64_t r, int64_t c, int64_t C) {
-  const int64_t i = r * C + c;
-  if constexpr (SRC < 0) {
-    return load_stream16((const uint16_t*)x + i);
-  } else {
-    const u32x2 w = __builtin_nontemporal_load((const u32x2*)((const uint8_t*)x + i));
-    return decode8_t<SRC>(make_uint2(w.x, w.y), xs[i >> 5]);
-  }
-}
-
 // One 128 x 128 tile at rows R0.., columns C0.. (one tile per workgroup).
-template <int MODE, int EL, int SRC>
-__device__ __forceinline__ void quant_tile(const void* __restrict__ x, const uint8_t* __restrict__ xs,
-                                           int64_t R, int64_t C,
+template <int MODE, int EL>
+__device__ __forceinline__ void quant_tile(const uint16_t* __restrict__ x, int64_t R, int64_t C,
                                            uint8_t* __restrict__ q, uint8_t* __restrict__ s,
                                            uint8_t* __restrict__ qt, uint8_t* __restrict__ st,
                                            int64_t G, const int64_t* __restrict__ offsets,
@@ -231,12 +151,12 @@ __device__ __forceinline__ void quant_tile(const void* __restrict__ x, const uin
     if (r0 < R) gcol_block(offsets, G, T, r0, lane, src, nreal);
 #pragma unroll
     for (int i = 0; i < 4; i++)
-      v[i] = (live && 4 * g + i < nreal) ? load_chunk<SRC>(x, xs, src + 4 * g + i, c, C)
+      v[i] = (live && 4 * g + i < nreal) ? load_stream16(x + (src + 4 * g + i) * C + c)
                                          : make_uint4(0, 0, 0, 0);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; i++)
-      v[i] = live ? load_chunk<SRC>(x, xs, r0 + 4 * g + i, c, C) : make_uint4(0, 0, 0, 0);
+      v[i] = live ? load_stream16(x + (r0 + 4 * g + i) * C + c) : make_uint4(0, 0, 0, 0);
   }
 
   const int rl = 32 * wr + 4 * g;        // local row of this lane's first row
@@ -342,9 +262,9 @@ __device__ __forceinline__ void quant_tile(const void* __restrict__ x, const uin
 // grid.z indexes a batch of equally shaped matrices (contiguous inputs and
 // outputs); the grouped column mode uses G, offsets and T (x has T rows, R is
 // the padded capacity).  One tile per workgroup in every mode.
-template <int MODE, int EL, int SRC>
+template <int MODE, int EL>
 __global__ void __launch_bounds__(TILE_THREADS)
-quant_tile_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ xs, int64_t R, int64_t C, uint8_t* __restrict__ q,
+quant_tile_kernel(const uint16_t* __restrict__ x, int64_t R, int64_t C, uint8_t* __restrict__ q,
                   uint8_t* __restrict__ s, uint8_t* __restrict__ qt, uint8_t* __restrict__ st,
                   int64_t G, const int64_t* __restrict__ offsets, int64_t T) {
   if (blockIdx.z) {
@@ -369,7 +289,7 @@ quant_tile_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ xs
     tr = lin / gridDim.y;
     tc = lin - tr * gridDim.y;
   }
-  quant_tile<MODE, EL, SRC>(x, xs, R, C, q, s, qt, st, G, offsets, T, tr * TILE_ROWS, (lds8*)lq, (lds8*)lqt,
+  quant_tile<MODE, EL>(x, R, C, q, s, qt, st, G, offsets, T, tr * TILE_ROWS, (lds8*)lq, (lds8*)lqt,
                        (lds8*)ls, (lds8*)lst, tc * TILE_COLS);
 }
 
@@ -395,8 +315,8 @@ hipError_t launch_quant_row(const void* x, int64_t n, void* q, void* s, int elem
 template <int MODE, int EL>
 static void launch_tile(dim3 grid, const void* x, int64_t R, int64_t C, void* q, void* s, void* qt,
                         void* st, int64_t G, const int64_t* offsets, int64_t T, hipStream_t stream) {
-  hipLaunchKernelGGL((quant_tile_kernel<MODE, EL, -1>), grid, dim3(TILE_THREADS), 0, stream,
-                     (const uint16_t*)x, (const uint8_t*)nullptr, R, C, (uint8_t*)q, (uint8_t*)s, (uint8_t*)qt, (uint8_t*)st,
+  hipLaunchKernelGGL((quant_tile_kernel<MODE, EL>), grid, dim3(TILE_THREADS), 0, stream,
+                     (const uint16_t*)x, R, C, (uint8_t*)q, (uint8_t*)s, (uint8_t*)qt, (uint8_t*)st,
                      G, offsets, T);
 }
 
@@ -446,39 +366,6 @@ hipError_t launch_quant_grouped_col(const void* x, int64_t T, int64_t C, int64_t
   dim3 grid((unsigned)((cap + TILE_ROWS - 1) / TILE_ROWS), (unsigned)((C + TILE_COLS - 1) / TILE_COLS));
   launch_tile_elem<TILE_GCOL>(elem, grid, x, cap, C, nullptr, nullptr, qt, st, G, offsets, T, stream);
   return hipGetLastError();
-}
-
-template <int MODE>
-static hipError_t launch_requant(int elem, int out_elem, dim3 grid, const void* x, const void* xs,
-                                 int64_t R, int64_t C, void* qt, void* st, int64_t G,
-                                 const int64_t* offsets, int64_t T, hipStream_t stream) {
-#define MX_REQUANT(SRC_, EL_)                                                                       \
-  hipLaunchKernelGGL((quant_tile_kernel<MODE, EL_, SRC_>), grid, dim3(TILE_THREADS), 0, stream,     \
-                     (const uint16_t*)x, (const uint8_t*)xs, R, C, (uint8_t*)nullptr,              \
-                     (uint8_t*)nullptr, (uint8_t*)qt, (uint8_t*)st, G, offsets, T)
-  if (elem == ELEM_E4M3 && out_elem == ELEM_E4M3) MX_REQUANT(ELEM_E4M3, ELEM_E4M3);
-  else if (elem == ELEM_E4M3 && out_elem == ELEM_E5M2) MX_REQUANT(ELEM_E4M3, ELEM_E5M2);
-  else if (elem == ELEM_E5M2 && out_elem == ELEM_E4M3) MX_REQUANT(ELEM_E5M2, ELEM_E4M3);
-  else if (elem == ELEM_E5M2 && out_elem == ELEM_E5M2) MX_REQUANT(ELEM_E5M2, ELEM_E5M2);
-  else return hipErrorInvalidValue;
-#undef MX_REQUANT
-  return hipGetLastError();
-}
-
-hipError_t launch_requant_col(int elem, int out_elem, const void* q, const void* s, int64_t R,
-                              int64_t C, void* qt, void* st, hipStream_t stream) {
-  const dim3 grid((unsigned)((R + TILE_ROWS - 1) / TILE_ROWS),
-                  (unsigned)((C + TILE_COLS - 1) / TILE_COLS));
-  return launch_requant<TILE_COL>(elem, out_elem, grid, q, s, R, C, qt, st, 0, nullptr, 0, stream);
-}
-
-hipError_t launch_requant_grouped_col(int elem, int out_elem, const void* q, const void* s,
-                                      int64_t T, int64_t C, int64_t G, const int64_t* offsets,
-                                      int64_t cap, void* qt, void* st, hipStream_t stream) {
-  if (G < 1 || G > GCOL_MAX_GROUPS) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)((cap + TILE_ROWS - 1) / TILE_ROWS),
-                  (unsigned)((C + TILE_COLS - 1) / TILE_COLS));
-  return launch_requant<TILE_GCOL>(elem, out_elem, grid, q, s, cap, C, qt, st, G, offsets, T, stream);
 }
 
 }  // namespace mx

@@ -9,17 +9,11 @@
 //
 // All kernels are bound by HBM: x is read once, every output byte is written
 // once.
+#include "mx_columns.h"
 #include "mx_device.h"
 #include "mx_kernels.h"
 
 namespace mx {
-
-typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-
-__device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
-  u16x2 r = __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b));
-  return __builtin_bit_cast(uint32_t, r);
-}
 
 constexpr int ROW4_THREADS = 256;
 constexpr int ROW4_UNROLL = 4;
@@ -71,10 +65,10 @@ quant4_tile_kernel(const uint16_t* __restrict__ x, int64_t R, int64_t C, uint8_t
                    uint8_t* __restrict__ s, uint8_t* __restrict__ qt, uint8_t* __restrict__ st) {
   constexpr int COLS = 64 * NC;
   __shared__ __attribute__((aligned(16))) uint8_t lqt_[COLS * 128];  // column payload
-  __shared__ __attribute__((aligned(16))) uint8_t lst_[COLS * 8];    // column scales
+  __shared__ __attribute__((aligned(16))) uint8_t lsf_[8 * COLS * 2];  // column scales as BF16: [wave][column]
   __shared__ __attribute__((aligned(16))) uint8_t lq_[DUAL ? TILE4_ROWS * COLS / 2 : 16];
   __shared__ __attribute__((aligned(16))) uint8_t ls_[DUAL ? TILE4_ROWS * COLS / 32 : 16];
-  lds8 *lqt = (lds8*)lqt_, *lst = (lds8*)lst_, *lq = (lds8*)lq_, *ls = (lds8*)ls_;
+  lds8 *lqt = (lds8*)lqt_, *lsf = (lds8*)lsf_, *lq = (lds8*)lq_, *ls = (lds8*)ls_;
   {
     const int64_t z = blockIdx.z, n = R * C;
     x += z * n;
@@ -114,38 +108,37 @@ quant4_tile_kernel(const uint16_t* __restrict__ x, int64_t R, int64_t C, uint8_t
         if ((h & 3) == 0) ls[r * (COLS / 32) + 2 * n + (h >> 2)] = (uint8_t)sb;
       }
     }
-    // column maxima, two columns to a word
+    // column maxima, two columns to a word; lanes 2 k and 2 k + 1 of g form the
+    // scales of columns 8 h + 2 k and + 1, and every lane reads all back
     const uint32_t M = 0x7FFF7FFFu;
     const uint32_t* w0 = (const uint32_t*)&v[n][0];
     const uint32_t* w1 = (const uint32_t*)&v[n][1];
     const uint32_t* w2 = (const uint32_t*)&v[n][2];
     const uint32_t* w3 = (const uint32_t*)&v[n][3];
-    uint32_t sbc[8];
+    uint32_t m[4];
 #pragma unroll
-    for (int k = 0; k < 4; k++) {
-      uint32_t m = pk_max(pk_max(w0[k] & M, w1[k] & M), pk_max(w2[k] & M, w3[k] & M));
-      m = pk_max(m, (uint32_t)__shfl_xor((int)m, 8, 64));
-      m = pk_max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
-      m = pk_max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
-      sbc[2 * k] = scale_byte_t<ELEM_E2M1>(m & 0xFFFFu);
-      sbc[2 * k + 1] = scale_byte_t<ELEM_E2M1>(m >> 16);
-    }
-    uint32_t mine = sbc[0];
+    for (int k = 0; k < 4; k++) m[k] = pk_max(pk_max(w0[k] & M, w1[k] & M), pk_max(w2[k] & M, w3[k] & M));
+    const uint32_t two = pair_scale<ELEM_E2M1>(column_max4(m));
+    lds8* own = lsf + (wave * NC + n) * 128 + 16 * h;
+    *(lds32*)(own + 4 * (g >> 1)) = two;
+    const bool bad = __any((two & 0xFFFFu) == 0x7F80u || (two >> 16) == 0x7F80u);
+    const u32x4 f = *(const __attribute__((address_space(3))) u32x4*)own;
+    const uint32_t fs[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
     for (int j = 0; j < 8; j++) {
       const int k = j >> 1;
-      const uint32_t p01 = (j & 1) ? pair_hi(w0[k], w1[k]) : pair_lo(w0[k], w1[k]);
-      const uint32_t p23 = (j & 1) ? pair_hi(w2[k], w3[k]) : pair_lo(w2[k], w3[k]);
-      const float sc = cvt_scale(sbc[j]);
+      const uint32_t sel = (j & 1) ? 0x07060302u : 0x05040100u;
+      const uint32_t p01 = __builtin_amdgcn_perm(w1[k], w0[k], sel);
+      const uint32_t p23 = __builtin_amdgcn_perm(w3[k], w2[k], sel);
+      const uint32_t fb = (j & 1) ? fs[k] & 0xFFFF0000u : fs[k] << 16;
+      const float sc = __uint_as_float(fb);
       uint32_t o = 0;
       o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(v2bf, p01), sc, 0);
       o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(v2bf, p23), sc, 1);
-      if (sbc[j] == 0xFFu) o = 0x7777u;
+      if (bad && fb == 0x7F800000u) o = 0x7777u;
       const int cc = 64 * n + 8 * h + j;
       *(lds16*)(lqt + cc * 128 + ((wave ^ h) << 4) + 2 * g) = (uint16_t)o;
-      mine = g == j ? sbc[j] : mine;
     }
-    lst[(64 * n + 8 * h + g) * 8 + wave] = (uint8_t)mine;
   }
   __syncthreads();
 
@@ -163,12 +156,17 @@ quant4_tile_kernel(const uint16_t* __restrict__ x, int64_t R, int64_t C, uint8_t
     }
   }
   if (t < cols_here) {
+    uint32_t word[2] = {0, 0};
+#pragma unroll
+    for (int b = 0; b < 8; b++)
+      word[b >> 2] |= (((uint32_t)lsf[b * COLS * 2 + 2 * t] >> 7) | ((uint32_t)lsf[b * COLS * 2 + 2 * t + 1] << 1))
+                      << (8 * (b & 3));
     uint8_t* dst = st + (C0 + t) * (R >> 5) + (R0 >> 5);
     const int nb = (int)(rows_here >> 5);
     if (nb == 8 && ((uintptr_t)dst & 7) == 0) {
-      *(u32x2*)dst = *(const __attribute__((address_space(3))) u32x2*)(lst + t * 8);
+      *(u32x2*)dst = (u32x2){word[0], word[1]};
     } else {
-      for (int b = 0; b < nb; b++) dst[b] = lst[t * 8 + b];
+      for (int b = 0; b < nb; b++) dst[b] = (uint8_t)(word[b >> 2] >> (8 * (b & 3)));
     }
   }
   if (DUAL) {
