@@ -910,10 +910,28 @@ def grad_clip(tensors, max_norm: float):
 # 4-bit weights and 8-bit activation checkpoints
 # ---------------------------------------------------------------------------
 
-def _elem(name, known, what="element type"):
+def _elem(name, known):
     if name not in known:
-        raise ValueError(f"unknown {what} {name!r}; expected one of {list(known)}")
+        raise ValueError(f"unknown element type {name!r}; expected one of {list(known)}")
     return known[name]
+
+
+def _needs(dtype, ndim, *named):
+    """``_need`` of several (tensor, name) pairs of one type and rank: the
+    properties are swept first, and the one at fault is looked for only once
+    there is one (a call of a few microseconds has no time for more)."""
+    try:
+        here = _torch().cuda.current_device()
+        for t, _ in named:
+            if not (t.dtype is dtype and t.dim() == ndim and t.get_device() == here
+                    and t.is_contiguous()):
+                break
+        else:
+            return
+    except (AttributeError, RuntimeError, AssertionError):
+        pass
+    for t, name in named:
+        _need(t, dtype, name, ndim)
 
 
 def _out(out, shape, device):
@@ -987,10 +1005,11 @@ def gemm4(a, sa, b, sb, a_elem: str = "e4m3", out=None):
     gradient its column blocks.  out may share no memory with the operands."""
     torch = _torch()
     code = _elem(a_elem, OPERAND_ELEMS)
-    for t, n in ((a, "a"), (sa, "sa"), (b, "b"), (sb, "sb")):
-        _need(t, torch.uint8, n, 2)
-    M, N = a.shape[0], b.shape[0]
-    K = a.shape[1] * (2 if a_elem == "e2m1" else 1)
+    _needs(torch.uint8, 2, (a, "a"), (sa, "sa"), (b, "b"), (sb, "sb"))
+    M, K = a.shape
+    N = b.shape[0]
+    if a_elem == "e2m1":
+        K *= 2
     if K % 32 == 0:
         _shape(sa, (M, K // 32), "sa")
         _shape(b, (N, K // 2), "b")
@@ -1013,10 +1032,8 @@ def grouped_gemm4(offsets, a, sa, b, sb, a_elem: str = "e4m3", out=None):
     torch = _torch()
     code = _elem(a_elem, OPERAND_ELEMS)
     _need(offsets, torch.int64, "offsets", 1)
-    for t, n in ((a, "a"), (sa, "sa")):
-        _need(t, torch.uint8, n, 2)
-    for t, n in ((b, "b"), (sb, "sb")):
-        _need(t, torch.uint8, n, 3)
+    _needs(torch.uint8, 2, (a, "a"), (sa, "sa"))
+    _needs(torch.uint8, 3, (b, "b"), (sb, "sb"))
     G, T, N = offsets.numel() - 1, a.shape[0], b.shape[1]
     K = a.shape[1] * (2 if a_elem == "e2m1" else 1)
     if G < 1:
@@ -1041,7 +1058,7 @@ def swiglu_quant(gate_up, elem: str = "e4m3", checkpoint: bool = True, checkpoin
     ``swiglu_backward``; None with checkpoint=False."""
     torch = _torch()
     code, ckpt_code = _elem(elem, ELEM_TYPES), _elem(checkpoint_elem, ELEM_TYPES)
-    _need(gate_up, torch.bfloat16, "gate_up", 2)
+    _needs(torch.bfloat16, 2, (gate_up, "gate_up"))
     T, F2 = gate_up.shape
     if F2 % 2:
         raise ValueError(f"gate_up must have an even number of columns, got {F2}")
@@ -1058,9 +1075,8 @@ def swiglu_quant(gate_up, elem: str = "e4m3", checkpoint: bool = True, checkpoin
 
 def _swiglu_operands(dh, ckpt_q, ckpt_s):
     torch = _torch()
-    _need(dh, torch.bfloat16, "dh", 2)
-    _need(ckpt_q, torch.uint8, "ckpt_q", 2)
-    _need(ckpt_s, torch.uint8, "ckpt_s", 2)
+    _needs(torch.bfloat16, 2, (dh, "dh"))
+    _needs(torch.uint8, 2, (ckpt_q, "ckpt_q"), (ckpt_s, "ckpt_s"))
     T, F = dh.shape
     _shape(ckpt_q, (T, 2 * F), "ckpt_q")
     if F % 32 == 0:
@@ -1101,8 +1117,7 @@ def requant_col(q, s, elem: str = "e4m3", out_elem: str = "e4m3"):
     rows/32])."""
     torch = _torch()
     code, out_code = _elem(elem, ELEM_TYPES), _elem(out_elem, ELEM_TYPES)
-    _need(q, torch.uint8, "q", 2)
-    _need(s, torch.uint8, "s", 2)
+    _needs(torch.uint8, 2, (q, "q"), (s, "s"))
     R, C = q.shape
     if C % 32 == 0:
         _shape(s, (R, C // 32), "s")
@@ -1119,8 +1134,7 @@ def requant_grouped_col(q, s, offsets, elem: str = "e4m3", out_elem: str = "e4m3
     on the device -> (q_t u8 [C, cap], s_t u8 [C, cap/32])."""
     torch = _torch()
     code, out_code = _elem(elem, ELEM_TYPES), _elem(out_elem, ELEM_TYPES)
-    _need(q, torch.uint8, "q", 2)
-    _need(s, torch.uint8, "s", 2)
+    _needs(torch.uint8, 2, (q, "q"), (s, "s"))
     _need(offsets, torch.int64, "offsets", 1)
     T, C = q.shape
     if C % 32 == 0:

@@ -477,8 +477,10 @@ grouped4_deep_kernel(const int64_t* __restrict__ offsets, int64_t rows, const ui
 // 7168: 15.5, one to a unit 17.0); up to 64 rows 64 x 128 (64 x 18432: 24.2, two
 // to a unit 26.3); above, 128 x 128 while its tiles find a unit each (512 x 7168
 // x 18432: 75, against 117 with 128 x 256), 128 x 256 beyond (2048 rows: 318
-// against 361).  K is split so far as workgroups still find a unit each, eight
-// steps to a split at least (1 x 7168 x 18432: 15.6 in four, 31 whole).
+// against 361).  K is split so far as workgroups still find a unit each and the
+// steps saved outweigh the second launch and the partial sums' way through
+// memory (1 x 7168 x 18432: 15.6 in four, 31 whole; 1 x 4096 x 4096: 9.8 whole,
+// 12.4 in four).
 enum Shape4 { TILE_32, TILE_64, TILE_128, TILE_WIDE };
 
 struct Plan4 {
@@ -495,10 +497,17 @@ static Plan4 plan_of(int64_t M, int64_t N, int64_t K) {
   else if (M <= 64) p.shape = TILE_64, p.tiles = n128;
   else if (t128 <= 256) p.shape = TILE_128, p.tiles = t128;
   else p.shape = TILE_WIDE, p.tiles = (M + 127) / 128 * ((N + 255) / 256);
-  int64_t s = 256 / p.tiles;
-  if (s > K / 2048) s = K / 2048;
-  // the wide tile's partial sums would need rows of its own width
-  p.splits = s < 1 || p.shape == TILE_WIDE ? 1 : s > 16 ? 16 : (int)s;
+  p.splits = 1;
+  if (p.shape == TILE_WIDE) return p;
+  // microseconds: a step of 256 elements by the tile's height, eight for the
+  // second launch, and partial sums written and read at 4 TB/s
+  const double step = p.shape == TILE_32 ? 0.55 : p.shape == TILE_64 ? 0.85 : 1.1;
+  const int64_t steps = (K + 255) / 256;
+  double best = steps * step;
+  for (int s = 2; s <= 16 && s * p.tiles <= 256 && s <= steps; s++) {
+    const double us = (steps + s - 1) / s * step + 8.0 + 8e-6 / 4 * s * M * p.ldw;
+    if (us < best) best = us, p.splits = s;
+  }
   return p;
 }
 
