@@ -87,37 +87,38 @@ struct Deep4 {
     if (nkb < 4) off_s = OOB;  // rows shorter than a dword: short_scales() loads them
   }
 
-  // Loads of step kt into the stage at `to`.  WHOLE: the step lies in K and
-  // in this workgroup's part, its offset is scalar.  Otherwise chunks past K
-  // read as zero, and a step past the last touches no memory.
+  // Load D (of OPS: A's, B's, the scales') of step kt into the stage at `to`.
+  // WHOLE: the step lies in K and in this workgroup's part, its offset is
+  // scalar.  Otherwise chunks past K read as zero, and a step past the last
+  // touches no memory.
   template <bool WHOLE>
-  __device__ __forceinline__ void issue(lds_u8* to, int kt, int wave) {
-    const uint32_t ka = (uint32_t)kt * (128 * PANELS), kb = (uint32_t)kt * BROW, ks = (uint32_t)kt * (KS / 32);
-    lds_u8* const tb = to + A_BYTES;
-    lds_u8* const ts = tb + B_BYTES + 256 * wave;
-    if constexpr (WHOLE) {
-#pragma unroll
-      for (int u = 0; u < A_OPS; u++) dma16_at(to + (wave + WAVES * u) * 1024, off_a[u], ra, ka);
-#pragma unroll
-      for (int u = 0; u < B_OPS; u++) dma16_at(tb + (wave + WAVES * u) * 1024, off_b[u], rb, kb);
-#pragma unroll
-      for (int h = 0; h < KH; h++) dma4_at(ts + S_BYTES * h, off_s, rs, ks + 4 * h);
+  __device__ __forceinline__ void issue_one(lds_u8* to, int kt, int d, int wave) {
+    if (d < A_OPS) {
+      const uint32_t ka = (uint32_t)kt * (128 * PANELS);
+      lds_u8* const at = to + (wave + WAVES * d) * 1024;
+      if constexpr (WHOLE) dma16_at(at, off_a[d], ra, ka);
+      else dma16(at, kt < kt1 && ka + pos_a[d] < row_a ? off_a[d] + ka : OOB, ra);
+    } else if (d < A_OPS + B_OPS) {
+      const int u = d - A_OPS;
+      const uint32_t kb = (uint32_t)kt * BROW;
+      lds_u8* const at = to + A_BYTES + (wave + WAVES * u) * 1024;
+      if constexpr (WHOLE) dma16_at(at, off_b[u], rb, kb);
+      else dma16(at, kt < kt1 && kb + pos_b < row_b ? off_b[u] + kb : OOB, rb);
     } else {
-      const bool live = kt < kt1;
-#pragma unroll
-      for (int u = 0; u < A_OPS; u++)
-        dma16(to + (wave + WAVES * u) * 1024, live && ka + pos_a[u] < row_a ? off_a[u] + ka : OOB, ra);
-#pragma unroll
-      for (int u = 0; u < B_OPS; u++)
-        dma16(tb + (wave + WAVES * u) * 1024, live && kb + pos_b < row_b ? off_b[u] + kb : OOB, rb);
+      const int h = d - A_OPS - B_OPS;
+      const uint32_t ks = (uint32_t)kt * (KS / 32) + 4 * h;
+      lds_u8* const at = to + A_BYTES + B_BYTES + S_BYTES * h + 256 * wave;
       // a dword that would pass the row's last scale byte ends there instead
       // and is shifted when it is read
-#pragma unroll
-      for (int h = 0; h < KH; h++) {
-        const uint32_t at = ks + 4 * h;
-        dma4(ts + S_BYTES * h, live && at < nkb ? off_s + (at + 4 <= nkb ? at : nkb - 4) : OOB, rs);
-      }
+      if constexpr (WHOLE) dma4_at(at, off_s, rs, ks);
+      else dma4(at, kt < kt1 && ks < nkb ? off_s + (ks + 4 <= nkb ? ks : nkb - 4) : OOB, rs);
     }
+  }
+  // Loads D0 .. D1 - 1 of step kt
+  template <bool WHOLE, int D0, int D1>
+  __device__ __forceinline__ void issue(lds_u8* to, int kt, int wave) {
+#pragma unroll
+    for (int d = D0; d < D1; d++) issue_one<WHOLE>(to, kt, d, wave);
   }
 
   // A row's scale words of a step: with 8-bit A word h holds byte S for half S
@@ -144,22 +145,24 @@ struct Deep4 {
     }
   }
 
-  // A step's MFMAs come in UNITS of half a panel (half a step with 4-bit A),
-  // whose fragments are read while the unit before is multiplied: unit 0 of a
-  // stage while the last unit of the stage before is.
+  // A step's MFMAs come in UNITS of half a panel (half a step with 4-bit A).
+  // While one unit is multiplied the fragments of the next are read, those of a
+  // step's first unit with the last unit of the step before, and a share of a
+  // later step's loads is issued.
   static constexpr int UNITS = 2 * PANELS;
+  static constexpr int MFMAS = FM * FN * (A4 ? 2 : 1);  // of a unit
   struct Frags {
     v8i a[FM], b[FN];
   };
+  // Fragment r of a unit: A's, then B's
   template <int U>
-  __device__ __forceinline__ static void read_unit(const lds_u8* cur, Frags& f, int wm, int wn, int lane) {
+  __device__ __forceinline__ static void read_one(const lds_u8* cur, Frags& f, int r, int wm, int wn, int lane) {
     constexpr int h = U / 2, S = U % 2;
     const int g = lane >> 5, i = lane & 31;
-#pragma unroll
-    for (int x = 0; x < FM; x++) f.a[x] = read_frag(cur + h * A_PANEL, 32 * FM * wm + 32 * x + i, S, g);
-#pragma unroll
-    for (int x = 0; x < FN; x++) {
-      const int row = 32 * FN * wn + 32 * x + i;
+    if (r < FM) {
+      f.a[r] = read_frag(cur + h * A_PANEL, 32 * FM * wm + 32 * r + i, S, g);
+    } else {
+      const int x = r - FM, row = 32 * FN * wn + 32 * x + i;
       if (A4) {
         f.b[x] = read_frag(cur + A_BYTES, row, S, g);
       } else {
@@ -170,32 +173,46 @@ struct Deep4 {
       }
     }
   }
+  // MFMA m of a unit
   template <int U>
-  __device__ __forceinline__ static void mma_unit(const Frags& f, v16f (&acc)[FN][FM],
-                                                  const uint32_t (&sar)[FM][KH],
-                                                  const uint32_t (&sbr)[FN][KH]) {
+  __device__ __forceinline__ static void mma_one(const Frags& f, int m, v16f (&acc)[FN][FM],
+                                                 const uint32_t (&sar)[FM][KH],
+                                                 const uint32_t (&sbr)[FN][KH]) {
     constexpr int h = U / 2, S = U % 2;
+    const int x = m / FM % FN, y = m % FM;
     if constexpr (A4) {
-#pragma unroll
-      for (int x = 0; x < FN; x++)
-#pragma unroll
-        for (int y = 0; y < FM; y++)
-          acc[x][y] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              low(f.b[x]), low(f.a[y]), acc[x][y], ELEM_E2M1, ELEM_E2M1, S, (int)sbr[x][0], S, (int)sar[y][0]);
-#pragma unroll
-      for (int x = 0; x < FN; x++)
-#pragma unroll
-        for (int y = 0; y < FM; y++)
-          acc[x][y] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              high(f.b[x]), high(f.a[y]), acc[x][y], ELEM_E2M1, ELEM_E2M1, S + 2, (int)sbr[x][0], S + 2,
-              (int)sar[y][0]);
+      if (m < FM * FN)
+        acc[x][y] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            low(f.b[x]), low(f.a[y]), acc[x][y], ELEM_E2M1, ELEM_E2M1, S, (int)sbr[x][0], S, (int)sar[y][0]);
+      else
+        acc[x][y] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            high(f.b[x]), high(f.a[y]), acc[x][y], ELEM_E2M1, ELEM_E2M1, S + 2, (int)sbr[x][0], S + 2,
+            (int)sar[y][0]);
     } else {
+      acc[x][y] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          f.b[x], f.a[y], acc[x][y], ELEM_E2M1, FA, S, (int)sbr[x][h], S, (int)sar[y][h]);
+    }
+  }
+  // Multiplies unit U out of f, reads unit V of the stage at `from` into nx and
+  // issues share P of step kl's loads into the stage at `to`.  The order is
+  // held: a wave issues in order, so loads in a bunch (18 cycles of the
+  // compute unit each) would hold its MFMAs back; in a bunch after the barrier
+  // they took as long as the MFMAs, 2050 cycles a step of a 128 x 128 tile
+  // where the MFMAs need 1024.
+  template <int U, int V, int P, bool WHOLE>
+  __device__ __forceinline__ void unit(const Frags& f, Frags& nx, const lds_u8* from, lds_u8* to, int kl,
+                                       int wave, int wm, int wn, int lane, const uint32_t (&sar)[FM][KH],
+                                       const uint32_t (&sbr)[FN][KH], v16f (&acc)[FN][FM]) {
+    constexpr int D0 = P * OPS / UNITS, D1 = (P + 1) * OPS / UNITS, R = FM + FN;
 #pragma unroll
-      for (int x = 0; x < FN; x++)
+    for (int m = 0; m < MFMAS; m++) {
+      mma_one<U>(f, m, acc, sar, sbr);
 #pragma unroll
-        for (int y = 0; y < FM; y++)
-          acc[x][y] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              f.b[x], f.a[y], acc[x][y], ELEM_E2M1, FA, S, (int)sbr[x][h], S, (int)sar[y][h]);
+      for (int r = m * R / MFMAS; r < (m + 1) * R / MFMAS; r++) read_one<V>(from, nx, r, wm, wn, lane);
+#pragma unroll
+      for (int d = D0 + m * (D1 - D0) / MFMAS; d < D0 + (m + 1) * (D1 - D0) / MFMAS; d++)
+        issue_one<WHOLE>(to, kl, d, wave);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 
@@ -216,18 +233,6 @@ struct Deep4 {
     for (int f = 0; f < FN; f++) shape<WHOLE>(sbr[f], kt, lane >> 5);
   }
 
-  // One unit's MFMAs with the LDS reads of the next among them
-  template <int NDS>
-  __device__ __forceinline__ static void interleave() {
-    constexpr int n = FM * FN * (A4 ? 2 : 1), per = (NDS + n - 1) / n;
-#pragma unroll
-    for (int i = 0; i < n; i++) {
-      __builtin_amdgcn_sched_group_barrier(0x100, per, 0);  // LDS reads
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);    // MFMA
-    }
-  }
-  static constexpr int UNIT_READS = 2 * FM + (A4 ? 2 : 1) * FN;
-
   // K below 128, one step: the scale bytes of each row one by one, placed as
   // shape() expects them of the last dword of a row.
   __device__ __forceinline__ void short_scales(int wave, int lane) {
@@ -244,35 +249,27 @@ struct Deep4 {
     __syncthreads();
   }
 
-  // Step kt on stage `cur`, unit 0 of it in f0 and its scales shaped; leaves
-  // the same of step kt + 1.  WHOLE: steps up to kt + NS are whole ones.
+  // Step kt on stage `cur`, its first unit in f0 and its scales shaped; leaves
+  // the same of step kt + 1.  On the way the loads of step kt - 1 + NS, into the
+  // stage `old` of step kt - 1, are completed, and those of kt + NS begun.
+  // WHOLE: all of these are whole steps.
   template <bool WHOLE>
-  __device__ __forceinline__ void step(lds_u8* cur, const lds_u8* nxt, int kt, int wave, int wm, int wn,
-                                       int lane, Frags& f0, uint32_t (&sar)[FM][KH],
+  __device__ __forceinline__ void step(lds_u8* old, lds_u8* cur, const lds_u8* nxt, int kt, int wave, int wm,
+                                       int wn, int lane, Frags& f0, uint32_t (&sar)[FM][KH],
                                        uint32_t (&sbr)[FN][KH], v16f (&acc)[FN][FM]) {
     Frags f1;
-    uint32_t nar[FM][KH], nbr[FN][KH];
-    read_unit<1>(cur, f1, wm, wn, lane);
-    mma_unit<0>(f0, acc, sar, sbr);
-    interleave<UNIT_READS>();
+    const int kl = kt - 1 + NS;
+    unit<0, 1, 1, WHOLE>(f0, f1, cur, old, kl, wave, wm, wn, lane, sar, sbr, acc);
     if constexpr (UNITS == 4) {
-      read_unit<2>(cur, f0, wm, wn, lane);
-      mma_unit<1>(f1, acc, sar, sbr);
-      interleave<UNIT_READS>();
-      read_unit<3>(cur, f1, wm, wn, lane);
-      mma_unit<2>(f0, acc, sar, sbr);
-      interleave<UNIT_READS>();
+      unit<1, 2, 2, WHOLE>(f1, f0, cur, old, kl, wave, wm, wn, lane, sar, sbr, acc);
+      unit<2, 3, 3, WHOLE>(f0, f1, cur, old, kl, wave, wm, wn, lane, sar, sbr, acc);
     }
-    // every wave has read this stage, which takes step kt + NS; the next one
-    // has landed for every wave
+    // every wave has read this stage; the next one has landed for every wave
     wait_vm<(NS - 2) * OPS>();
     __syncthreads();
+    uint32_t nar[FM][KH], nbr[FN][KH];
     read_scales(nxt, wm, wn, lane, nar, nbr);
-    read_unit<0>(nxt, f0, wm, wn, lane);
-    issue<WHOLE>(cur, kt + NS, wave);
-    mma_unit<UNITS - 1>(f1, acc, sar, sbr);
-    interleave<UNIT_READS + (FM + FN) * KH>();
-    __builtin_amdgcn_sched_barrier(0);  // the scales' shifts would wait on their reads among the MFMAs
+    unit<UNITS - 1, 0, 0, WHOLE>(f1, f0, nxt, cur, kl + 1, wave, wm, wn, lane, sar, sbr, acc);
     shape_scales<WHOLE>(kt + 1, lane, nar, nbr);
 #pragma unroll
     for (int h = 0; h < KH; h++) {
@@ -285,32 +282,43 @@ struct Deep4 {
 
   __device__ __forceinline__ void run(v16f (&acc)[FN][FM], int wave, int lane) {
     const int wm = wave % WM, wn = wave / WM;
+    constexpr int FIRST = OPS / UNITS;  // loads of a step's share 0
 #pragma unroll
     for (int x = 0; x < FN; x++)
 #pragma unroll
       for (int y = 0; y < FM; y++) acc[x][y] = (v16f){};
-#pragma unroll
-    for (int p = 0; p < NS; p++) issue<false>(st + p * STAGE_BYTES, kt0 + p, wave);
-    wait_vm<(NS - 1) * OPS>();
+    const int last = kt1 < full ? kt1 : full;  // the end of whole steps
+    // NS - 1 steps and the first share of one more are on their way
+#pragma unroll 1
+    for (int p = 0; p < NS - 1; p++) {
+      if (kt0 + p < last) issue<true, 0, OPS>(st + p * STAGE_BYTES, kt0 + p, wave);
+      else issue<false, 0, OPS>(st + p * STAGE_BYTES, kt0 + p, wave);
+    }
+    lds_u8* old = st + (NS - 1) * STAGE_BYTES;
+    if (kt0 + NS - 1 < last) issue<true, 0, FIRST>(old, kt0 + NS - 1, wave);
+    else issue<false, 0, FIRST>(old, kt0 + NS - 1, wave);
+    wait_vm<(NS - 2) * OPS + FIRST>();
     __syncthreads();
     if (nkb < 4) short_scales(wave, lane);
     Frags f0;
     uint32_t sar[FM][KH], sbr[FN][KH];
     read_scales(st, wm, wn, lane, sar, sbr);
-    read_unit<0>(st, f0, wm, wn, lane);
+#pragma unroll
+    for (int r = 0; r < FM + FN; r++) read_one<0>(st, f0, r, wm, wn, lane);
     shape_scales<false>(kt0, lane, sar, sbr);
     lds_u8* cur = st;
     lds_u8* const end = st + NS * STAGE_BYTES;
-    const int whole = (kt1 < full ? kt1 : full) - NS;  // steps before it start whole ones
     int kt = kt0;
-    for (; kt < whole; kt++) {
+    for (; kt < last - NS; kt++) {
       lds_u8* nxt = cur + STAGE_BYTES == end ? st : cur + STAGE_BYTES;
-      step<true>(cur, nxt, kt, wave, wm, wn, lane, f0, sar, sbr, acc);
+      step<true>(old, cur, nxt, kt, wave, wm, wn, lane, f0, sar, sbr, acc);
+      old = cur;
       cur = nxt;
     }
     for (; kt < kt1; kt++) {
       lds_u8* nxt = cur + STAGE_BYTES == end ? st : cur + STAGE_BYTES;
-      step<false>(cur, nxt, kt, wave, wm, wn, lane, f0, sar, sbr, acc);
+      step<false>(old, cur, nxt, kt, wave, wm, wn, lane, f0, sar, sbr, acc);
+      old = cur;
       cur = nxt;
     }
     wait_vm_all();  // no load may still be writing LDS when the workgroup ends
