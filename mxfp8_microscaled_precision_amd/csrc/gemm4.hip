@@ -5,7 +5,7 @@
 // 4-bit weights with 8-bit activations for serving and 4-bit training of the
 // routed experts (practice page, w4a8-mx; torchtitan-npu MXFP8/HiF8 tutorial,
 // step-2 environment table, ENABLE_MXFP4_QAT).  This file has the large tiles
-// for many rows; gemm4_deep.hip the small ones, for everything else.
+// for many rows; gemm4_deep.hip has the small ones, for everything else.
 //
 // Lane layout of v_mfma_scale_f32_32x32x64, found by one-hot operands on the
 // device: lane l = 32 g + i holds row i; in 4 bits its 16 bytes are K 32 g ..
@@ -30,7 +30,12 @@ namespace mx {
 // multiplies blocks S and 2 + S, of which A's lanes hold 16 bytes each (chunks
 // 2 S + g and 4 + 2 S + g) and B's lane half g the block 2 g + S (chunk 2 g +
 // S).
-template <int FA>
+//
+// WHOLE: K is a multiple of 512 and N of 8.  Otherwise chunks past the end of a
+// row are not loaded (they read as zero), the scales are loaded in dwords, the
+// last one of a row ending with the row, and the result leaves in pieces of 16
+// bytes at any address.
+template <int FA, bool WHOLE>
 struct Tile4 {
   static constexpr int F = 4;
   static constexpr bool A4 = FA == ELEM_E2M1;
@@ -49,6 +54,8 @@ struct Tile4 {
   const uint8_t* __restrict__ sb;
   int64_t m0, m_end, n0, N, K;
   int64_t nks, nkb;
+  uint32_t row_a, row_b;  // bytes of a row, for a lane's chunks at pos_a and pos_b of a step
+  uint32_t pos_a, pos_b;
   lds_u8 *st0, *st1;  // stages: A tile, then B tile
   lds_u8 *ss0, *ss1;  // scale tiles of 16 bytes a row: A's rows, then B's
   u32x4 ra, rb, rsa, rsb;
@@ -59,7 +66,7 @@ struct Tile4 {
   __device__ __forceinline__ void setup(int wave, int lane) {
     const int64_t mrows = m_end - m0, nrows = (N - n0) < ROWS ? (N - n0) : ROWS;
     const int64_t pa = A4 ? K >> 1 : K, pb = K >> 1;
-    nks = K / KS;
+    nks = (K + KS - 1) / KS;
     nkb = K >> 5;
     ra = make_rsrc(a + m0 * pa, mrows * pa);
     rb = make_rsrc(b + n0 * pb, nrows * pb);
@@ -68,15 +75,19 @@ struct Tile4 {
     // A: load t = wave + 4 u covers LDS rows 8 t .. 8 t + 7; lane i lands in
     // row r = 8 t + i / 8 at physical chunk i % 8, logical (i % 8) ^ swz(r)
     const int sw = (4 * wave + (lane >> 4)) & 7;
-    voff_a = (uint32_t)((8 * wave + (lane >> 3)) * pa + 16 * ((lane & 7) ^ sw));
+    row_a = (uint32_t)pa, row_b = (uint32_t)pb;
+    pos_a = 16 * ((lane & 7) ^ sw);
+    voff_a = (uint32_t)((8 * wave + (lane >> 3)) * pa) + pos_a;
     a_step = (uint32_t)(32 * pa);
     if (A4) {
-      voff_b = (uint32_t)((8 * wave + (lane >> 3)) * pb + 16 * ((lane & 7) ^ sw));
+      pos_b = pos_a;
+      voff_b = (uint32_t)((8 * wave + (lane >> 3)) * pb) + pos_b;
       b_step = (uint32_t)(32 * pb);
     } else {
       // rows of 64 bytes: load t covers LDS rows 16 t .. 16 t + 15; lane i
       // lands in row 16 t + i / 4 at chunk i % 4, logical (i % 4) ^ (i / 16)
-      voff_b = (uint32_t)((16 * wave + (lane >> 2)) * pb + 16 * ((lane & 3) ^ (lane >> 4)));
+      pos_b = 16 * ((lane & 3) ^ (lane >> 4));
+      voff_b = (uint32_t)((16 * wave + (lane >> 2)) * pb) + pos_b;
       b_step = (uint32_t)(64 * pb);
     }
     svoff = (uint32_t)((64 * wave + lane) * nkb);
@@ -86,11 +97,13 @@ struct Tile4 {
 
   // Loads of step kt into stage st; a step past the last touches no memory.
   __device__ __forceinline__ void load_a(lds_u8* st, int64_t kt, int u, int wave) {
-    const uint32_t base = kt < nks ? (uint32_t)(128 * kt) : OOB;
+    const bool in = WHOLE ? kt < nks : (uint32_t)(128 * kt) + pos_a < row_a;
+    const uint32_t base = in ? (uint32_t)(128 * kt) : OOB;
     dma16(st + (wave + 4 * u) * 1024, voff_a + base + u * a_step, ra);
   }
   __device__ __forceinline__ void load_b(lds_u8* st, int64_t kt, int u, int wave) {
-    const uint32_t base = kt < nks ? (uint32_t)(BROW * kt) : OOB;
+    const bool in = WHOLE ? kt < nks : (uint32_t)(BROW * kt) + pos_b < row_b;
+    const uint32_t base = in ? (uint32_t)(BROW * kt) : OOB;
     dma16(st + A_BYTES + (wave + 4 * u) * 1024, voff_b + base + u * b_step, rb);
   }
   __device__ __forceinline__ void issue_stage(lds_u8* st, int64_t kt, int wave) {
@@ -100,11 +113,22 @@ struct Tile4 {
     for (int u = 0; u < B_OPS; u++) load_b(st, kt, u, wave);
   }
 
-  // Scale bytes of GS steps, 16 bytes a row (K a multiple of 512)
+  // Scale bytes of GS steps: 16 bytes a row if WHOLE, otherwise four planes of a
+  // dword a row
   __device__ __forceinline__ void issue_scales(lds_u8* buf, int64_t group, int wave) {
-    const uint32_t off = 16 * group < nkb ? svoff + (uint32_t)(16 * group) : OOB;
-    dma16(buf + wave * 1024, off, rsa);
-    dma16(buf + 4096 + wave * 1024, off, rsb);
+    if constexpr (WHOLE) {
+      const uint32_t off = 16 * group < nkb ? svoff + (uint32_t)(16 * group) : OOB;
+      dma16(buf + wave * 1024, off, rsa);
+      dma16(buf + 4096 + wave * 1024, off, rsb);
+    } else {
+#pragma unroll
+      for (int d = 0; d < 4; d++) {
+        const uint32_t at = (uint32_t)(16 * group) + 4 * d, n = (uint32_t)nkb;
+        const uint32_t off = at < n ? svoff + (at + 4 <= n ? at : n - 4) : OOB;
+        dma4(buf + d * 1024 + wave * 256, off, rsa);
+        dma4(buf + 4096 + d * 1024 + wave * 256, off, rsb);
+      }
+    }
   }
 
   // A row's scale bytes of one step (8 of them: `hi` the last four) as the
@@ -114,20 +138,39 @@ struct Tile4 {
     if (A4) return __builtin_amdgcn_perm(hi, lo, g ? 0x07050301u : 0x06040200u);
     return lo >> (16 * g);
   }
-  __device__ __forceinline__ void read_scales(const lds_u8* buf, int q, int wm, int wn, int lane,
+  // Scales of step kt, the one numbered q of the GS whose scales buf holds
+  __device__ __forceinline__ void read_scales(const lds_u8* buf, int q, int64_t kt, int wm, int wn, int lane,
                                               uint32_t* sar, uint32_t* sbr) {
     const int g = lane >> 5, i = lane & 31;
+    if constexpr (WHOLE) {
 #pragma unroll
-    for (int f = 0; f < F; f++) {
-      const lds_u8* pa = buf + (32 * F * wm + 32 * f + i) * 16 + SB * q;
-      const lds_u8* pb = buf + 4096 + (32 * F * wn + 32 * f + i) * 16 + SB * q;
-      if (A4) {
-        const v2i x = *(const lds_v2i*)pa, y = *(const lds_v2i*)pb;
-        sar[f] = shape_scale((uint32_t)x.x, (uint32_t)x.y, g);
-        sbr[f] = shape_scale((uint32_t)y.x, (uint32_t)y.y, g);
-      } else {
-        sar[f] = *(const lds_u16*)(pa + 2 * g);
-        sbr[f] = *(const lds_u16*)(pb + 2 * g);
+      for (int f = 0; f < F; f++) {
+        const lds_u8* pa = buf + (32 * F * wm + 32 * f + i) * 16 + SB * q;
+        const lds_u8* pb = buf + 4096 + (32 * F * wn + 32 * f + i) * 16 + SB * q;
+        if (A4) {
+          const v2i x = *(const lds_v2i*)pa, y = *(const lds_v2i*)pb;
+          sar[f] = shape_scale((uint32_t)x.x, (uint32_t)x.y, g);
+          sbr[f] = shape_scale((uint32_t)y.x, (uint32_t)y.y, g);
+        } else {
+          sar[f] = *(const lds_u16*)(pa + 2 * g);
+          sbr[f] = *(const lds_u16*)(pb + 2 * g);
+        }
+      }
+    } else {
+      typedef const __attribute__((address_space(3))) uint32_t lds_u32;
+      // a dword that ended with the row holds bytes of the block before it;
+      // one past the row was not loaded and is 0
+      const int over0 = (int)(SB * kt + 4 - nkb), over1 = over0 + 4;
+      const int sh0 = over0 > 0 ? (8 * over0) & 31 : 0, sh1 = over1 > 0 ? (8 * over1) & 31 : 0;
+      const lds_u8* plane = buf + q * (SB / 4) * 1024;
+#pragma unroll
+      for (int f = 0; f < F; f++) {
+        const lds_u8* pa = plane + 4 * (32 * F * wm + 32 * f + i);
+        const lds_u8* pb = plane + 4096 + 4 * (32 * F * wn + 32 * f + i);
+        uint32_t a1 = 0, b1 = 0;
+        if (A4) a1 = *(lds_u32*)(pa + 1024) >> sh1, b1 = *(lds_u32*)(pb + 1024) >> sh1;
+        sar[f] = shape_scale(*(lds_u32*)pa >> sh0, a1, g);
+        sbr[f] = shape_scale(*(lds_u32*)pb >> sh0, b1, g);
       }
     }
   }
@@ -200,9 +243,10 @@ struct Tile4 {
     prefetch_lines(pf_scratch + wave * 512, (pf_row_a + (uint32_t)(128 * kt)) | pf_a | live, ra);
     prefetch_lines(pf_scratch + wave * 512 + 256, (pf_row_b + (uint32_t)(BROW * kt)) | pf_b | live, rb);
   }
-  template <int U>
-  __device__ __forceinline__ void step(lds_u8* cur, lds_u8* nxt, const lds_u8* sread, lds_u8* sdma,
-                                       int64_t kt, int wave, int wm, int wn, int lane, uint32_t* sc_a,
+  // The next step's scales are number q of those at sread; `group` starts the
+  // load of the next group's into sdma.
+  __device__ __forceinline__ void step(lds_u8* cur, lds_u8* nxt, const lds_u8* sread, int q, bool group,
+                                       lds_u8* sdma, int64_t kt, int wave, int wm, int wn, int lane, uint32_t* sc_a,
                                        uint32_t* sc_b, v8i* f0a, v8i* f0b, v8i* f1a, v8i* f1b,
                                        v16f (&acc)[F][F]) {
     uint32_t nx_a[F], nx_b[F];
@@ -211,8 +255,8 @@ struct Tile4 {
     interleave<DS_READS>();
     wait_vm_but_prefetch();
     __syncthreads();
-    if (U == 0) issue_scales(sdma, kt / GS + 1, wave);
-    read_scales(sread, (U + 1) % GS, wm, wn, lane, nx_a, nx_b);
+    if (group) issue_scales(sdma, kt / GS + 1, wave);
+    read_scales(sread, q, kt + 1, wm, wn, lane, nx_a, nx_b);
 #pragma unroll
     for (int f = 0; f < F; f++) {
       f0a[f] = frag_a<0>(nxt, wm, f, lane);
@@ -265,29 +309,29 @@ struct Tile4 {
     __syncthreads();
     uint32_t sc_a[F], sc_b[F];
     v8i f0a[F], f0b[F], f1a[F], f1b[F];
-    read_scales(ss0, 0, wm, wn, lane, sc_a, sc_b);
+    read_scales(ss0, 0, 0, wm, wn, lane, sc_a, sc_b);
     prefetch(2, wave);
     read_frags<0>(st0, wm, wn, lane, f0a, f0b);
-    for (int64_t j = 0; j * GS < nks; j++) {
-      const int64_t kt = j * GS;
+    constexpr int STEPS = WHOLE ? GS : 2;  // whole groups, or pairs: a step past the last adds zeros
+    for (int64_t k0 = 0; k0 < nks; k0 += STEPS) {
+      const int64_t j = k0 / GS;
       lds_u8 *scur = (j & 1) ? ss1 : ss0, *snxt = (j & 1) ? ss0 : ss1;
-      if constexpr (GS == 2) {
-        step<0>(st0, st1, scur, snxt, kt, wave, wm, wn, lane, sc_a, sc_b, f0a, f0b, f1a, f1b, acc);
-        step<1>(st1, st0, snxt, snxt, kt + 1, wave, wm, wn, lane, sc_a, sc_b, f0a, f0b, f1a, f1b, acc);
-      } else {
-        step<0>(st0, st1, scur, snxt, kt, wave, wm, wn, lane, sc_a, sc_b, f0a, f0b, f1a, f1b, acc);
-        step<1>(st1, st0, scur, snxt, kt + 1, wave, wm, wn, lane, sc_a, sc_b, f0a, f0b, f1a, f1b, acc);
-        step<2>(st0, st1, scur, snxt, kt + 2, wave, wm, wn, lane, sc_a, sc_b, f0a, f0b, f1a, f1b, acc);
-        step<3>(st1, st0, snxt, snxt, kt + 3, wave, wm, wn, lane, sc_a, sc_b, f0a, f0b, f1a, f1b, acc);
+#pragma unroll
+      for (int u = 0; u < STEPS; u++) {
+        const int64_t kt = k0 + u;
+        const int q = WHOLE || GS == 2 ? (u + 1) % GS : (int)(kt + 1) % GS;
+        const bool group = WHOLE || GS == 2 ? u == 0 : kt % GS == 0;
+        step(u & 1 ? st1 : st0, u & 1 ? st0 : st1, q == 0 ? snxt : scur, q, group, snxt, kt, wave, wm, wn, lane,
+             sc_a, sc_b, f0a, f0b, f1a, f1b, acc);
       }
     }
   }
 };
 
-// Persistent, K a multiple of 512 and N of 8: one workgroup per compute unit
+// Persistent: one workgroup per compute unit
 // walks tiles bid, bid + grid, ...; a tile's first loads run while the last
 // one's result is stored.
-template <int FA>
+template <int FA, bool WHOLE>
 __global__ void __launch_bounds__(NT)
 gemm4_persistent_kernel(const uint8_t* __restrict__ a, const uint8_t* __restrict__ sa,
                         const uint8_t* __restrict__ b, const uint8_t* __restrict__ sb,
@@ -299,7 +343,7 @@ gemm4_persistent_kernel(const uint8_t* __restrict__ a, const uint8_t* __restrict
   const int64_t nm = (M + BM - 1) / BM, nn = (N + BN - 1) / BN, tiles = nm * nn;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  typedef Tile4<FA> T;
+  typedef Tile4<FA, WHOLE> T;
   auto make = [&](int64_t t, T& tl) {
     int64_t mt, nt;
     tile_of(t, nm, nn, mt, nt);
@@ -337,9 +381,13 @@ gemm4_persistent_kernel(const uint8_t* __restrict__ a, const uint8_t* __restrict
       tl.setup(wave, lane);
       tl.first(wave);
     }
-    store_tile_bf16_lds_halves(acc, (lds_u8*)smem1, c, N, m0, m_end, n0, N, wave & 1, wave >> 1, wave,
-                               lane);
-    stored = true;
+    if constexpr (WHOLE) {
+      store_tile_bf16_lds_halves(acc, (lds_u8*)smem1, c, N, m0, m_end, n0, N, wave & 1, wave >> 1, wave,
+                                 lane);
+      stored = true;
+    } else {
+      store_bf16(acc, c, N, m0 + 128 * (wave & 1), m_end, n0 + 128 * (wave >> 1), lane);
+    }
     if (!more) break;
   }
 }
@@ -347,8 +395,8 @@ gemm4_persistent_kernel(const uint8_t* __restrict__ a, const uint8_t* __restrict
 // Grouped: every workgroup derives the tile list from the device-side offsets
 // (clamped into [0, T] and made non-decreasing, so bad offsets never address
 // outside the operands) and walks it with a static stride, the tiles of a
-// group in the dense kernel's order.  K a multiple of 512, N of 8.
-template <int FA>
+// group in the dense kernel's order.
+template <int FA, bool WHOLE>
 __global__ void __launch_bounds__(NT)
 grouped_gemm4_kernel(int64_t G, const int64_t* __restrict__ offsets, int64_t T_, int64_t N, int64_t K,
                      const uint8_t* __restrict__ a, const uint8_t* __restrict__ sa,
@@ -393,7 +441,7 @@ grouped_gemm4_kernel(int64_t G, const int64_t* __restrict__ offsets, int64_t T_,
       if (s_pre[mid] <= wg) g = mid; else hi = mid;
     }
   }
-  typedef Tile4<FA> T;
+  typedef Tile4<FA, WHOLE> T;
   auto make = [&](int64_t t, T& tl) {
     while (s_pre[g + 1] <= t) g++;  // s_pre[G] = total > t stops it
     const uint32_t local = (uint32_t)(t - s_pre[g]);
@@ -440,25 +488,35 @@ grouped_gemm4_kernel(int64_t G, const int64_t* __restrict__ offsets, int64_t T_,
       tl.setup(wave, lane);
       tl.first(wave);
     }
-    store_tile_bf16_lds_halves(acc, (lds_u8*)smem1, c, N, m0, m_end, n0, N, wave & 1, wave >> 1, wave,
-                               lane);
-    stored = true;
+    if constexpr (WHOLE) {
+      store_tile_bf16_lds_halves(acc, (lds_u8*)smem1, c, N, m0, m_end, n0, N, wave & 1, wave >> 1, wave,
+                                 lane);
+      stored = true;
+    } else {
+      store_bf16(acc, c, N, m0 + 128 * (wave & 1), m_end, n0 + 128 * (wave >> 1), lane);
+    }
     if (!more) break;
   }
 }
 
-// Which kernel: K and N that the pipelined tiles take are whole groups of 16
-// scale bytes, whole 16-byte chunks of a result row and 32-bit offsets within
-// a tile's rows.
-static bool pipelined(int64_t N, int64_t K) {
+// Whole groups of 16 scale bytes, whole 16-byte chunks of a result row and
+// 32-bit offsets within a tile's rows of the result.
+static bool whole(int64_t N, int64_t K) {
   return K % 512 == 0 && N % 8 == 0 && (int64_t)BM * N * 2 < ((int64_t)1 << 31);
 }
 
-// Large tiles from 160 of them on (K = 18432, N = 7168, 8-bit A: 2048 rows, 224
-// tiles, 237 us against 318 in small ones; 1024 rows, 112 tiles, 203 against
-// 163).
+// Large tiles where they are done first: a round of them, a tile on each
+// compute unit, takes 1.5 to 2 times as long as a round of the small ones with
+// half their columns (us, large against small, rounds in brackets, 8-bit A.
+// Whole: 2048 x 7168 x 18432 240 (1) and 318 (2), 4096 x 4352 x 4096 91 (2) and
+// 103 (3), 1024 x 7168 x 18432 203 (1) and 136 (1).  Otherwise: 2048 x 7168 x
+// 18400 380 (1) and 391 (2), 8192 x 8192 x 2880 196 (4) and 268 (8), 4096 x 4130
+// x 2080 79 (2) and 64 (3), 2048 x 18432 x 544 50 (3) and 44 (5)).  Up to 128 rows half a large tile would be empty, and the rounds are
+// as many.  K from 128 on: a row has a whole dword of scales.
 static bool many(int64_t M, int64_t N, int64_t K) {
-  return pipelined(N, K) && ((M + BM - 1) / BM) * ((N + BN - 1) / BN) >= 160;
+  const int64_t large = ((M + BM - 1) / BM) * ((N + BN - 1) / BN);
+  const int64_t small = ((M + 127) / 128) * ((N + 255) / 256);
+  return K >= 128 && 100 * ((large + 255) / 256) <= (whole(N, K) ? 67 : 58) * ((small + 255) / 256);
 }
 
 template <int FA>
@@ -467,8 +525,11 @@ static void launch_many(int64_t M, int64_t N, int64_t K, const uint8_t* a, const
                         hipStream_t stream) {
   const int64_t tiles = ((M + BM - 1) / BM) * ((N + BN - 1) / BN);
   const int64_t cus = (num_cus > 8 ? num_cus : 256) / 8 * 8;
-  hipLaunchKernelGGL((gemm4_persistent_kernel<FA>), dim3((unsigned)(tiles < cus ? tiles : cus)), dim3(NT), 0,
-                     stream, a, sa, b, sb, c, M, N, K);
+  const dim3 grid((unsigned)(tiles < cus ? tiles : cus));
+  if (whole(N, K))
+    hipLaunchKernelGGL((gemm4_persistent_kernel<FA, true>), grid, dim3(NT), 0, stream, a, sa, b, sb, c, M, N, K);
+  else
+    hipLaunchKernelGGL((gemm4_persistent_kernel<FA, false>), grid, dim3(NT), 0, stream, a, sa, b, sb, c, M, N, K);
 }
 
 size_t gemm4_workspace(int64_t M, int64_t N, int64_t K) {
@@ -494,19 +555,25 @@ hipError_t launch_grouped_gemm4(int a_elem, int64_t G, const int64_t* offsets, i
                                 const void* sb, void* c, int num_cus, hipStream_t stream) {
   if (G < 1 || G > MAX_GROUPS) return hipErrorInvalidValue;
   // large tiles from 96 rows a group on (64 groups of 4096 x 4096: 128 rows each
-  // 265 us against 304 in small ones, 78 rows each 255 against 218)
-  if (!pipelined(N, K) || T < 96 * G)
+  // 265 us against 304 in small ones, 78 rows each 255 against 218), and where
+  // rows do not fill the loads from 192 (4096 x 2080: 256 rows each 279 against
+  // 315, 128 rows each 213 against 191)
+  const bool w = whole(N, K);
+  if (K < 128 || T < (w ? 96 : 192) * G)
     return launch_grouped_gemm4_deep(a_elem, G, offsets, T, N, K, a, sa, b, sb, c, stream);
   const int64_t upper = ((T + BM - 1) / BM + G) * ((N + BN - 1) / BN);
   int64_t wgs = ((num_cus > 0 ? num_cus : 256) + 7) / 8 * 8;
   if (upper < wgs) wgs = (upper + 7) / 8 * 8;
-#define MX_GROUPED4(FA_)                                                                          \
-  hipLaunchKernelGGL((grouped_gemm4_kernel<FA_>), dim3((unsigned)wgs), dim3(NT), 0, stream, G, offsets, \
-                     T, N, K, (const uint8_t*)a, (const uint8_t*)sa, (const uint8_t*)b,           \
+#define MX_GROUPED4(FA_, WHOLE_)                                                                  \
+  hipLaunchKernelGGL((grouped_gemm4_kernel<FA_, WHOLE_>), dim3((unsigned)wgs), dim3(NT), 0, stream, G, \
+                     offsets, T, N, K, (const uint8_t*)a, (const uint8_t*)sa, (const uint8_t*)b,  \
                      (const uint8_t*)sb, (uint16_t*)c)
-  if (a_elem == ELEM_E4M3) MX_GROUPED4(ELEM_E4M3);
-  else if (a_elem == ELEM_E5M2) MX_GROUPED4(ELEM_E5M2);
-  else if (a_elem == ELEM_E2M1) MX_GROUPED4(ELEM_E2M1);
+  if (a_elem == ELEM_E4M3 && w) MX_GROUPED4(ELEM_E4M3, true);
+  else if (a_elem == ELEM_E4M3) MX_GROUPED4(ELEM_E4M3, false);
+  else if (a_elem == ELEM_E5M2 && w) MX_GROUPED4(ELEM_E5M2, true);
+  else if (a_elem == ELEM_E5M2) MX_GROUPED4(ELEM_E5M2, false);
+  else if (a_elem == ELEM_E2M1 && w) MX_GROUPED4(ELEM_E2M1, true);
+  else if (a_elem == ELEM_E2M1) MX_GROUPED4(ELEM_E2M1, false);
   else return hipErrorInvalidValue;
 #undef MX_GROUPED4
   return hipGetLastError();

@@ -8,7 +8,6 @@
 // result has fewer tiles than the chip has places, K is split over workgroups
 // whose FP32 sums a second kernel adds in the order of the splits.
 #include "gemm4.h"
-#include "mx_rows.h"
 
 namespace mx {
 
@@ -327,48 +326,6 @@ struct Deep4 {
   __device__ __forceinline__ static v8i low(v8i v) { return (v8i){v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
   __device__ __forceinline__ static v8i high(v8i v) { return (v8i){v[4], v[5], v[6], v[7], 0, 0, 0, 0}; }
 
-  // The result in BF16, any N: lanes l and l + 32 trade groups so that a lane
-  // holds eight consecutive columns (gemm_common.h).
-  __device__ __forceinline__ void store(const v16f (&acc)[FN][FM], uint16_t* __restrict__ c, int wave,
-                                        int lane) const {
-    const int wm = wave % WM, wn = wave / WM, g = lane >> 5, i = lane & 31;
-#pragma unroll
-    for (int fn = 0; fn < FN; fn++)
-#pragma unroll
-      for (int fm = 0; fm < FM; fm++) {
-        const v16f& v = acc[fn][fm];
-        uint32_t p[4][2];
-#pragma unroll
-        for (int r4 = 0; r4 < 4; r4++) {
-          p[r4][0] = cvt_pk_bf16(v[4 * r4 + 0], v[4 * r4 + 1]);
-          p[r4][1] = cvt_pk_bf16(v[4 * r4 + 2], v[4 * r4 + 3]);
-        }
-#pragma unroll
-        for (int h = 0; h < 2; h++)
-#pragma unroll
-          for (int d = 0; d < 2; d++) {
-            const auto s = __builtin_amdgcn_permlane32_swap(p[2 * h][d], p[2 * h + 1][d], false, false);
-            p[2 * h][d] = s[0];
-            p[2 * h + 1][d] = s[1];
-          }
-        const int64_t m = m0 + 32 * FM * wm + 32 * fm + i;
-        if (m >= m_end) continue;
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-          const int64_t n = n0 + 32 * FN * wn + 32 * fn + 16 * h + 8 * g;
-          const uint32_t w[4] = {p[2 * h][0], p[2 * h][1], p[2 * h + 1][0], p[2 * h + 1][1]};
-          uint16_t* dst = c + m * N + n;
-          if (n + 8 <= N) {
-            *(u32x4_at2*)dst = (u32x4_at2){w[0], w[1], w[2], w[3]};
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-              if (n + e < N) dst[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-          }
-        }
-      }
-  }
-
   // The FP32 sums of one split into its share of the workspace, whole tiles in
   // rows of ldw columns: a lane writes groups of four consecutive columns.
   __device__ __forceinline__ void store_partial(const v16f (&acc)[FN][FM], float* __restrict__ ws, int64_t ldw,
@@ -420,7 +377,7 @@ gemm4_deep_kernel(const uint8_t* __restrict__ a, const uint8_t* __restrict__ sa,
   t.setup(wave, lane);
   v16f acc[FN][FM];
   t.run(acc, wave, lane);
-  if (gridDim.y == 1) t.store(acc, c, wave, lane);
+  if (gridDim.y == 1) store_bf16(acc, c, N, t.m0 + 32 * FM * (wave % WM), t.m_end, t.n0 + 32 * FN * (wave / WM), lane);
   else t.store_partial(acc, ws + (int64_t)blockIdx.y * M * ldw, ldw, wave, lane);
 }
 
@@ -475,19 +432,19 @@ grouped4_deep_kernel(const int64_t* __restrict__ offsets, int64_t rows, const ui
     t.setup(wave, lane);
     v16f acc[FN][FM];
     t.run(acc, wave, lane);
-    t.store(acc, c, wave, lane);
+    store_bf16(acc, c, N, t.m0 + 32 * FM * (wave % WM), t.m_end, t.n0 + 32 * FN * (wave / WM), lane);
     __syncthreads();  // every wave is done with the stages
   }
 }
 
 // Which tile, measured at K = 7168 and 18432 with N = 18432 and 7168 (us, 8-bit
 // A).  Up to 32 rows 32 x 128, two workgroups to a compute unit (1 x 18432 x
-// 7168: 15.5, one to a unit 17.0); up to 64 rows 64 x 128 (64 x 18432: 24.2, two
+// 7168: 15.0, one to a unit 17.0); up to 64 rows 64 x 128 (64 x 18432: 22.2, two
 // to a unit 26.3); above, 128 x 128 while its tiles find a unit each (512 x 7168
-// x 18432: 75, against 117 with 128 x 256), 128 x 256 beyond (2048 rows: 318
+// x 18432: 70, against 117 with 128 x 256), 128 x 256 beyond (2048 rows: 318
 // against 361).  K is split so far as workgroups still find a unit each and the
 // steps saved outweigh the second launch and the partial sums' way through
-// memory (1 x 7168 x 18432: 15.6 in four, 31 whole; 1 x 4096 x 4096: 9.8 whole,
+// memory (1 x 7168 x 18432: 15.3 in four, 31 whole; 1 x 4096 x 4096: 9.8 whole,
 // 12.4 in four).
 enum Shape4 { TILE_32, TILE_64, TILE_128, TILE_WIDE };
 

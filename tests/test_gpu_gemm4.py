@@ -56,6 +56,13 @@ def test_gemm4_many_tiles(elem):
 
 
 @pytest.mark.parametrize("elem", ELEMS)
+@pytest.mark.parametrize("N,K", [(3304, 128), (3301, 160), (3304, 544), (3303, 768), (3298, 1024), (3302, 2080)])
+def test_gemm4_many_tiles_of_any_length(elem, N, K):
+    """Rows that end inside a K step, inside a dword of scales, at every parity."""
+    _check(3301, N, K, elem)
+
+
+@pytest.mark.parametrize("elem", ELEMS)
 @pytest.mark.parametrize("M", [1, 20, 300])
 def test_one_hot_rows_give_the_weight(elem, M):
     """One code 1.0 a row: the result is a column of the weight, exactly, at
@@ -168,6 +175,35 @@ def test_grouped_many_tiles(elem):
         r = slice(off[g], off[g + 1])
         if sizes[g]:
             _close(got[r], *P.gemm(a[r], sa[r], b[g], sb[g], elem), K, elem, f"group {g}")
+
+
+@pytest.mark.parametrize("elem", ELEMS)
+@pytest.mark.parametrize("K", [128, 416, 1056, 1312])
+def test_grouped_long_groups_of_any_length(elem, K):
+    off = np.array([0, 300, 300, 811, 1230], np.int64)
+    T, N = 1233, 301
+    a, sa = _operand((T, K), elem, 1)
+    b, sb = _operand((4, N, K), "e2m1", 2)
+    out = torch.full((T, N), -3.0, dtype=torch.bfloat16, device="cuda")
+    got = mx.grouped_gemm4(dev(off), dev(a), dev(sa), dev(b), dev(sb), elem, out=out)
+    for g in (0, 2, 3):
+        r = slice(off[g], off[g + 1])
+        _close(got[r], *P.gemm(a[r], sa[r], b[g], sb[g], elem), K, elem, f"group {g}")
+    assert (got[1230:] == -3.0).all()
+
+
+def test_not_a_number_at_the_end_of_a_row_stays_there():
+    """A row whose last scale is NaN leaves the others as they were."""
+    M, N, K = 3301, 3301, 416
+    a, sa = _operand((M, K), "e4m3", 1)
+    b, sb = _operand((N, K), "e2m1", 2)
+    whole = mx.gemm4(dev(a), dev(sa), dev(b), dev(sb))
+    sa[5, -1] = sb[7, -1] = 255
+    got = mx.gemm4(dev(a), dev(sa), dev(b), dev(sb))
+    nan = torch.zeros((M, N), dtype=torch.bool, device="cuda")
+    nan[5] = nan[:, 7] = True
+    assert torch.isnan(got[nan]).all()
+    assert torch.equal(got[~nan].view(torch.int16), whole[~nan].view(torch.int16))
 
 
 @pytest.mark.parametrize("T", [8, 600])
