@@ -6,7 +6,9 @@
 // Small tiles and many stages: the loads of NS - 1 K steps are in flight, so
 // that a compute unit keeps some 60 KB of the weight on its way.  Where the
 // result has fewer tiles than the chip has places, K is split over workgroups
-// whose FP32 sums a second kernel adds in the order of the splits.
+// whose FP32 sums a second kernel adds in the order of the splits.  One row is
+// bound by the weight's bytes: 151936 x 4096 in 65.5 us (5.05 TB/s), 18432 x
+// 7168 in 15.0 (4.7 TB/s, launch and host included).
 #include "gemm4.h"
 
 namespace mx {
@@ -403,32 +405,67 @@ gemm4_join_kernel(const float* __restrict__ ws, int64_t M, int64_t N, int64_t ld
   }
 }
 
-// Grouped: blockIdx.y is the group, blockIdx.x the column tile; a workgroup
-// takes its group's rows tile by tile.
+// Row tile number `slot` of BMR rows among those of all groups, counted group
+// by group: its group and its rows [m0, m_end).  Offsets are clamped into [0,
+// rows], so that bad ones name rows of [0, rows) only.  False past the last.
+template <int BMR>
+__device__ __forceinline__ bool row_tile(const int64_t* __restrict__ offsets, int64_t G, int64_t rows,
+                                         uint32_t slot, int lane, int64_t& g, int64_t& m0, int64_t& m_end) {
+  uint32_t before = 0;
+  for (int64_t base = 0; base < G; base += 64) {
+    int64_t lo = 0, hi = 0;
+    if (base + lane < G) {
+      lo = offsets[base + lane], hi = offsets[base + lane + 1];
+      lo = lo < 0 ? 0 : (lo > rows ? rows : lo);
+      hi = hi < lo ? lo : (hi > rows ? rows : hi);
+    }
+    const uint32_t n = (uint32_t)((hi - lo + BMR - 1) / BMR);
+    uint32_t sum = n;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const uint32_t y = __shfl_up(sum, d);
+      if (lane >= d) sum += y;
+    }
+    const uint32_t tile = slot - (before + sum - n);
+    const uint64_t hit = __ballot(tile < n);
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      g = base + l;
+      const int64_t end = __shfl(hi, l);
+      m0 = __shfl(lo, l) + (int64_t)__shfl(tile, l) * BMR;
+      m_end = m0 + BMR < end ? m0 + BMR : end;
+      return true;
+    }
+    before += __shfl(sum, 63);
+  }
+  return false;
+}
+
+// Grouped: blockIdx.y is the row tile (and those gridDim.y further on),
+// blockIdx.x the column tile, so that a group with most of the rows has as many
+// workgroups as its tiles (1536 rows, all in one of 64 groups of 4096 x 4096: 49
+// us; 354 where a workgroup took its group's tiles in turn).  128 rows over 64
+// such groups: 90 us, at 4.9 TB/s the weights of the groups that have rows.
 template <int FA, int WM, int WN, int FM, int FN, int KH, bool TWO>
 __global__ void __launch_bounds__(64 * WM * WN)
-grouped4_deep_kernel(const int64_t* __restrict__ offsets, int64_t rows, const uint8_t* __restrict__ a,
-                     const uint8_t* __restrict__ sa, const uint8_t* __restrict__ b,
-                     const uint8_t* __restrict__ sb, uint16_t* __restrict__ c, int64_t N, int64_t K) {
+grouped4_deep_kernel(const int64_t* __restrict__ offsets, int64_t G, int64_t rows,
+                     const uint8_t* __restrict__ a, const uint8_t* __restrict__ sa,
+                     const uint8_t* __restrict__ b, const uint8_t* __restrict__ sb,
+                     uint16_t* __restrict__ c, int64_t N, int64_t K) {
   typedef Deep4<FA, WM, WN, FM, FN, KH, TWO> T;
   __shared__ __attribute__((aligned(16))) uint8_t stages[T::NS * T::STAGE_BYTES];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t g = blockIdx.y;
-  // clamped, so that bad offsets read and write rows of [0, rows) only
-  int64_t lo = offsets[g], hi = offsets[g + 1];
-  lo = lo < 0 ? 0 : (lo > rows ? rows : lo);
-  hi = hi < lo ? lo : (hi > rows ? rows : hi);
   T t;
   t.a = a, t.sa = sa;
-  t.b = b + g * N * (K >> 1), t.sb = sb + g * N * (K >> 5);
   t.n0 = (int64_t)blockIdx.x * T::BNR;
   t.N = N, t.K = K;
   t.kt0 = 0, t.kt1 = (int)((K + T::KS - 1) / T::KS);
   t.st = (lds_u8*)stages;
-  for (int64_t m0 = lo; m0 < hi; m0 += T::BMR) {
-    t.m0 = m0;
-    t.m_end = m0 + T::BMR < hi ? m0 + T::BMR : hi;
+  for (uint32_t slot = blockIdx.y;; slot += gridDim.y) {
+    int64_t g;
+    if (!row_tile<T::BMR>(offsets, G, rows, slot, lane, g, t.m0, t.m_end)) break;
+    t.b = b + g * N * (K >> 1), t.sb = sb + g * N * (K >> 5);
     t.setup(wave, lane);
     v16f acc[FN][FM];
     t.run(acc, wave, lane);
@@ -518,15 +555,18 @@ template <int FA>
 static void launch_grouped_deep(int64_t G, const int64_t* offsets, int64_t T, int64_t N, int64_t K,
                                 const uint8_t* a, const uint8_t* sa, const uint8_t* b, const uint8_t* sb,
                                 uint16_t* c, hipStream_t stream) {
-  const dim3 grid((unsigned)((N + 127) / 128), (unsigned)G);
   // 64 groups of 4096 x 4096: 16 rows each 129 us in tiles of 32 rows, 157 in
   // 128; 62 rows each 262 and 199
-  if (T <= 24 * G)
-    hipLaunchKernelGGL((grouped4_deep_kernel<FA, 1, 4, 1, 1, 2, true>), grid, dim3(256), 0, stream, offsets, T, a,
-                       sa, b, sb, c, N, K);
+  const bool few = T <= 24 * G;
+  // no more row tiles than this: each group ends in at most one that is short
+  const int64_t slots = T / (few ? 32 : 128) + G;
+  const dim3 grid((unsigned)((N + 127) / 128), (unsigned)(slots < 65535 ? slots : 65535));
+  if (few)
+    hipLaunchKernelGGL((grouped4_deep_kernel<FA, 1, 4, 1, 1, 2, true>), grid, dim3(256), 0, stream, offsets, G, T,
+                       a, sa, b, sb, c, N, K);
   else
     hipLaunchKernelGGL((grouped4_deep_kernel<FA, 2, 2, 2, 2, 1, FA != ELEM_E2M1>), grid, dim3(256), 0, stream,
-                       offsets, T, a, sa, b, sb, c, N, K);
+                       offsets, G, T, a, sa, b, sb, c, N, K);
 }
 
 hipError_t launch_grouped_gemm4_deep(int a_elem, int64_t G, const int64_t* offsets, int64_t T,

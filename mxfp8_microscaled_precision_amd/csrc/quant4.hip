@@ -8,7 +8,9 @@
 // step-2 environment table, ENABLE_MXFP4_QAT; practice page, w4a8-mx).
 //
 // All kernels are bound by HBM: x is read once, every output byte is written
-// once.
+// once.  Measured at 18432 x 7168: rows 52 us (6.4 TB/s), columns 67 (5.0), both
+// 84 (4.8; its writes go four ways); back to BF16 51 us from E2M1 and 60 from
+// E4M3 (6.5 and 6.7).
 #include "mx_columns.h"
 #include "mx_device.h"
 #include "mx_kernels.h"

@@ -11,7 +11,12 @@
 // element leave little time for each, so the column maxima are reduced by
 // halving (column_max8: 16 instructions for 16 columns instead of a butterfly
 // of all), each scale is formed in one lane, and the lanes that need it read
-// it back from LDS as a BF16 factor.
+// it back from LDS as a BF16 factor.  Measured at 131072 x 4096: 238 us dense
+// and 247 in 64 groups (4.7 and 4.5 TB/s; 361 with a butterfly for every column
+// and the scales formed by all lanes).  What is left of the gap to a copy's rate
+// is the vector unit, busy 46% of the time, and the latency between the load,
+// the exchange and the store of a tile.  Tiles dealt to the XCDs in contiguous
+// parts: 238 us in groups, but 292 dense.
 #include "mx_columns.h"
 #include "mx_device.h"
 #include "mx_kernels.h"

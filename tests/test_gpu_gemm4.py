@@ -192,6 +192,35 @@ def test_grouped_long_groups_of_any_length(elem, K):
     assert (got[1230:] == -3.0).all()
 
 
+@pytest.mark.parametrize("elem", ["e4m3", "e2m1"])
+@pytest.mark.parametrize("T", [150, 700])
+def test_grouped_one_group_has_most_rows(elem, T):
+    """Many row tiles of one group, none of most others, more than 64 groups."""
+    G, N, K = 70, 140, 288
+    sizes = np.zeros(G, np.int64)
+    sizes[[2, 66, 69]] = 3, T - 5, 2
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int64)
+    a, sa = _operand((T, K), elem, 1)
+    b, sb = _operand((G, N, K), "e2m1", 2)
+    got = mx.grouped_gemm4(dev(off), dev(a), dev(sa), dev(b), dev(sb), elem)
+    for g in (2, 66, 69):
+        r = slice(off[g], off[g + 1])
+        _close(got[r], *P.gemm(a[r], sa[r], b[g], sb[g], elem), K, elem, f"group {g}")
+
+
+def test_grouped_more_row_tiles_than_a_grid_takes():
+    """Ones times ones over 65600 tiles of 128 rows: every row is 32."""
+    T = 128 * 65600
+    a = torch.full((T, 32), 0x38, dtype=torch.uint8, device="cuda")
+    s = torch.full((T, 1), 127, dtype=torch.uint8, device="cuda")
+    b = torch.full((2, 3, 16), 0x22, dtype=torch.uint8, device="cuda")
+    sb = torch.full((2, 3, 1), 127, dtype=torch.uint8, device="cuda")
+    sb[1] = 128                                   # the second group's weight is 2
+    off = dev(np.array([0, T - 1000, T], np.int64))
+    c = mx.grouped_gemm4(off, a, s, b, sb)
+    assert (c[:T - 1000] == 32).all() and (c[T - 1000:] == 64).all()
+
+
 def test_not_a_number_at_the_end_of_a_row_stays_there():
     """A row whose last scale is NaN leaves the others as they were."""
     M, N, K = 3301, 3301, 416
