@@ -560,12 +560,18 @@ hipError_t launch_grouped_gemm4(int a_elem, int64_t G, const int64_t* offsets, i
                                 int64_t K, const void* a, const void* sa, const void* b,
                                 const void* sb, void* c, int num_cus, hipStream_t stream) {
   if (G < 1 || G > MAX_GROUPS) return hipErrorInvalidValue;
-  // large tiles from 96 rows a group on (64 groups of 4096 x 4096: 128 rows each
-  // 265 us against 304 in small ones, 78 rows each 255 against 218), and where
-  // rows do not fill the loads from 192 (4096 x 2080: 256 rows each 279 against
-  // 315, 128 rows each 213 against 191)
+  // Large tiles from 96 rows a group on (us, large against small, 64 groups of
+  // 4096 x 4096: 128 rows each 267 and 261 with an 8-bit A, 187 and 234 with a
+  // 4-bit one, 192 rows each 284 and 339, 78 rows each 255 and 205), where rows do
+  // not fill the loads from 192 (4096 x 2080: 256 rows each 260 and 263, with a
+  // 4-bit A 192 rows each 156 and 222, 128 rows each 213 and 165); and from 150
+  // tiles on, with half a tile empty in each group (8 groups of N x 4096: 157 tiles
+  // 46 and 54, 114 tiles 47 and 35; one group: 258 tiles 54 and 83, 70 tiles 44 and
+  // 24), where rows do not fill the loads from 256 (8 groups of 4096 x 2880: 189
+  // tiles 51 and 42)
   const bool w = whole(N, K);
-  if (K < 128 || T < (w ? 96 : 192) * G)
+  const int64_t halves = (2 * T / BM + G) * ((N + BN - 1) / BN);
+  if (K < 128 || T < (w ? 96 : 192) * G || halves < 2 * (w ? 150 : 256))
     return launch_grouped_gemm4_deep(a_elem, G, offsets, T, N, K, a, sa, b, sb, c, stream);
   const int64_t upper = ((T + BM - 1) / BM + G) * ((N + BN - 1) / BN);
   int64_t wgs = ((num_cus > 0 ? num_cus : 256) + 7) / 8 * 8;

@@ -556,7 +556,7 @@ static void launch_grouped_deep(int64_t G, const int64_t* offsets, int64_t T, in
                                 const uint8_t* a, const uint8_t* sa, const uint8_t* b, const uint8_t* sb,
                                 uint16_t* c, hipStream_t stream) {
   // 64 groups of 4096 x 4096: 16 rows each 129 us in tiles of 32 rows, 157 in
-  // 128; 62 rows each 262 and 199
+  // 128; 62 rows each 262 and 194
   const bool few = T <= 24 * G;
   // no more row tiles than this: each group ends in at most one that is short
   const int64_t slots = T / (few ? 32 : 128) + G;

@@ -180,16 +180,31 @@ def test_grouped_many_tiles(elem):
 @pytest.mark.parametrize("elem", ELEMS)
 @pytest.mark.parametrize("K", [128, 416, 1056, 1312])
 def test_grouped_long_groups_of_any_length(elem, K):
-    off = np.array([0, 300, 300, 811, 1230], np.int64)
-    T, N = 1233, 301
+    rng = np.random.default_rng(K)
+    sizes = rng.integers(100, 700, 12)
+    sizes[5] = 0
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int64)
+    T, N, G = int(off[-1]) + 3, 2603, len(sizes)
     a, sa = _operand((T, K), elem, 1)
-    b, sb = _operand((4, N, K), "e2m1", 2)
+    b, sb = _operand((G, N, K), "e2m1", 2)
     out = torch.full((T, N), -3.0, dtype=torch.bfloat16, device="cuda")
     got = mx.grouped_gemm4(dev(off), dev(a), dev(sa), dev(b), dev(sb), elem, out=out)
-    for g in (0, 2, 3):
+    for g in range(G):
         r = slice(off[g], off[g + 1])
-        _close(got[r], *P.gemm(a[r], sa[r], b[g], sb[g], elem), K, elem, f"group {g}")
-    assert (got[1230:] == -3.0).all()
+        if sizes[g]:
+            _close(got[r], *P.gemm(a[r], sa[r], b[g], sb[g], elem), K, elem, f"group {g}")
+    assert (got[T - 3:] == -3.0).all()
+
+
+@pytest.mark.parametrize("K", [512, 544])
+def test_grouped_large_with_bad_offsets_stays_in_bounds(K):
+    T, N = 6000, 2600
+    a, sa = _operand((T, K), "e4m3", 1)
+    b, sb = _operand((3, N, K), "e2m1", 2)
+    guard = torch.full((T + 300, N), -3.0, dtype=torch.bfloat16, device="cuda")
+    for off in ([0, T + 900, 2, T], [-5, 3, 1 << 40, T], [T, 1, 0, T]):
+        mx.grouped_gemm4(dev(np.array(off, np.int64)), dev(a), dev(sa), dev(b), dev(sb), out=guard[:T])
+        assert (guard[T:] == -3.0).all()
 
 
 @pytest.mark.parametrize("elem", ["e4m3", "e2m1"])
