@@ -331,7 +331,7 @@ struct Tile4 {
 // Persistent: one workgroup per compute unit
 // walks tiles bid, bid + grid, ...; a tile's first loads run while the last
 // one's result is stored.  Bound by the matrix unit and the power it may draw:
-// 32768 x 18432 x 7168 with both operands in 4 bits takes 1.98 to 2.06 ms (4.2
+// 32768 x 18432 x 7168 with both operands in 4 bits takes 1.98 to 2.14 ms (4.0
 // to 4.4 PFLOP/s), the unit busy 60% of the time at a clock of 1.54 GHz.  Rows
 // that end off a K step of 128 elements cost more (2048 x 7168 x 18432 240 us,
 // x 18304 298, x 18400, whose rows begin inside a line, 380).
@@ -400,7 +400,7 @@ gemm4_persistent_kernel(const uint8_t* __restrict__ a, const uint8_t* __restrict
 // (clamped into [0, T] and made non-decreasing, so bad offsets never address
 // outside the operands) and walks it with a static stride, the tiles of a
 // group in the dense kernel's order.  131072 tokens over 64 experts of
-// 4096 x 4096, 8-bit A: 1.86 ms (2.36 PFLOP/s), the matrix unit busy 63% of the
+// 4096 x 4096, 8-bit A: 1.81 to 1.92 ms (2.3 to 2.4 PFLOP/s), the matrix unit busy 63% of the
 // time at 1.79 GHz.
 template <int FA, bool WHOLE>
 __global__ void __launch_bounds__(NT)
