@@ -446,7 +446,7 @@ size_t mx_grad_norm_workspace_size(int64_t n);
  * value of it NaN, and payload 0x77.
  *
  * Payload and BF16 pointers of these calls must be 16-byte aligned
- * (MX_ERR_INVALID_ARG).
+ * (MX_ERR_INVALID_ARG); scales may stand at any address.
  * ------------------------------------------------------------------------- */
 
 /* Dynamic MX quantisation to E2M1 of `batch` contiguous BF16 [rows, cols]

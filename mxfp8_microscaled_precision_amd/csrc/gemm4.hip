@@ -31,10 +31,11 @@ namespace mx {
 // 2 S + g and 4 + 2 S + g) and B's lane half g the block 2 g + S (chunk 2 g +
 // S).
 //
-// WHOLE: K is a multiple of 512 and N of 8.  Otherwise chunks past the end of a
-// row are not loaded (they read as zero), the scales are loaded in dwords, the
-// last one of a row ending with the row, and the result leaves in pieces of 16
-// bytes at any address.
+// WHOLE: K is a multiple of 512 and N of 8, and the scales begin at 16-byte
+// addresses.  Otherwise chunks past the end of a row are not loaded (they read
+// as zero), the scales are loaded in dwords at any address, the last one of a
+// row ending with the row, and the result leaves in pieces of 16 bytes at any
+// address.
 template <int FA, bool WHOLE>
 struct Tile4 {
   static constexpr int F = 4;
@@ -511,6 +512,13 @@ static bool whole(int64_t N, int64_t K) {
   return K % 512 == 0 && N % 8 == 0 && (int64_t)BM * N * 2 < ((int64_t)1 << 31);
 }
 
+// Scales may begin at any address; the whole form loads them 16 bytes at a time.
+// (A row of it has a multiple of 16, so the first row's address decides.)  The
+// choice of the tiles goes by sizes alone, as the workspace does.
+static bool whole_scales(const void* sa, const void* sb) {
+  return (((uintptr_t)sa | (uintptr_t)sb) & 15) == 0;
+}
+
 // Large tiles where they are done first: a round of them, a tile on each
 // compute unit, takes 1.5 to 2 times as long as a round of the small ones with
 // half their columns (us, large against small, rounds in brackets, 8-bit A.
@@ -532,7 +540,7 @@ static void launch_many(int64_t M, int64_t N, int64_t K, const uint8_t* a, const
   const int64_t tiles = ((M + BM - 1) / BM) * ((N + BN - 1) / BN);
   const int64_t cus = (num_cus > 8 ? num_cus : 256) / 8 * 8;
   const dim3 grid((unsigned)(tiles < cus ? tiles : cus));
-  if (whole(N, K))
+  if (whole(N, K) && whole_scales(sa, sb))
     hipLaunchKernelGGL((gemm4_persistent_kernel<FA, true>), grid, dim3(NT), 0, stream, a, sa, b, sb, c, M, N, K);
   else
     hipLaunchKernelGGL((gemm4_persistent_kernel<FA, false>), grid, dim3(NT), 0, stream, a, sa, b, sb, c, M, N, K);
@@ -569,10 +577,11 @@ hipError_t launch_grouped_gemm4(int a_elem, int64_t G, const int64_t* offsets, i
   // 46 and 54, 114 tiles 47 and 35; one group: 258 tiles 54 and 83, 70 tiles 44 and
   // 24), where rows do not fill the loads from 256 (8 groups of 4096 x 2880: 189
   // tiles 51 and 42)
-  const bool w = whole(N, K);
+  bool w = whole(N, K);
   const int64_t halves = (2 * T / BM + G) * ((N + BN - 1) / BN);
   if (K < 128 || T < (w ? 96 : 192) * G || halves < 2 * (w ? 150 : 256))
     return launch_grouped_gemm4_deep(a_elem, G, offsets, T, N, K, a, sa, b, sb, c, stream);
+  w = w && whole_scales(sa, sb);
   const int64_t upper = ((T + BM - 1) / BM + G) * ((N + BN - 1) / BN);
   int64_t wgs = ((num_cus > 0 ? num_cus : 256) + 7) / 8 * 8;
   if (upper < wgs) wgs = (upper + 7) / 8 * 8;
