@@ -42,7 +42,7 @@ swiglu_quant_kernel(const uint16_t* __restrict__ x, uint32_t n8, uint32_t nchunk
   if (c >= nchunks) return;
   const uint32_t row = c / n8, k = c - row * n8;
   const int64_t F = 8 * (int64_t)n8;
-  const uint16_t* src = x + (int64_t)row * 2 * F + 8 * k;
+  const uint16_t* src = x + (int64_t)row * 2 * F + 8 * (int64_t)k;
   const uint4 vg = load_stream16(src), vu = load_stream16(src + F);
   float g[8], u[8], h[8];
   unpack8(as_vec(vg), g);
@@ -57,7 +57,7 @@ swiglu_quant_kernel(const uint16_t* __restrict__ x, uint32_t n8, uint32_t nchunk
   if (CKPT) {
     const uint32_t sg = scale_byte_t<CE>(quad_max(chunk_absmax(vg)));
     const uint32_t su = scale_byte_t<CE>(quad_max(chunk_absmax(vu)));
-    const int64_t at = (int64_t)row * 2 * F + 8 * k;
+    const int64_t at = (int64_t)row * 2 * F + 8 * (int64_t)k;
     *(uint2*)(cq + at) = cvt8_t<CE>(vg, sg);
     *(uint2*)(cq + at + F) = cvt8_t<CE>(vu, su);
     if ((k & 3) == 0) {
@@ -78,7 +78,7 @@ swiglu_backward_kernel(const uint16_t* __restrict__ dh, const uint8_t* __restric
   if (c >= nchunks) return;
   const uint32_t row = c / n8, k = c - row * n8;
   const int64_t F = 8 * (int64_t)n8;
-  const int64_t at = (int64_t)row * 2 * F + 8 * k;
+  const int64_t at = (int64_t)row * 2 * F + 8 * (int64_t)k;
   const u32x2 wg = __builtin_nontemporal_load((const u32x2*)(cq + at));
   const u32x2 wu = __builtin_nontemporal_load((const u32x2*)(cq + at + F));
   const uint4 vd = load_stream16(dh + 8 * (int64_t)c);
