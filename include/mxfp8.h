@@ -489,7 +489,8 @@ size_t mx_gemm4_workspace_size(mx_elem_type a_elem, int64_t M, int64_t N, int64_
 
 /* mx_gemm4 over per-expert token groups: rows offsets[g] .. offsets[g+1] - 1
  * of c are those of a times b[g]^T, b [G, N, K/2], sb [G, N, K/32].  offsets:
- * DEVICE int64 [G+1] as in mx_grouped_gemm; rows from offsets[G] on are left
+ * DEVICE int64 [G+1] as in mx_grouped_gemm (a bad one below the one before it
+ * counts as that one, so that no row has two groups); rows of no group are left
  * as they were.  Requires 1 <= G <= 512 besides mx_gemm4's rules. */
 mx_status mx_grouped_gemm4(mx_elem_type a_elem, int64_t G, const int64_t* offsets, int64_t T,
                            int64_t N, int64_t K, const void* a, const void* sa, const void* b,

@@ -10,6 +10,7 @@
 // bound by the weight's bytes: 151936 x 4096 in 65.5 us (5.05 TB/s), 18432 x
 // 7168 in 15.0 (4.7 TB/s, launch and host included).
 #include "gemm4.h"
+#include "mx_columns.h"
 
 namespace mx {
 
@@ -407,19 +408,33 @@ gemm4_join_kernel(const float* __restrict__ ws, int64_t M, int64_t N, int64_t ld
 
 // Row tile number `slot` of BMR rows among those of all groups, counted group
 // by group: its group and its rows [m0, m_end).  Offsets are clamped into [0,
-// rows], so that bad ones name rows of [0, rows) only.  False past the last.
+// rows] and made non-decreasing, as the large tiles do: bad ones name rows of
+// [0, rows) only, no row twice, and no more tiles than good ones.  False past
+// the last.
 template <int BMR>
 __device__ __forceinline__ bool row_tile(const int64_t* __restrict__ offsets, int64_t G, int64_t rows,
                                          uint32_t slot, int lane, int64_t& g, int64_t& m0, int64_t& m_end) {
   uint32_t before = 0;
+  int64_t top = 0;  // the largest offset so far
+  int64_t next_lo = 0, next_hi = 0;
+  if (lane < G) next_lo = offsets[lane], next_hi = offsets[lane + 1];
   for (int64_t base = 0; base < G; base += 64) {
-    int64_t lo = 0, hi = 0;
-    if (base + lane < G) {
-      lo = offsets[base + lane], hi = offsets[base + lane + 1];
-      lo = lo < 0 ? 0 : (lo > rows ? rows : lo);
-      hi = hi < lo ? lo : (hi > rows ? rows : hi);
+    const bool in = base + lane < G;
+    int64_t lo = next_lo, hi = next_hi;
+    if (base + 64 + lane < G) next_lo = offsets[base + 64 + lane], next_hi = offsets[base + 65 + lane];
+    lo = lo < 0 ? 0 : (lo > rows ? rows : lo);
+    hi = hi < 0 ? 0 : (hi > rows ? rows : hi);
+    if (__any(in && (lo < top || hi < lo))) {  // running maxima, where some offset is smaller
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const int64_t y = __shfl_up(lo, d);
+        if (lane >= d && y > lo) lo = y;
+      }
+      lo = lo < top ? top : lo;
+      hi = hi < lo ? lo : hi;
     }
-    const uint32_t n = (uint32_t)((hi - lo + BMR - 1) / BMR);
+    top = readlane64(lo, 63);  // (a part that is not full is the last)
+    const uint32_t n = in ? (uint32_t)((hi - lo + BMR - 1) / BMR) : 0;
     uint32_t sum = n;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
@@ -436,7 +451,7 @@ __device__ __forceinline__ bool row_tile(const int64_t* __restrict__ offsets, in
       m_end = m0 + BMR < end ? m0 + BMR : end;
       return true;
     }
-    before += __shfl(sum, 63);
+    before += (uint32_t)__builtin_amdgcn_readlane((int)sum, 63);
   }
   return false;
 }

@@ -51,3 +51,26 @@ def test_grouped_scales_at_any_address(rows, N, K, elem, shift_a, shift_b):
     want = mx.grouped_gemm4(off, a, _at(sa, 0), b, _at(sb, 0), elem)
     got = mx.grouped_gemm4(off, a, _at(sa, shift_a), b, _at(sb, shift_b), elem)
     assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("elem", ["e4m3", "e2m1"])
+@pytest.mark.parametrize("T,G,N,K", [(40, 5, 70, 96), (150, 70, 140, 288), (1500, 12, 140, 288), (1500, 135, 40, 288),
+                                     (6000, 9, 2600, 512)])
+def test_bad_offsets_count_as_their_running_maximum(T, G, N, K, elem):
+    """Offsets that fall, or lie outside [0, T], name the rows that their running
+    maximum within [0, T] names, in every form: each row once."""
+    rng = np.random.default_rng(T + G)
+    a, sa = (dev(t) for t in _operand((T, K), elem, 1))
+    b, sb = (dev(t) for t in _operand((G, N, K), "e2m1", 2))
+    for trial in range(6):
+        off = np.sort(rng.integers(0, T + 1, G + 1))
+        at = rng.integers(0, G + 1, 1 + G // 8)
+        off[at] = rng.integers(-T, 2 * T, len(at)) if trial < 4 else rng.choice([0, T, -1 << 60, 1 << 60], len(at))
+        if trial == 5:
+            off[::2] = 0                          # every group falls back to the first row
+        good = np.maximum.accumulate(np.clip(off, 0, T))
+        want, got = (torch.full((T, N), -3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        mx.grouped_gemm4(dev(good), a, sa, b, sb, elem, out=want)
+        mx.grouped_gemm4(dev(off), a, sa, b, sb, elem, out=got)
+        assert torch.equal(got.view(torch.int16), want.view(torch.int16)), trial
+        assert (got[good[-1]:] == -3.0).all() and (got[:good[0]] == -3.0).all()
