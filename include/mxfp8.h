@@ -503,7 +503,7 @@ mx_status mx_grouped_gemm4(mx_elem_type a_elem, int64_t G, const int64_t* offset
  *   mx_quant_elem(MX_QUANT_ROW_1x32, elem) of h, the down product's operand.
  *   ckpt_q [T, 2F], ckpt_s [T, 2F/32]: x itself in row blocks of ckpt_elem,
  *   the 8-bit checkpoint for the backward pass; both NULL for none.
- * Where sigmoid(g) is below 2^-126 it counts as 0.  Requires F % 32 == 0, F <
+ * Where sigmoid(g) is below 2^-240 it may count as 0.  Requires F % 32 == 0, F <
  * 2^33.  T == 0 or F == 0 is a no-op. */
 mx_status mx_swiglu_quant(mx_elem_type elem, mx_elem_type ckpt_elem, const void* x, int64_t T,
                           int64_t F, void* q, void* s, void* ckpt_q, void* ckpt_s,

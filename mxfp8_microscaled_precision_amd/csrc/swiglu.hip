@@ -10,10 +10,11 @@
 //
 // The kernels are bound by HBM.  A lane takes eight columns: 16 bytes of the
 // gates and 16 of the up values, four lanes to a block of 32, so that a block's
-// maximum needs two lane exchanges and all eight waves fit a SIMD (29 to 47
+// maximum needs two lane exchanges and all eight waves fit a SIMD (25 to 36
 // registers).  Measured at 131072 x 2048 (E4M3): forward 217 us without the
-// checkpoint (6.2 TB/s) and 328 with it (5.8); backward 349 us to BF16 (6.2) and
-// 308 quantised (5.3).  One token of 18432: 8.8 us, the host's calls.
+// checkpoint (6.2 TB/s) and 328 with it (5.8); backward 340 us to BF16 (6.4) and
+// 315 quantised (5.2).  One token of 18432: 8.8 us, the host's calls.
+#include "mx_columns.h"
 #include "mx_device.h"
 #include "mx_kernels.h"
 #include "mx_rows.h"
@@ -22,11 +23,62 @@ namespace mx {
 
 constexpr int ACT_THREADS = 256;
 
-// sig(g) with no overflow: t = exp(-|g|) <= 1
-__device__ __forceinline__ float sigmoid(float g) {
-  const float t = __expf(-fabsf(g));
-  const float r = __builtin_amdgcn_rcpf(1.0f + t);
-  return g >= 0.0f ? r : t * r;
+// sig(g) = p t with no overflow: exp(-|g|) <= 1.  FP32's normal values end near
+// sig(-87), but a product with the up value or the gradient need not: below -80
+// the sigmoid keeps exp(-80) in p and the rest in t, which the caller multiplies
+// last.  Values are formed without t (which is 1) first, and once more in a wave
+// that has such a gate (the quantised gradient below 315 us; 325 where a wave takes
+// one of two forms).
+constexpr float DEEP_GATE = -80.0f;
+struct Sigmoid {
+  float p, t;
+};
+template <bool DEEP>
+__device__ __forceinline__ Sigmoid sigmoid(float g) {
+  const float x = DEEP ? fmaxf(-fabsf(g), DEEP_GATE) : -fabsf(g);
+  const float e = __expf(x);
+  const float r = __builtin_amdgcn_rcpf(1.0f + e);
+  Sigmoid s = {g >= 0.0f ? r : e * r, 1.0f};
+  if (DEEP && g < DEEP_GATE) {
+    const float t = __expf(g - DEEP_GATE);
+    // from 2^-241 on it counts as 0, whatever the gate's size
+    if (t == 0.0f) s.p = 0.0f;
+    else s.t = t;
+  }
+  return s;
+}
+
+// Whether some lane of the wave has a gate below DEEP_GATE, by its eight gates'
+// BF16 bits (a NaN with its sign bit set may count as one).
+__device__ __forceinline__ bool any_deep(uint4 gates) {
+  constexpr uint32_t DEEP_BITS = 0xC2A0;  // -80
+  const uint32_t m = pk_max(pk_max(gates.x, gates.y), pk_max(gates.z, gates.w));
+  return __any((m & 0xFFFFu) > DEEP_BITS || (m >> 16) > DEEP_BITS);
+}
+
+template <bool DEEP>
+__device__ __forceinline__ void swiglu8(const float g[8], const float u[8], float h[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const Sigmoid s = sigmoid<DEEP>(g[i]);
+    h[i] = g[i] * s.p * u[i];
+    if (DEEP) h[i] *= s.t;
+  }
+}
+
+template <bool DEEP>
+__device__ __forceinline__ void swiglu_backward8(const float g[8], const float u[8], const float d[8],
+                                                 float dg[8], float du[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const Sigmoid s = sigmoid<DEEP>(g[i]);
+    const float p = s.p;
+    // p (1 + g (1 - p)) lies in -0.1 .. 1.1 and |g p| <= |g|, whatever finite g is
+    // (below DEEP_GATE p is 2^-115, and 1 - p as good as 1 - p t)
+    dg[i] = d[i] * (u[i] * (p * (1.0f + g[i] * (1.0f - p))));
+    du[i] = d[i] * (g[i] * p);
+    if (DEEP) dg[i] *= s.t, du[i] *= s.t;
+  }
 }
 
 __device__ __forceinline__ uint4 as_uint4(u32x4 v) { return make_uint4(v.x, v.y, v.z, v.w); }
@@ -47,8 +99,8 @@ swiglu_quant_kernel(const uint16_t* __restrict__ x, uint32_t n8, uint32_t nchunk
   float g[8], u[8], h[8];
   unpack8(as_vec(vg), g);
   unpack8(as_vec(vu), u);
-#pragma unroll
-  for (int i = 0; i < 8; i++) h[i] = g[i] * sigmoid(g[i]) * u[i];
+  swiglu8<false>(g, u, h);
+  if (__builtin_expect(any_deep(vg), 0)) swiglu8<true>(g, u, h);
   const uint4 vh = as_uint4(pack8(h));
   // a row's quads are whole: n8 is a multiple of 4, and so is nchunks
   const uint32_t sb = scale_byte_t<EL>(quad_max(chunk_absmax(vh)));
@@ -84,17 +136,16 @@ swiglu_backward_kernel(const uint16_t* __restrict__ dh, const uint8_t* __restric
   const uint4 vd = load_stream16(dh + 8 * (int64_t)c);
   const uint32_t sg = cs[at >> 5], su = cs[(at + F) >> 5];
   float g[8], u[8], d[8], dg[8], du[8];
-  unpack8(as_vec(decode8_t<CE>(make_uint2(wg.x, wg.y), sg)), g);
+  const uint4 vg = decode8_t<CE>(make_uint2(wg.x, wg.y), sg);
+  unpack8(as_vec(vg), g);
   unpack8(as_vec(decode8_t<CE>(make_uint2(wu.x, wu.y), su)), u);
   unpack8(as_vec(vd), d);
-#pragma unroll
-  for (int i = 0; i < 8; i++) {
-    const float p = sigmoid(g[i]);
-    // p (1 + g (1 - p)) lies in -0.1 .. 1.1 and |g p| <= |g|, whatever g is
-    dg[i] = d[i] * (u[i] * (p * (1.0f + g[i] * (1.0f - p))));
-    du[i] = d[i] * (g[i] * p);
+  swiglu_backward8<false>(g, u, d, dg, du);
+  u32x4 og = pack8(dg), ou = pack8(du);
+  if (__builtin_expect(any_deep(vg), 0)) {
+    swiglu_backward8<true>(g, u, d, dg, du);
+    og = pack8(dg), ou = pack8(du);
   }
-  const u32x4 og = pack8(dg), ou = pack8(du);
   if (OUT < 0) {
     __builtin_nontemporal_store(og, (u32x4*)(dx + at));
     __builtin_nontemporal_store(ou, (u32x4*)(dx + at + F));
