@@ -12,8 +12,8 @@
 // gates and 16 of the up values, four lanes to a block of 32, so that a block's
 // maximum needs two lane exchanges and all eight waves fit a SIMD (25 to 36
 // registers).  Measured at 131072 x 2048 (E4M3): forward 217 us without the
-// checkpoint (6.2 TB/s) and 328 with it (5.8); backward 340 us to BF16 (6.4) and
-// 315 quantised (5.2).  One token of 18432: 8.8 us, the host's calls.
+// checkpoint (6.2 TB/s) and 328 with it (5.8); backward 346 us to BF16 (6.3) and
+// 313 quantised (5.3).  One token of 18432: 8.8 us, the host's calls.
 #include "mx_columns.h"
 #include "mx_device.h"
 #include "mx_kernels.h"
@@ -27,8 +27,8 @@ constexpr int ACT_THREADS = 256;
 // sig(-87), but a product with the up value or the gradient need not: below -80
 // the sigmoid keeps exp(-80) in p and the rest in t, which the caller multiplies
 // last.  Values are formed without t (which is 1) first, and once more in a wave
-// that has such a gate (the quantised gradient below 315 us; 325 where a wave takes
-// one of two forms).
+// that has such a gate (the quantised gradient in 313 us; 325 where a wave takes one
+// of two forms, 323 with half of every product).
 constexpr float DEEP_GATE = -80.0f;
 struct Sigmoid {
   float p, t;
@@ -56,6 +56,18 @@ __device__ __forceinline__ bool any_deep(uint4 gates) {
   return __any((m & 0xFFFFu) > DEEP_BITS || (m >> 16) > DEEP_BITS);
 }
 
+// Whether some lane of the wave needs the form with t for the gradient: for a
+// gate, or for an up value of 1.875 2^127 or more, whose product with p (1 + g (1
+// - p)), up to 1.1, may pass FP32's end before the gradient makes it smaller.
+// The blocks' scales tell most waves that they have neither.
+template <int CE>
+__device__ __forceinline__ bool any_far(uint32_t gate_scale, uint32_t up_scale, uint4 gates) {
+  constexpr uint32_t first = CE == ELEM_E5M2 ? 118 : 125;  // largest finite value 112; 56 with one less
+  constexpr uint32_t end = CE == ELEM_E5M2 ? 240 : 247;    // largest values of 2^128; 1.75 2^127 with one less
+  if (!__any(gate_scale >= first || up_scale >= end)) return false;
+  return any_deep(gates) || __any(up_scale >= end);
+}
+
 template <bool DEEP>
 __device__ __forceinline__ void swiglu8(const float g[8], const float u[8], float h[8]) {
 #pragma unroll
@@ -75,9 +87,10 @@ __device__ __forceinline__ void swiglu_backward8(const float g[8], const float u
     const float p = s.p;
     // p (1 + g (1 - p)) lies in -0.1 .. 1.1 and |g p| <= |g|, whatever finite g is
     // (below DEEP_GATE p is 2^-115, and 1 - p as good as 1 - p t)
-    dg[i] = d[i] * (u[i] * (p * (1.0f + g[i] * (1.0f - p))));
+    const float f = p * (1.0f + g[i] * (1.0f - p));
+    dg[i] = DEEP ? 2.0f * (d[i] * (u[i] * (0.5f * f))) * s.t : d[i] * (u[i] * f);
     du[i] = d[i] * (g[i] * p);
-    if (DEEP) dg[i] *= s.t, du[i] *= s.t;
+    if (DEEP) du[i] *= s.t;
   }
 }
 
@@ -142,7 +155,7 @@ swiglu_backward_kernel(const uint16_t* __restrict__ dh, const uint8_t* __restric
   unpack8(as_vec(vd), d);
   swiglu_backward8<false>(g, u, d, dg, du);
   u32x4 og = pack8(dg), ou = pack8(du);
-  if (__builtin_expect(any_deep(vg), 0)) {
+  if (__builtin_expect(any_far<CE>(sg, su, vg), 0)) {
     swiglu_backward8<true>(g, u, d, dg, du);
     og = pack8(dg), ou = pack8(du);
   }

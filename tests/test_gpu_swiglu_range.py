@@ -78,19 +78,20 @@ def test_gates_whose_sigmoid_has_no_fp32_value():
     assert (off <= (2.0 ** -4 + 2.0 ** -7 + DEEP_EPS) * np.abs(h) + floor).all()
 
 
-def test_gradient_at_gates_whose_sigmoid_has_no_fp32_value():
+@pytest.mark.parametrize("elem", ["e4m3", "e5m2"])
+def test_gradient_at_gates_whose_sigmoid_has_no_fp32_value(elem):
     g, u = _deep_gates()
     x = np.concatenate([g, u], 1)
-    ck = P.quant_rows(x, "e4m3")
-    x = P.values(*ck, "e4m3")
+    ck = P.quant_rows(x, elem)
+    x = P.values(*ck, elem)
     # one half row has dh near 1, the other brings du into the normal range
     for dh in (np.ones_like(g), P.bf16_round(np.abs(u))):
         if dh[0, 0] != 1:
             x = x.copy()
             x[:, 32:] = P.bf16_round(np.sign(x[:, 32:]))
-            ck = P.quant_rows(x, "e4m3")
+            ck = P.quant_rows(x, elem)
         got = P.bf16_values(bits(mx.swiglu_backward(torch.from_numpy(dh).to(torch.bfloat16).cuda(),
-                                                    dev(ck[0]), dev(ck[1]))))
+                                                    dev(ck[0]), dev(ck[1]), elem)))
         ref = P.swiglu_backward(dh, x)
         p = P.sigmoid(x[:, :32])
         mag = np.concatenate([np.abs(dh * x[:, 32:]) * p * (1 + np.abs(x[:, :32])), np.abs(dh * x[:, :32]) * p], 1)
@@ -113,3 +114,19 @@ def test_closed_gates_of_any_size_give_zero():
     for d in (1.0, 3e38):
         dx = mx.swiglu_backward(torch.full((4, 32), d, dtype=torch.bfloat16, device="cuda"), *ck).float()
         assert (dx[finite] == 0).all()
+
+
+def test_gradient_where_up_values_near_the_end_meet_small_gradients():
+    """p (1 + g (1 - p)) passes 1 for gates above 1.28: times an up value near the
+    type's end it leaves FP32's range, the gradient's own value does not."""
+    rng = np.random.default_rng(5)
+    g = P.bf16_round(rng.uniform(1.5, 4.0, (8, 32)))
+    u = np.full((8, 32), 1.875 * 2.0 ** 127) * np.where(rng.random((8, 32)) < 0.5, -1, 1)
+    ck = P.quant_rows(np.concatenate([g, u], 1), "e4m3")
+    x = P.values(*ck, "e4m3")
+    assert (np.abs(x[:, 32:]) == 1.875 * 2.0 ** 127).all()
+    for scale in (1e-2, 1e-20, 0.9):
+        dh = P.bf16_round(scale * rng.uniform(0.5, 1.0, (8, 32)))
+        got = P.bf16_values(bits(mx.swiglu_backward(torch.from_numpy(dh).to(torch.bfloat16).cuda(), dev(ck[0]), dev(ck[1]))))
+        ref = P.swiglu_backward(dh, x)
+        assert (np.abs(got - ref) <= P.swiglu_backward_tolerance(dh, x)).all()
