@@ -74,3 +74,89 @@ def test_bad_offsets_count_as_their_running_maximum(T, G, N, K, elem):
         mx.grouped_gemm4(dev(off), a, sa, b, sb, elem, out=got)
         assert torch.equal(got.view(torch.int16), want.view(torch.int16)), trial
         assert (got[good[-1]:] == -3.0).all() and (got[:good[0]] == -3.0).all()
+
+
+ONE = {"e4m3": 0x38, "e5m2": 0x3C, "e2m1": 2}
+
+
+def _signs(shape, elem, rng):
+    """Codes of 1 and -1 with scales 1/4 to 4: (payload, scales, values).  A sum
+    of their products is a multiple of 1/16 below 2^20, exact in FP32 in any
+    order; eight neighbouring products have one scale, or two 2^8 apart at most,
+    and lose no bit to the matrix instruction's alignment."""
+    codes = np.where(rng.random(shape) < 0.5, ONE[elem] | (8 if elem == "e2m1" else 128), ONE[elem]).astype(np.uint8)
+    s = rng.integers(125, 130, shape[:-1] + (shape[-1] // 32,), dtype=np.uint8)
+    q = P.pack(codes) if elem == "e2m1" else codes
+    return q, s, P.values(q, s, elem)
+
+
+# one to 128 rows whose contraction is split: whole steps and not, whole dwords
+# of scales and not, columns of every remainder by four
+SPLIT = [(1, 8, 18432), (1, 33, 8224), (1, 512, 12288), (3, 7, 12320), (5, 40, 32768), (5, 130, 8192), (32, 34, 8288),
+         (32, 40, 8192), (40, 129, 8224), (64, 70, 18432), (64, 131, 8256), (100, 33, 8224), (128, 64, 4096),
+         (200, 66, 4128)]
+
+
+@pytest.mark.parametrize("M,N,K", SPLIT)
+@pytest.mark.parametrize("elem", ELEMS)
+def test_split_contraction_is_exact(M, N, K, elem):
+    """Sums of signed powers of two, in which no step of 128 elements can be lost
+    or counted twice without a result that differs."""
+    assert mx.mx_gemm4_workspace_size(mx.OPERAND_ELEMS[elem], M, N, K) > 0
+    rng = np.random.default_rng(M + N + K)
+    a, sa, x = _signs((M, K), elem, rng)
+    b, sb, y = _signs((N, K), "e2m1", rng)
+    ref = x @ y.T
+    want = P.bf16_round(ref)
+    for k in range(0, K, 128):
+        part = x[:, k:k + 128] @ y[:, k:k + 128].T
+        assert (P.bf16_round(ref - part) != want).any() and (P.bf16_round(ref + part) != want).any()
+    got = mx.gemm4(dev(a), dev(sa), dev(b), dev(sb), elem).double().cpu().numpy()
+    np.testing.assert_array_equal(got, want)
+
+
+@pytest.mark.parametrize("M", [1, 32, 64, 128])
+@pytest.mark.parametrize("K", [8192, 8224])
+@pytest.mark.parametrize("elem", ELEMS)
+def test_split_contraction_takes_every_step_once(M, K, elem):
+    """One code 1 a row, beside every edge of a step: the weight's column."""
+    N = 33
+    assert mx.mx_gemm4_workspace_size(mx.OPERAND_ELEMS[elem], M, N, K) > 0
+    b, sb = _operand((N, K), "e2m1", 5)
+    w = P.values(b, sb, "e2m1")
+    at = np.unique(np.clip(np.concatenate([np.arange(0, K + 1, 256) + d for d in (-1, 0)]), 0, K - 1))
+    if M == 1:
+        at = at[::7]
+    for first in range(0, len(at), M):
+        rows = at[first:first + M]
+        codes = np.zeros((M, K), np.uint8)
+        codes[np.arange(len(rows)), rows] = ONE[elem]
+        a = P.pack(codes) if elem == "e2m1" else codes
+        sa = np.full((M, K // 32), 127, np.uint8)
+        got = mx.gemm4(dev(a), dev(sa), dev(b), dev(sb), elem).double().cpu().numpy()
+        np.testing.assert_array_equal(got[:len(rows)], w[:, rows].T)
+
+
+@pytest.mark.parametrize("elem", ELEMS)
+@pytest.mark.parametrize("M,N,K", [(3304, 3304, 2560), (3301, 3303, 2080)])
+def test_large_tiles_over_many_scale_groups(M, N, K, elem):
+    """More K than two buffers of scales hold, each block with scales of its own."""
+    rng = np.random.default_rng(K)
+    a, sa, x = _signs((M, K), elem, rng)
+    b, sb, y = _signs((N, K), "e2m1", rng)
+    got = mx.gemm4(dev(a), dev(sa), dev(b), dev(sb), elem).double().cpu().numpy()
+    np.testing.assert_array_equal(got, P.bf16_round(x @ y.T))
+
+
+@pytest.mark.parametrize("elem", ELEMS)
+@pytest.mark.parametrize("N,K", [(2600, 2560), (2603, 2080)])
+def test_grouped_large_tiles_over_many_scale_groups(N, K, elem):
+    rng = np.random.default_rng(K)
+    sizes = rng.integers(200, 700, 12)
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int64)
+    a, sa, x = _signs((int(off[-1]), K), elem, rng)
+    b, sb, y = _signs((12, N, K), "e2m1", rng)
+    got = mx.grouped_gemm4(dev(off), dev(a), dev(sa), dev(b), dev(sb), elem).double().cpu().numpy()
+    for g in range(12):
+        r = slice(off[g], off[g + 1])
+        np.testing.assert_array_equal(got[r], P.bf16_round(x[r] @ y[g].T))
