@@ -164,7 +164,9 @@ bool is_elem(mx_elem_type e) { return is_fp8(e) || e == MX_ELEM_E2M1; }
 // The kernels for 4-bit weights and checkpoints move 16 bytes at a time.
 bool misaligned(const void* p) { return ((uintptr_t)p & 15) != 0; }
 
-constexpr int64_t GEMM4_N_LIMIT = int64_t(1) << 28;   // 32-column tiles of 512 threads in one grid
+// A launch with few rows has 256 threads for every 128 columns, 2 N work-items in
+// its grid, and the join of split sums numbers columns in 32 bits.
+constexpr int64_t GEMM4_N_LIMIT = int64_t(1) << 28;
 constexpr int64_t SWIGLU_F_LIMIT = int64_t(1) << 33;  // eight-column chunks of a row in 32 bits
 
 // What the dense and the grouped product with a 4-bit weight share (M rows in

@@ -519,13 +519,13 @@ static bool whole_scales(const void* sa, const void* sb) {
   return (((uintptr_t)sa | (uintptr_t)sb) & 15) == 0;
 }
 
-// Large tiles where they are done first: a round of them, a tile on each
-// compute unit, takes 1.5 to 2 times as long as a round of the small ones with
-// half their columns (us, large against small, rounds in brackets, 8-bit A.
+// Large tiles where they are done first: a round of them, a tile on each of 256
+// compute units, takes 1.5 to 2 times as long as a round of the small ones with
+// half their rows (us, large against small, rounds in brackets, 8-bit A.
 // Whole: 2048 x 7168 x 18432 240 (1) and 318 (2), 4096 x 4352 x 4096 91 (2) and
 // 103 (3), 1024 x 7168 x 18432 203 (1) and 136 (1).  Otherwise: 2048 x 7168 x
 // 18400 380 (1) and 391 (2), 8192 x 8192 x 2880 196 (4) and 268 (8), 4096 x 4130
-// x 2080 79 (2) and 64 (3), 2048 x 18432 x 544 50 (3) and 44 (5)).  Up to 128 rows half a large tile would be empty, and the rounds are
+// x 2080 79 (2) and 68 (3), 2048 x 18432 x 544 50 (3) and 44 (5)).  Up to 128 rows half a large tile would be empty, and the rounds are
 // as many.  K from 128 on: a row has a whole dword of scales.
 static bool many(int64_t M, int64_t N, int64_t K) {
   const int64_t large = ((M + BM - 1) / BM) * ((N + BN - 1) / BN);

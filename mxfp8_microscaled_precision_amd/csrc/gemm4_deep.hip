@@ -20,7 +20,9 @@ namespace mx {
 // (128 with 4-bit A) and the step's scale words, a dword of four scale bytes a
 // row and 128 elements: A's rows, padded to whole waves, then B's.  Chunk
 // swizzles and the meeting of blocks are those of gemm4.hip, panel by panel.
-// TWO: stages for two workgroups on a compute unit.
+// TWO: stages for two workgroups on a compute unit.  Stages, with an 8-bit A and
+// a 4-bit one: 3 and 3 for 32 rows, 4 and 6 for 64, 3 and 4 for 128, 4 and 3 for
+// 128 x 256, 3 and 4 for 128 rows of a group.
 template <int FA, int WM, int WN, int FM, int FN, int KH_, bool TWO>
 struct Deep4 {
   static constexpr bool A4 = FA == ELEM_E2M1;
@@ -40,8 +42,7 @@ struct Deep4 {
   static_assert(A_OPS * 1024 * WAVES == A_BYTES && B_OPS * 1024 * WAVES == B_BYTES, "whole loads");
   static constexpr int S_BYTES = 256 * WAVES;           // one array of scale words
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + KH * S_BYTES;
-  static constexpr int FIT = (TWO ? 81920 : 163840) / STAGE_BYTES;
-  static constexpr int NS = FIT > 8 ? 8 : FIT;
+  static constexpr int NS = (TWO ? 81920 : 163840) / STAGE_BYTES;  // 3 to 6
   static_assert(NS >= 2 && (NS - 1) * OPS < 64, "vmcnt holds 6 bits");
 
   const uint8_t* __restrict__ a;
@@ -497,7 +498,8 @@ grouped4_deep_kernel(const int64_t* __restrict__ offsets, int64_t G, int64_t row
 // against 361).  K is split so far as workgroups still find a unit each and the
 // steps saved outweigh the second launch and the partial sums' way through
 // memory (1 x 7168 x 18432: 15.3 in four, 31 whole; 1 x 4096 x 4096: 9.8 whole,
-// 12.4 in four).
+// 12.4 in four).  Sizes alone decide, as they do on the workspace's bytes, for the
+// 256 units of the card; on fewer the same workgroups run in more rounds.
 enum Shape4 { TILE_32, TILE_64, TILE_128, TILE_WIDE };
 
 struct Plan4 {
