@@ -476,7 +476,8 @@ mx_status mx_dequant(mx_elem_type elem, const void* q, const void* s, int64_t ro
  * backward one its column blocks.  Requires K % 32 == 0, K < 2^23, N < 2^28.
  * K == 0 writes zeros; M == 0 or N == 0 is a no-op.
  *   workspace: DEVICE scratch of at least mx_gemm4_workspace_size bytes, 16-byte
- *   aligned, for sums of a split contraction (NULL where that size is 0);
+ *   aligned and apart from c and the operands (MX_ERR_INVALID_ARG), for sums of a
+ *   split contraction (NULL where that size is 0);
  *   written and read by the call's own kernels only, so calls on one stream
  *   may share it, calls that may run at the same time not. */
 mx_status mx_gemm4(mx_elem_type a_elem, int64_t M, int64_t N, int64_t K, const void* a,

@@ -893,6 +893,14 @@ mx_status mx_gemm4(mx_elem_type a_elem, int64_t M, int64_t N, int64_t K, const v
   if (workspace_bytes < need || (need > 0 && !workspace))
     return fail(MX_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
   if (misaligned(workspace)) return fail(MX_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+  if (need > 0) {
+    const int64_t bytes = (int64_t)need;
+    if (share_memory(workspace, bytes, c, 2 * M * N) ||
+        share_memory(workspace, bytes, a, a_elem == MX_ELEM_E2M1 ? M * K / 2 : M * K) ||
+        share_memory(workspace, bytes, sa, M * (K / 32)) || share_memory(workspace, bytes, b, N * (K / 2)) ||
+        share_memory(workspace, bytes, sb, N * (K / 32)))
+      return fail(MX_ERR_INVALID_ARG, "workspace shares memory with the result or an operand");
+  }
   int dev;
   st = current_device(&dev);
   if (st != MX_OK) return st;
