@@ -160,3 +160,37 @@ def test_grouped_large_tiles_over_many_scale_groups(N, K, elem):
     for g in range(12):
         r = slice(off[g], off[g + 1])
         np.testing.assert_array_equal(got[r], P.bf16_round(x[r] @ y[g].T))
+
+
+@pytest.mark.parametrize("elem", ["e4m3", "e2m1"])
+@pytest.mark.parametrize("T,G,N,K", [(40, 5, 140, 288), (1500, 70, 140, 288), (6000, 9, 2600, 512)])
+def test_grouped_graph_reads_the_offsets_of_each_replay(T, G, N, K, elem):
+    rng = np.random.default_rng(T)
+    a, sa = (dev(t) for t in _signs((T, K), elem, rng)[:2])
+    b, sb = (dev(t) for t in _signs((G, N, K), "e2m1", rng)[:2])
+    off = torch.zeros(G + 1, dtype=torch.int64, device="cuda")
+    out = torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    mx.grouped_gemm4(off, a, sa, b, sb, elem, out=out)
+    with torch.cuda.graph(graph):
+        mx.grouped_gemm4(off, a, sa, b, sb, elem, out=out)
+    for top in (T, T // 2, 0, T):
+        off.copy_(dev(np.sort(rng.integers(0, top + 1, G + 1))))
+        out.fill_(-3.0)
+        graph.replay()
+        want = torch.full_like(out, -3.0)
+        mx.grouped_gemm4(off, a, sa, b, sb, elem, out=want)
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+        for g in range(G):
+            r = slice(int(off[g]), int(off[g + 1]))
+            assert torch.equal(out[r], mx.gemm4(a[r], sa[r], b[g], sb[g], elem))     # exact in any order
+        assert (out[int(off[G]):] == -3.0).all() and (out[:int(off[0])] == -3.0).all()
+
+
+def test_grouped_without_a_contraction_writes_zeros():
+    u8 = dict(dtype=torch.uint8, device="cuda")
+    off = dev(np.array([1, 3, 3, 6], np.int64))
+    out = torch.full((8, 40), -3.0, dtype=torch.bfloat16, device="cuda")
+    mx.grouped_gemm4(off, torch.empty((8, 0), **u8), torch.empty((8, 0), **u8), torch.empty((3, 40, 0), **u8),
+                     torch.empty((3, 40, 0), **u8), out=out)
+    assert not out[1:6].any() and (out[0] == -3.0).all() and (out[6:] == -3.0).all()
