@@ -497,8 +497,8 @@ grouped4_deep_kernel(const int64_t* __restrict__ offsets, int64_t G, int64_t row
 // x 18432: 70, against 117 with 128 x 256), 128 x 256 beyond (2048 rows: 318
 // against 361).  K is split so far as workgroups still find a unit each and the
 // steps saved outweigh the second launch and the partial sums' way through
-// memory (1 x 7168 x 18432: 15.3 in four, 31 whole; 1 x 4096 x 4096: 9.8 whole,
-// 12.4 in four).  Sizes alone decide, as they do on the workspace's bytes, for the
+// memory (1 x 7168 x 18432: 15.3 in four, 31 whole; 1 x 4096 x 4096: 8.2 to 9.8
+// whole, 12.4 in four).  Sizes alone decide, as they do on the workspace's bytes, for the
 // 256 units of the card; on fewer the same workgroups run in more rounds.
 enum Shape4 { TILE_32, TILE_64, TILE_128, TILE_WIDE };
 

@@ -11,8 +11,8 @@
 // The kernels are bound by HBM.  A lane takes eight columns: 16 bytes of the
 // gates and 16 of the up values, four lanes to a block of 32, so that a block's
 // maximum needs two lane exchanges and all eight waves fit a SIMD (25 to 36
-// registers).  Measured at 131072 x 2048 (E4M3): forward 217 us without the
-// checkpoint (6.2 TB/s) and 328 with it (5.8); backward 346 us to BF16 (6.3) and
+// registers).  Measured at 131072 x 2048 (E4M3): forward 223 us without the
+// checkpoint (6.1 TB/s) and 328 with it (5.8); backward 346 us to BF16 (6.3) and
 // 313 quantised (5.3).  One token of 18432: 8.8 us, the host's calls.
 #include "mx_columns.h"
 #include "mx_device.h"
