@@ -88,7 +88,11 @@ __device__ __forceinline__ void swiglu_backward8(const float g[8], const float u
     // p (1 + g (1 - p)) lies in -0.1 .. 1.1 and |g p| <= |g|, whatever finite g is
     // (below DEEP_GATE p is 2^-115, and 1 - p as good as 1 - p t)
     const float f = p * (1.0f + g[i] * (1.0f - p));
-    dg[i] = DEEP ? 2.0f * (d[i] * (u[i] * (0.5f * f))) * s.t : d[i] * (u[i] * f);
+    // half of it for an up value of 2^127 or more (of these only: what is below
+    // FP32's normal values would lose a bit, and a row's bits follow its neighbours)
+    const bool end = DEEP && fabsf(u[i]) >= 0x1p127f;
+    dg[i] = d[i] * (u[i] * (end ? 0.5f * f : f));
+    if (DEEP) dg[i] *= end ? 2.0f * s.t : s.t;
     du[i] = d[i] * (g[i] * p);
     if (DEEP) du[i] *= s.t;
   }

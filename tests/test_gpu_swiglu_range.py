@@ -130,3 +130,25 @@ def test_gradient_where_up_values_near_the_end_meet_small_gradients():
         got = P.bf16_values(bits(mx.swiglu_backward(torch.from_numpy(dh).to(torch.bfloat16).cuda(), dev(ck[0]), dev(ck[1]))))
         ref = P.swiglu_backward(dh, x)
         assert (np.abs(got - ref) <= P.swiglu_backward_tolerance(dh, x)).all()
+
+
+@pytest.mark.parametrize("elem", ["e4m3", "e5m2"])
+def test_rows_do_not_depend_on_far_neighbours(elem):
+    """A wave with gates below -80 or up values near 2^128 takes another form: its
+    other rows have the bits that they have alone, products below FP32's normal
+    range among them."""
+    rng = np.random.default_rng(9)
+    T, F = 512, 32
+    g = rng.uniform(-70, 70, (T, F))
+    u = rng.uniform(1, 2, (T, F)) * np.ldexp(1.0, rng.integers(-126, 126, (T, 1)))
+    dh = rng.uniform(1, 2, (T, F)) * np.ldexp(1.0, rng.integers(-126, 126, (T, 1)))
+    x = torch.from_numpy(np.concatenate([g, u], 1)).to(torch.bfloat16).cuda()
+    dh = torch.from_numpy(dh).to(torch.bfloat16).cuda()
+    far = torch.full((T, 2 * F), -96.0, dtype=torch.bfloat16, device="cuda")
+    far[::2] = 3.3e38
+    both = torch.stack([x, far], 1).view(2 * T, 2 * F)
+    d2 = torch.stack([dh, dh], 1).view(2 * T, F)
+    one, two = mx.swiglu_quant(x, checkpoint_elem=elem), mx.swiglu_quant(both, checkpoint_elem=elem)
+    assert torch.equal(one[0], two[0][::2]) and torch.equal(one[1], two[1][::2])
+    a, b = mx.swiglu_backward(dh, *one[2], elem), mx.swiglu_backward(d2, *two[2], elem)
+    assert torch.equal(a.view(torch.int16), b[::2].contiguous().view(torch.int16))
